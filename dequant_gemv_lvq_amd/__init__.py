@@ -21,6 +21,12 @@ STREAM_GEOM_SINK_WORDS = 65536
 MAX_FUSED = 4
 MAX_BATCH = 4
 
+LVQ_F32 = 0
+LVQ_F16 = 1
+LVQ_BF16 = 2
+LVQ_I8 = 3
+LVQ_E4M3 = 4
+
 LVQ_OK = 0
 LVQ_E_NULL = -1
 LVQ_E_SHAPE = -2
@@ -52,7 +58,7 @@ def _load():
         raise ImportError("liblvq.so is not built (%s); run python dequant_gemv_lvq_amd/build.py"
                           % LIB_PATH)
     lib = ctypes.CDLL(LIB_PATH)
-    vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    vp, i, sz, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
     sig = {
         "lvq_strerror": (ctypes.c_char_p, [i]),
         "lvq_last_error_index": (i, [ctypes.POINTER(i), ctypes.POINTER(i)]),
@@ -83,6 +89,11 @@ def _load():
         "bpdq_gemv": (i, [vp, vp, i, i, vp, vp, i, vp]),
         "trellis_gemv": (i, [vp, vp, vp, i, i, vp, vp, i, vp]),
         "fp16_gemv": (i, [vp, i, i, vp, vp, i, vp]),
+        "q4_gemv": (i, [vp, vp, vp, i, i, i, vp, vp, i, vp]),
+        "q4_gemv_q8": (i, [vp, vp, vp, i, i, i, vp, i, vp, i, vp, i, vp]),
+        "lvq_rms_norm": (i, [vp, i, i64, vp, i, vp, vp, i, ctypes.c_float, i, i, vp, i, vp, i,
+                             vp]),
+        "lvq_silu_mul": (i, [vp, vp, i, i64, i, i, vp, i, vp, i, vp]),
         "lvq_rotate": (i, [vp, vp, vp, i, i, vp, i, vp]),
         "lvq_gemv_rotated": (i, [vp, i, i, vp, vp, i, vp, vp, i, vp]),
         "lvq_stream_read": (i, [vp, sz, vp, vp]),
@@ -104,7 +115,8 @@ EXPORTED = ("lvq_strerror", "lvq_last_error_index", "lvq_class_table", "lvq_layo
             "lvq_layout_bytes_onehot", "lvq_expand_onehot", "lvq_gemv_onehot",
             "lvq_rank", "lvq_gemv", "lvq_gemv_gain",
             "lvq_unfold", "lvq_gemv_fused", "lvq_gemv_noweights", "lvq_decode",
-            "bpdq_gemv", "trellis_gemv", "fp16_gemv", "lvq_rotate", "lvq_gemv_rotated",
+            "bpdq_gemv", "trellis_gemv", "fp16_gemv", "q4_gemv", "q4_gemv_q8",
+            "lvq_rms_norm", "lvq_silu_mul", "lvq_rotate", "lvq_gemv_rotated",
             "lvq_stream_read", "lvq_stream_read_geom", "lvq_gemv_launch_info")
 
 
@@ -367,6 +379,145 @@ def trellis_gemv(bits, table, scale, rows: int, cols: int, x, y, batch: int = 1,
 def fp16_gemv(w, rows: int, cols: int, x, y, batch: int = 1, stream=None):
     _check(_lib.fp16_gemv(_ptr(w), int(rows), int(cols), _ptr(x), _ptr(y), int(batch),
                           _stream(stream)))
+
+
+try:
+    import torch as _torch
+    _TYPES = {_torch.float32: LVQ_F32, _torch.float16: LVQ_F16, _torch.bfloat16: LVQ_BF16,
+              _torch.int8: LVQ_I8, _torch.float8_e4m3fn: LVQ_E4M3}
+    # fp16 bit patterns are also accepted as 16-bit integers, codes as any bytes
+    _F16_BITS = (_torch.float16, _torch.int16, getattr(_torch, "uint16", None))
+    _BYTES = (_torch.uint8, _torch.int8, _torch.int32, getattr(_torch, "uint32", None))
+    _F32 = (_torch.float32,)
+    _FLOATS = (_torch.float32, _torch.float16, _torch.bfloat16)
+    _EIGHT = (_torch.int8, _torch.float8_e4m3fn)
+    _OUTS = (_torch.float16,) + _EIGHT
+except ImportError:  # raw addresses only
+    _torch = None
+    _TYPES = {}
+    _F16_BITS = _BYTES = _F32 = _FLOATS = _EIGHT = _OUTS = ()
+
+
+def _tensor(t, name, types):
+    """Address of a torch tensor on the current device, of one of `types`."""
+    if not hasattr(t, "data_ptr"):
+        raise TypeError("%s must be a tensor on the GPU" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be on the GPU" % name)
+    if t.get_device() != _torch.cuda.current_device():
+        raise ValueError("%s is on another device than the current one" % name)
+    if t.dtype not in types:
+        raise ValueError("%s has type %s" % (name, t.dtype))
+    return t.data_ptr()
+
+
+def _array(t, name, types, nbytes: int):
+    """Address of a contiguous tensor of at least nbytes bytes (checked, so that
+    the kernel never reads or writes past it), of an int (a raw address, not
+    checked) or of None."""
+    if t is None or isinstance(t, int):
+        return t
+    p = _tensor(t, name, types)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.numel() * t.element_size() < nbytes:
+        raise LvqError(LVQ_E_SHAPE, "%s: %s holds %d of %d bytes" % (
+            strerror(LVQ_E_SHAPE), name, t.numel() * t.element_size(), nbytes))
+    return p
+
+
+def _n_groups(cols: int, group: int) -> int:
+    return -(-cols // group) if group > 0 else 1
+
+
+def q4_gemv(codes, scale, zero, group: int, rows: int, cols: int, x, y, batch: int = 1,
+            stream=None):
+    """y = W x, W 4-bit codes with a scale (and a zero, or None for 8) per group
+    of columns (32, 64, 128, 256, or 0: one per row); x fp16, y fp32."""
+    group, rows, cols, batch = int(group), int(rows), int(cols), int(batch)
+    meta = rows * _n_groups(cols, group) * 2
+    _check(_lib.q4_gemv(_array(codes, "codes", _BYTES, rows * (-(-cols // 32) * 16)),
+                        _array(scale, "scale", _F16_BITS, meta),
+                        _array(zero, "zero", _F16_BITS, meta), group, rows, cols,
+                        _array(x, "x", _F16_BITS, batch * cols * 2),
+                        _array(y, "y", _F32, batch * rows * 4), batch, _stream(stream)))
+
+
+def q4_gemv_q8(codes, scale, zero, group: int, rows: int, cols: int, x, x_scale, x_group: int, y,
+               batch: int = 1, stream=None):
+    """q4_gemv with x in 8 bits (an int8 or float8_e4m3fn tensor) and its fp32
+    scales, one per x_group columns of a batch row (0: one per batch row)."""
+    group, rows, cols, batch = int(group), int(rows), int(cols), int(batch)
+    x_group = int(x_group)
+    meta = rows * _n_groups(cols, group) * 2
+    _tensor(x, "x", _EIGHT)  # its type says how to read it: no raw address
+    _check(_lib.q4_gemv_q8(_array(codes, "codes", _BYTES, rows * (-(-cols // 32) * 16)),
+                           _array(scale, "scale", _F16_BITS, meta),
+                           _array(zero, "zero", _F16_BITS, meta), group, rows, cols,
+                           _array(x, "x", _EIGHT, batch * cols), _TYPES[x.dtype],
+                           _array(x_scale, "x_scale", _F32, batch * _n_groups(cols, x_group) * 4),
+                           x_group, _array(y, "y", _F32, batch * rows * 4), batch,
+                           _stream(stream)))
+
+
+def _rows_of(t, name):
+    """(address, type, rows, cols, row stride) of a 2-D tensor of floats whose
+    columns are adjacent."""
+    p = _tensor(t, name, _FLOATS)
+    if t.dim() != 2:
+        raise ValueError("%s must have two dimensions, rows and columns" % name)
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have adjacent columns" % name)
+    return p, _TYPES[t.dtype], rows, cols, t.stride(0) if rows > 1 else cols
+
+
+def _out_of(out, scale, group, rows, cols):
+    op = _tensor(out, "out", _OUTS)
+    _array(out, "out", _OUTS, rows * cols * out.element_size())
+    return op, _TYPES[out.dtype], _array(scale, "scale", _F32,
+                                         rows * _n_groups(cols, group) * 4)
+
+
+def rms_norm(x, residual, weight, eps: float, out, residual_out=None, scale=None, group: int = 0,
+             stream=None):
+    """out = h * rsqrt(mean(h^2) + eps) * weight over the columns of h = x +
+    residual, and residual_out = h.  x is a 2-D tensor (rows may be strided) of
+    fp32, fp16 or bf16; residual and residual_out (which may be the same tensor)
+    are contiguous and of one such type, weight of any; residual, weight and
+    residual_out may be None.  out: fp16, or int8 / float8_e4m3fn with scale, one
+    fp32 per `group` columns of a row (32, 64, 128, 256, or 0: one per row)."""
+    group = int(group)
+    xp, xt, rows, cols, stride = _rows_of(x, "x")
+    rt = LVQ_F32
+    for t in (residual, residual_out):
+        if t is not None:
+            _array(t, "residual", _FLOATS, rows * cols * t.element_size())
+            rt = _TYPES[t.dtype]
+    if residual is not None and residual_out is not None and residual.dtype != residual_out.dtype:
+        raise ValueError("residual and residual_out must have the same type")
+    wp = wt = 0
+    if weight is not None:
+        wp = _array(weight, "weight", _FLOATS, cols * weight.element_size())
+        wt = _TYPES[weight.dtype]
+    op, ot, sp = _out_of(out, scale, group, rows, cols)
+    _check(_lib.lvq_rms_norm(xp, xt, stride, None if residual is None else residual.data_ptr(), rt,
+                             None if residual_out is None else residual_out.data_ptr(), wp or None,
+                             wt, float(eps), rows, cols, op, ot, sp, group, _stream(stream)))
+
+
+def silu_mul(gate, up, out, scale=None, group: int = 0, stream=None):
+    """out = gate / (1 + exp(-gate)) * up.  gate and up: 2-D tensors of one type
+    (fp32, fp16 or bf16), shape and row stride (for instance the halves of one
+    product's output); out, scale and group as in rms_norm()."""
+    group = int(group)
+    gp, gt, rows, cols, stride = _rows_of(gate, "gate")
+    up_p, ut, urows, ucols, ustride = _rows_of(up, "up")
+    if (ut, urows, ucols, ustride) != (gt, rows, cols, stride):
+        raise ValueError("gate and up must have the same type, shape and row stride")
+    op, ot, sp = _out_of(out, scale, group, rows, cols)
+    _check(_lib.lvq_silu_mul(gp, up_p, gt, stride, rows, cols, op, ot, sp, group,
+                             _stream(stream)))
 
 
 def rotate(x, n: int, m: int, sign_words, q, y, batch: int = 1, stream=None):

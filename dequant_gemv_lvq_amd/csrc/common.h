@@ -18,6 +18,12 @@ constexpr int kWave = 64;
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
+// Whether two byte ranges share a byte (a NULL or empty range shares none).
+inline bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
+  return a && b && na && nb && pa < pb + nb && pb < pa + na;
+}
+
 inline int check_batch(int batch) {
   return (batch < 1 || batch > LVQ_MAX_BATCH) ? LVQ_E_BATCH : LVQ_OK;
 }

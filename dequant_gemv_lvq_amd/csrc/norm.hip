@@ -1,0 +1,617 @@
+// The transforms between two projections of a decoder block: the
+// root-mean-square norm of a residual stream (lvq_rms_norm) and the gated
+// activation (lvq_silu_mul), with fp16 or 8-bit outputs.
+//
+//   rms_norm   h = x + residual, out = h (mean h^2 + eps)^-1/2 w
+//   silu_mul   out = g / (1 + e^-g) u
+//   8 bits     a = max |out| over a group, scale = a / M, code = rne(out M / a)
+//
+// Both are streams: a few operations per value, so the bytes and, for the few
+// rows of a decode step, the launch and one round of memory latency bound
+// them.  A thread owns chunks of 8 consecutive columns (16 bytes of fp16, 32 of
+// fp32): every array is read once into registers, the statistics are taken
+// there, and every output is written once.  A group of 32..256 columns is then
+// 4..32 neighbouring lanes of one wave, so its largest magnitude needs no LDS.
+// Magnitudes are compared as the bits of |v|: unsigned order is the order of
+// the values, with infinity above every finite value and NaN above infinity,
+// so a NaN is not lost as it is by a floating maximum.
+
+#include "common.h"
+
+namespace lvq {
+
+constexpr int kChunk = 8;          // columns a thread owns at a time
+constexpr int kNone = 3;           // "no residual" beside LVQ_F32, LVQ_F16, LVQ_BF16
+constexpr int kMaxCols = 65536;     // of any row
+constexpr int kMaxRowCols = 32768;  // of a row that one workgroup holds in registers
+constexpr int kRowThreads = 1024;
+
+// ---------------------------------------------------------------- loads and stores
+
+__device__ __forceinline__ float half_bits(uint32_t b) {
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)b);
+}
+__device__ __forceinline__ float bf16_bits(uint32_t b) {
+  return __builtin_bit_cast(float, b << 16);
+}
+__device__ __forceinline__ uint32_t to_half_bits(float f) {
+  return __builtin_bit_cast(uint16_t, (_Float16)f);
+}
+__device__ __forceinline__ uint32_t to_bf16_bits(float f) {
+  return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+
+template <int T>
+struct Chunk {  // 8 values as they lie in memory
+  uint4 q[T == LVQ_F32 ? 2 : 1];
+};
+
+// The column index through an empty statement, so that what the rare chunk at
+// a row's end compares is formed there and not held in registers from the start.
+__device__ __forceinline__ int opaque(int c) {
+  asm volatile("" : "+v"(c));
+  return c;
+}
+
+// Columns c..c+7 of a row; columns past cols read as 0.  A whole chunk is read
+// 16 bytes at a time whatever its alignment (global memory takes any); the
+// chunk that cols cuts reads its values one by one, the missing ones as copies
+// of the last, so there is no branch per value.
+template <int T>
+__device__ __forceinline__ Chunk<T> load_chunk(const void* row, int c, int cols) {
+  constexpr int E = T == LVQ_F32 ? 4 : 2;
+  Chunk<T> r;
+  if (c + kChunk <= cols) {
+    __builtin_memcpy(&r, (const uint8_t*)row + (size_t)c * E, sizeof(r));
+    return r;
+  }
+  uint32_t w[T == LVQ_F32 ? 8 : 4];
+#pragma unroll
+  for (int i = 0; i < (T == LVQ_F32 ? 8 : 4); ++i) w[i] = 0;
+  if (c < cols) {
+    c = opaque(c);
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      const int at = c + i < cols ? c + i : cols - 1;
+      uint32_t v = T == LVQ_F32 ? ((const uint32_t*)row)[at] : ((const uint16_t*)row)[at];
+      v = c + i < cols ? v : 0u;
+      if constexpr (T == LVQ_F32) w[i] = v;
+      else w[i >> 1] |= v << (16 * (i & 1));
+    }
+  }
+  r.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  if constexpr (T == LVQ_F32) r.q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  return r;
+}
+
+template <int T>
+__device__ __forceinline__ void unpack(const Chunk<T>& r, float (&v)[kChunk]) {
+#pragma unroll
+  for (int h = 0; h < (T == LVQ_F32 ? 2 : 1); ++h) {
+    const uint32_t w[4] = {r.q[h].x, r.q[h].y, r.q[h].z, r.q[h].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (T == LVQ_F32) {
+        v[4 * h + i] = __builtin_bit_cast(float, w[i]);
+      } else if constexpr (T == LVQ_F16) {
+        v[2 * i] = half_bits(w[i] & 0xFFFFu);
+        v[2 * i + 1] = half_bits(w[i] >> 16);
+      } else {
+        v[2 * i] = bf16_bits(w[i] & 0xFFFFu);
+        v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
+// Columns c..c+7 (c < cols) of a row of `type` (fp32, fp16 or bf16) from fp32,
+// rounded once to the nearest even.
+__device__ __forceinline__ void store_chunk(void* row, int type, int c, int cols,
+                                            const float (&v)[kChunk]) {
+  if (type == LVQ_F32) {
+    float* p = (float*)row + c;
+    if (c + kChunk <= cols) {
+      __builtin_memcpy(p, v, sizeof(v));
+    } else {
+      c = opaque(c);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (c + i < cols) p[i] = v[i];
+    }
+    return;
+  }
+  uint32_t b[4];
+  if (type == LVQ_F16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = to_half_bits(v[2 * i]) | to_half_bits(v[2 * i + 1]) << 16;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = to_bf16_bits(v[2 * i]) | to_bf16_bits(v[2 * i + 1]) << 16;
+  }
+  uint16_t* p = (uint16_t*)row + c;
+  if (c + kChunk <= cols) {
+    __builtin_memcpy(p, b, sizeof(b));
+  } else {
+    c = opaque(c);
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i)
+      if (c + i < cols) p[i] = (uint16_t)(b[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+// ---------------------------------------------------------------- maxima
+
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  // max of v and the value DPP routes to this lane (0 where the row is masked)
+  const uint32_t m =
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW_MASK, 0xF, false);
+  return v > m ? v : m;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = dpp_max<0xB1, 0xF>(v);   // the pairing of wave_sum_lane63
+  v = dpp_max<0x4E, 0xF>(v);
+  v = dpp_max<0x141, 0xF>(v);
+  v = dpp_max<0x140, 0xF>(v);
+  v = dpp_max<0x142, 0xA>(v);
+  v = dpp_max<0x143, 0xC>(v);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
+}
+
+// Maximum over the aligned group of `lanes` (4, 8, 16 or 32) lanes.
+__device__ __forceinline__ uint32_t group_max(uint32_t v, int lanes) {
+  v = dpp_max<0xB1, 0xF>(v);
+  v = dpp_max<0x4E, 0xF>(v);
+  if (lanes >= 8) v = dpp_max<0x141, 0xF>(v);
+  if (lanes >= 16) v = dpp_max<0x140, 0xF>(v);
+  if (lanes >= 32) {
+    const uint32_t m = (uint32_t)__shfl_xor((int)v, 16, kWave);
+    v = v > m ? v : m;
+  }
+  return v;
+}
+
+// ---------------------------------------------------------------- outputs
+
+struct Out {
+  void* out;
+  float* scale;
+  int type, group, groups, cols;
+};
+
+// Writes a row's results o[k] (columns 8 (t + k n) .. + 7 belong to thread t of
+// the n that share the row).  WAVE: those threads are lanes of one wave.  red:
+// LDS words, one per wave of the workgroup, not in use by any thread.
+template <int NV, bool WAVE>
+__device__ __forceinline__ void emit(const Out& a, size_t row, const float (&o)[NV][kChunk], int t,
+                                     int n, uint32_t* red) {
+  if (a.type == LVQ_F16) {
+    uint16_t* p = (uint16_t*)a.out + row * a.cols;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (t + k * n) * kChunk;
+      if (c < a.cols) store_chunk(p, LVQ_F16, c, a.cols, o[k]);
+    }
+    return;
+  }
+  uint32_t top[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    top[k] = 0;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      const uint32_t b = __builtin_bit_cast(uint32_t, o[k][i]) & 0x7FFFFFFFu;
+      top[k] = top[k] > b ? top[k] : b;
+    }
+  }
+  if (a.group == 0) {
+    uint32_t m = top[0];
+#pragma unroll
+    for (int k = 1; k < NV; ++k) m = m > top[k] ? m : top[k];
+    m = wave_max(m);
+    if constexpr (!WAVE) {
+      if ((t & (kWave - 1)) == 0) red[t / kWave] = m;
+      __syncthreads();
+      m = red[0];
+      for (int w = 1; w < n / kWave; ++w) m = m > red[w] ? m : red[w];
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) top[k] = m;
+  } else {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) top[k] = group_max(top[k], a.group / kChunk);
+  }
+  const float most = a.type == LVQ_I8 ? 127.f : 448.f;
+  uint8_t* p = (uint8_t*)a.out + row * a.cols;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = (t + k * n) * kChunk;
+    if (c >= a.cols) continue;
+    const float m = __builtin_bit_cast(float, top[k]);
+    // below 2^-100 the reciprocal leaves the fp32 range; NaN compares false
+    const bool ok = top[k] < 0x7F800000u && m >= 0x1p-100f;
+    const float inv = ok ? most / m : 0.f;
+    if (a.group == 0 ? c == 0 : (c & (a.group - 1)) == 0)
+      a.scale[row * a.groups + (a.group == 0 ? 0 : c / a.group)] =
+          ok ? m / most : top[k] < 0x7F800000u ? 0.f : m;
+    uint32_t lo = 0, hi = 0;
+    float v[kChunk];
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) v[i] = ok ? o[k][i] * inv : 0.f;
+    if (a.type == LVQ_I8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo |= ((uint32_t)(int)__builtin_rintf(v[i]) & 0xFFu) << (8 * i);
+        hi |= ((uint32_t)(int)__builtin_rintf(v[i + 4]) & 0xFFu) << (8 * i);
+      }
+    } else {
+      int q = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+      lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], q, true);
+      q = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+      hi = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], q, true);
+    }
+    if (c + kChunk <= a.cols) {
+      const uint32_t q[2] = {lo, hi};
+      __builtin_memcpy(p + c, q, sizeof(q));
+    } else {
+      const int e = opaque(c);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (e + i < a.cols) p[e + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+    }
+    if constexpr (NV > 2) __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// ---------------------------------------------------------------- rms_norm
+
+struct NormArgs {
+  const void* x;
+  int64_t x_stride;  // bytes
+  const void* residual;
+  void* residual_out;
+  const void* weight;
+  int residual_type, weight_type;
+  float eps;
+  int rows, cols;
+  Out out;
+};
+
+__device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&w)[kChunk]) {
+  if (!a.weight) {
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) w[i] = 1.f;
+  } else if (a.weight_type == LVQ_F32) {
+    unpack(load_chunk<LVQ_F32>(a.weight, c, a.cols), w);
+  } else if (a.weight_type == LVQ_F16) {
+    unpack(load_chunk<LVQ_F16>(a.weight, c, a.cols), w);
+  } else {
+    unpack(load_chunk<LVQ_BF16>(a.weight, c, a.cols), w);
+  }
+}
+
+// A row per workgroup, or per wave where 64 lanes hold one (WAVE).  Rows are
+// taken a grid apart.
+template <int TX, int TR, int NV, bool WAVE>
+__global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
+  __shared__ uint32_t red[2][2][kRowThreads / kWave];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nw = blockDim.x / kWave;
+  const int t = WAVE ? lane : (int)threadIdx.x;
+  const int n = WAVE ? kWave : (int)blockDim.x;
+  const int64_t step = WAVE ? (int64_t)gridDim.x * nw : gridDim.x;
+  constexpr int kResBytes = TR == LVQ_F32 ? 4 : 2;
+  int turn = 0;
+  for (int64_t row = WAVE ? (int64_t)blockIdx.x * nw + wv : blockIdx.x; row < a.rows;
+       row += step, turn ^= 1) {
+    const uint8_t* xr = (const uint8_t*)a.x + row * a.x_stride;
+    const uint8_t* rr = (const uint8_t*)a.residual + (size_t)row * a.cols * kResBytes;
+    // up to two chunks per thread: every load goes out before the first is
+    // used; more: two at a time, or the raw values would not fit in registers
+    constexpr int G = NV < 2 ? NV : 2;
+    float h[NV][kChunk], part = 0.f;
+#pragma unroll
+    for (int k0 = 0; k0 < NV; k0 += G) {
+      Chunk<TX> xc[G];
+      Chunk<TR == kNone ? LVQ_F16 : TR> rc[G];
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        const int c = (t + (k0 + k) * n) * kChunk;
+        xc[k] = load_chunk<TX>(xr, c, a.cols);
+        if constexpr (TR != kNone) rc[k] = load_chunk<TR>(rr, c, a.cols);
+      }
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        unpack(xc[k], h[k0 + k]);
+        if constexpr (TR != kNone) {
+          float r[kChunk];
+          unpack(rc[k], r);
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) h[k0 + k][i] += r[i];
+        }
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+          part = __builtin_fmaf(h[k0 + k][i], h[k0 + k][i], part);
+      }
+      if constexpr (NV > 2) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (a.residual_out) {
+      uint8_t* ro = (uint8_t*)a.residual_out +
+                    (size_t)row * a.cols * (a.residual_type == LVQ_F32 ? 4 : 2);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int c = (t + k * n) * kChunk;
+        if (c < a.cols) store_chunk(ro, a.residual_type, c, a.cols, h[k]);
+        if constexpr (NV > 2) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    part = wave_sum_lane63(part);
+    float sum = __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, part), kWave - 1));
+    if constexpr (!WAVE) {
+      // two sets of LDS words, used in turn: a wave can be at most one barrier
+      // ahead of another, so it never writes a set that is still being read
+      float* rs = (float*)red[turn][0];
+      if (lane == 0) rs[wv] = sum;
+      __syncthreads();
+      sum = rs[0];
+      for (int w = 1; w < nw; ++w) sum += rs[w];
+    }
+    const float inv = rsqrtf(sum / (float)a.cols + a.eps);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float w[kChunk];
+      load_weight(a, (t + k * n) * kChunk, w);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) h[k][i] = h[k][i] * inv * w[i];
+      if constexpr (NV > 2) __builtin_amdgcn_sched_barrier(0);
+    }
+    emit<NV, WAVE>(a.out, (size_t)row, h, t, n, red[turn][1]);
+  }
+}
+
+// Threads and chunks per thread of a row kernel: a wave per row up to 512
+// columns, else a workgroup per row.
+struct RowShape {
+  int nv, threads;
+  bool wave;
+};
+RowShape row_shape(int cols) {
+  const int chunks = (cols + kChunk - 1) / kChunk;
+  if (chunks <= kWave) return {1, 256, true};
+  int nv = 1;
+  while (chunks > nv * kRowThreads) nv *= 2;
+  const int threads = ((chunks + nv - 1) / nv + kWave - 1) / kWave * kWave;
+  return {nv, threads, false};
+}
+
+unsigned row_grid(int rows, const RowShape& s) {
+  long long wgs = s.wave ? ((long long)rows + s.threads / kWave - 1) / (s.threads / kWave) : rows;
+  const long long most = (long long)device_cus() * (2048 / s.threads) * 4;
+  return (unsigned)(wgs < most ? wgs : most);
+}
+
+template <int TX, int TR>
+int launch_norm_row(const NormArgs& a, hipStream_t st) {
+  const RowShape s = row_shape(a.cols);
+  const dim3 grid(row_grid(a.rows, s)), block(s.threads);
+  clear_hip_error();
+  if (s.wave) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 1, true>), grid, block, 0, st, a);
+  else if (s.nv == 1) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 1, false>), grid, block, 0, st, a);
+  else if (s.nv == 2) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 2, false>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 4, false>), grid, block, 0, st, a);
+  return launch_status();
+}
+
+template <int TX>
+int launch_norm(const NormArgs& a, hipStream_t st) {
+  if (!a.residual) return launch_norm_row<TX, kNone>(a, st);
+  if (a.residual_type == LVQ_F32) return launch_norm_row<TX, LVQ_F32>(a, st);
+  if (a.residual_type == LVQ_F16) return launch_norm_row<TX, LVQ_F16>(a, st);
+  return launch_norm_row<TX, LVQ_BF16>(a, st);
+}
+
+// ---------------------------------------------------------------- silu_mul
+
+struct SiluArgs {
+  const void *gate, *up;
+  int64_t stride;  // bytes
+  int rows, cols, seg_shift, segs;
+  Out out;
+};
+
+template <int T>
+__device__ __forceinline__ void silu_chunk(const Chunk<T>& gc, const Chunk<T>& uc,
+                                           float (&o)[kChunk]) {
+  float g[kChunk], u[kChunk];
+  unpack(gc, g);
+  unpack(uc, u);
+#pragma unroll
+  for (int i = 0; i < kChunk; ++i) {
+    // e^-g as 2^(-g log2 e); both of the hardware's approximations (2^v and
+    // 1/v) are within an ulp, the product of the exponent off by |g| 2^-24
+    const float e = __builtin_amdgcn_exp2f(g[i] * -1.44269504f);
+    o[i] = g[i] * __builtin_amdgcn_rcpf(1.f + e) * u[i];
+  }
+}
+
+// A row per workgroup or wave: for one scale per row.
+template <int T, int NV, bool WAVE>
+__global__ void __launch_bounds__(kRowThreads) silu_row_kernel(SiluArgs a) {
+  __shared__ uint32_t red[2][kRowThreads / kWave];
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nw = blockDim.x / kWave;
+  const int t = WAVE ? (int)(threadIdx.x & (kWave - 1)) : (int)threadIdx.x;
+  const int n = WAVE ? kWave : (int)blockDim.x;
+  const int64_t step = WAVE ? (int64_t)gridDim.x * nw : gridDim.x;
+  int turn = 0;
+  for (int64_t row = WAVE ? (int64_t)blockIdx.x * nw + wv : blockIdx.x; row < a.rows;
+       row += step, turn ^= 1) {
+    const uint8_t* gr = (const uint8_t*)a.gate + row * a.stride;
+    const uint8_t* ur = (const uint8_t*)a.up + row * a.stride;
+    Chunk<T> gc[NV], uc[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (t + k * n) * kChunk;
+      gc[k] = load_chunk<T>(gr, c, a.cols);
+      uc[k] = load_chunk<T>(ur, c, a.cols);
+    }
+    float o[NV][kChunk];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) silu_chunk<T>(gc[k], uc[k], o[k]);
+    emit<NV, WAVE>(a.out, (size_t)row, o, t, n, red[turn]);
+  }
+}
+
+// Chunks are independent (fp16, or groups inside a wave): a workgroup takes 256
+// chunks, 2^seg_shift neighbours of each of 256 >> seg_shift rows.
+template <int T>
+__global__ void __launch_bounds__(256) silu_flat_kernel(SiluArgs a) {
+  const int seg = 1 << a.seg_shift, per = 256 >> a.seg_shift;
+  const int64_t tiles = ((int64_t)a.rows + per - 1) / per * a.segs;
+  for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+    const int64_t block = i / a.segs;
+    const int64_t row = block * per + (threadIdx.x >> a.seg_shift);
+    const int chunk = (int)(i - block * a.segs) * seg + (threadIdx.x & (seg - 1));
+    const int c = row < a.rows ? chunk * kChunk : a.cols;  // a.cols: nothing of this tile
+    const int64_t r = row < a.rows ? row : 0;
+    const uint8_t* gr = (const uint8_t*)a.gate + r * a.stride;
+    const uint8_t* ur = (const uint8_t*)a.up + r * a.stride;
+    float o[1][kChunk];
+    silu_chunk<T>(load_chunk<T>(gr, c, a.cols), load_chunk<T>(ur, c, a.cols), o[0]);
+    emit<1, true>(a.out, (size_t)r, o, c < a.cols ? chunk : (a.cols + kChunk - 1) / kChunk, 0,
+                  nullptr);
+  }
+}
+
+template <int T>
+int launch_silu(SiluArgs& a, hipStream_t st) {
+  clear_hip_error();
+  if (a.out.type != LVQ_F16 && a.out.group == 0) {
+    const RowShape s = row_shape(a.cols);
+    const dim3 grid(row_grid(a.rows, s)), block(s.threads);
+    if (s.wave) hipLaunchKernelGGL((silu_row_kernel<T, 1, true>), grid, block, 0, st, a);
+    else if (s.nv == 1) hipLaunchKernelGGL((silu_row_kernel<T, 1, false>), grid, block, 0, st, a);
+    else if (s.nv == 2) hipLaunchKernelGGL((silu_row_kernel<T, 2, false>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((silu_row_kernel<T, 4, false>), grid, block, 0, st, a);
+    return launch_status();
+  }
+  const int chunks = (a.cols + kChunk - 1) / kChunk;
+  a.seg_shift = 5;  // at least the 32 lanes of the widest group
+  while (a.seg_shift < 8 && (1 << a.seg_shift) < chunks) ++a.seg_shift;
+  a.segs = (chunks + (1 << a.seg_shift) - 1) >> a.seg_shift;
+  const int per = 256 >> a.seg_shift;
+  const long long tiles = ((long long)a.rows + per - 1) / per * a.segs;
+  const long long most = (long long)device_cus() * 32;
+  const dim3 grid((unsigned)(tiles < most ? tiles : most));
+  hipLaunchKernelGGL(silu_flat_kernel<T>, grid, dim3(256), 0, st, a);
+  return launch_status();
+}
+
+// ---------------------------------------------------------------- checks
+
+inline bool float_type(int t) { return t == LVQ_F32 || t == LVQ_F16 || t == LVQ_BF16; }
+inline size_t type_bytes(int t) { return t == LVQ_F32 ? 4 : t == LVQ_I8 || t == LVQ_E4M3 ? 1 : 2; }
+inline bool aligned_to(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
+
+// The output arguments both entry points share; fills *o.
+int check_out(void* out, int out_type, float* out_scale, int out_group, int rows, int cols,
+              Out* o) {
+  if (out_type != LVQ_F16 && out_type != LVQ_I8 && out_type != LVQ_E4M3) return LVQ_E_SHAPE;
+  const bool eight = out_type != LVQ_F16;
+  if (out_group != 0 &&
+      (!eight || (out_group != 32 && out_group != 64 && out_group != 128 && out_group != 256)))
+    return LVQ_E_SHAPE;
+  if (!eight && out_scale) return LVQ_E_SHAPE;
+  if (rows && cols && (!out || (eight && !out_scale))) return LVQ_E_NULL;
+  if (!aligned16(out) || !aligned16(out_scale)) return LVQ_E_ALIGN;
+  o->out = out, o->scale = out_scale, o->type = out_type, o->group = out_group;
+  o->groups = out_group ? (cols + out_group - 1) / out_group : 1;
+  o->cols = cols;
+  return LVQ_OK;
+}
+
+struct Range {
+  const void* p;
+  size_t n;
+};
+// Bytes from the first to the last value of `rows` strided rows.
+inline size_t strided_bytes(int rows, int cols, int64_t stride, int type) {
+  return ((size_t)(rows - 1) * stride + cols) * type_bytes(type);
+}
+
+}  // namespace lvq
+
+using namespace lvq;
+
+extern "C" int lvq_rms_norm(const void* x, int x_type, int64_t x_stride, const void* residual,
+                            int residual_type, void* residual_out, const void* weight,
+                            int weight_type, float eps, int rows, int cols, void* out,
+                            int out_type, float* out_scale, int out_group, void* stream) {
+  if (rows < 0 || cols < 0 || cols > kMaxRowCols || x_stride < cols) return LVQ_E_SHAPE;
+  if (!float_type(x_type) || ((residual || residual_out) && !float_type(residual_type)) ||
+      (weight && !float_type(weight_type)))
+    return LVQ_E_SHAPE;
+  NormArgs a;
+  const int e = check_out(out, out_type, out_scale, out_group, rows, cols, &a.out);
+  if (e) return e;
+  if (rows == 0 || cols == 0) return LVQ_OK;
+  if (!x) return LVQ_E_NULL;
+  if (!aligned_to(x, type_bytes(x_type)) || !aligned16(residual) || !aligned16(residual_out) ||
+      !aligned16(weight))
+    return LVQ_E_ALIGN;
+  const size_t all = (size_t)rows * cols;
+  const Range in[3] = {{x, strided_bytes(rows, cols, x_stride, x_type)},
+                       {residual, residual ? all * type_bytes(residual_type) : 0},
+                       {weight, weight ? (size_t)cols * type_bytes(weight_type) : 0}};
+  const Range made[3] = {{residual_out, residual_out ? all * type_bytes(residual_type) : 0},
+                         {out, all * type_bytes(out_type)},
+                         {out_scale, out_scale ? (size_t)rows * a.out.groups * 4 : 0}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 3; ++j) {
+      const bool same_stream = i == 0 && j == 1 && residual == residual_out;
+      if (!same_stream && ranges_overlap(made[i].p, made[i].n, in[j].p, in[j].n))
+        return LVQ_E_SHAPE;
+      if (j > i && ranges_overlap(made[i].p, made[i].n, made[j].p, made[j].n)) return LVQ_E_SHAPE;
+    }
+  }
+  a.x = x, a.x_stride = x_stride * (int64_t)type_bytes(x_type);
+  a.residual = residual, a.residual_out = residual_out, a.residual_type = residual_type;
+  a.weight = weight, a.weight_type = weight_type, a.eps = eps;
+  a.rows = rows, a.cols = cols;
+  hipStream_t st = (hipStream_t)stream;
+  if (x_type == LVQ_F32) return launch_norm<LVQ_F32>(a, st);
+  if (x_type == LVQ_F16) return launch_norm<LVQ_F16>(a, st);
+  return launch_norm<LVQ_BF16>(a, st);
+}
+
+extern "C" int lvq_silu_mul(const void* gate, const void* up, int in_type, int64_t in_stride,
+                            int rows, int cols, void* out, int out_type, float* out_scale,
+                            int out_group, void* stream) {
+  if (rows < 0 || cols < 0 || cols > kMaxCols || in_stride < cols || !float_type(in_type))
+    return LVQ_E_SHAPE;
+  if (cols > kMaxRowCols && out_type != LVQ_F16 && out_group == 0) return LVQ_E_SHAPE;
+  SiluArgs a;
+  const int e = check_out(out, out_type, out_scale, out_group, rows, cols, &a.out);
+  if (e) return e;
+  if (rows == 0 || cols == 0) return LVQ_OK;
+  if (!gate || !up) return LVQ_E_NULL;
+  const size_t tb = type_bytes(in_type);
+  if (!aligned_to(gate, tb) || !aligned_to(up, tb)) return LVQ_E_ALIGN;
+  const size_t in_bytes = strided_bytes(rows, cols, in_stride, in_type);
+  const Range in[2] = {{gate, in_bytes}, {up, in_bytes}};
+  const Range made[2] = {{out, (size_t)rows * cols * type_bytes(out_type)},
+                         {out_scale, out_scale ? (size_t)rows * a.out.groups * 4 : 0}};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2; ++j)
+      if (ranges_overlap(made[i].p, made[i].n, in[j].p, in[j].n)) return LVQ_E_SHAPE;
+  if (ranges_overlap(made[0].p, made[0].n, made[1].p, made[1].n)) return LVQ_E_SHAPE;
+  a.gate = gate, a.up = up, a.stride = in_stride * (int64_t)tb;
+  a.rows = rows, a.cols = cols, a.seg_shift = 8, a.segs = 1;
+  hipStream_t st = (hipStream_t)stream;
+  if (in_type == LVQ_F32) return launch_silu<LVQ_F32>(a, st);
+  if (in_type == LVQ_F16) return launch_silu<LVQ_F16>(a, st);
+  return launch_silu<LVQ_BF16>(a, st);
+}

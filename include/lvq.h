@@ -55,6 +55,15 @@ enum {
   LVQ_E_LAYOUT = -8     /* a block's class cannot be stored in the requested layout */
 };
 
+/* Element types of the arguments that say so. */
+enum {
+  LVQ_F32 = 0,  /* IEEE binary32 */
+  LVQ_F16 = 1,  /* IEEE binary16 */
+  LVQ_BF16 = 2, /* bfloat16 */
+  LVQ_I8 = 3,   /* int8, -127..127, largest magnitude 127 */
+  LVQ_E4M3 = 4  /* 8-bit float, 4 exponent and 3 mantissa bits, no infinities, largest 448 */
+};
+
 #define LVQ_NUM_CLASSES 302 /* 301 classes on shells 2..12 plus the origin */
 #define LVQ_MAX_BATCH 4
 
@@ -365,6 +374,76 @@ int trellis_gemv(const uint32_t* bits, const uint16_t* table, const uint16_t* sc
  * cols must be a multiple of 8 and batch * cols <= 65536. */
 int fp16_gemv(const uint16_t* W, int rows, int cols, const uint16_t* x, float* y,
               int batch, void* stream);
+
+/* 4-bit weights with group scales: the arm for the projections that do not
+ * stand two bits.  y[b][r] = sum_c w[r][c] * x[b][c] with
+ *   w[r][c] = scale[r][c/group] * (q[r][c] - zero[r][c/group])
+ *   codes  uint8 [rows][16 * ceil(cols/32)], two columns per byte: q of column
+ *          c is bits 4*(c%2)..4*(c%2)+3 of byte c/2 of its row, 0..15 (read as
+ *          32-bit words, column c is bits 4*(c%8)..+3 of word c/8).  Rows are
+ *          padded to whole 16-byte units; the padding's content is ignored.
+ *   scale  fp16 [rows][G], G = ceil(cols/group)
+ *   zero   fp16 [rows][G], any finite value; NULL for 8 everywhere
+ *   group  columns per scale: 32, 64, 128, 256, or 0 for one scale per row
+ *          (G = 1); the last group of a row may be short
+ * cols is any number with batch * cols <= 65536.  LVQ_E_SHAPE for any other
+ * size or group; LVQ_E_SHAPE too when y overlaps x (or x_scale).  A row's result is the same
+ * from run to run and at every batch; the order of its sum depends on the
+ * matrix's shape and the device. */
+int q4_gemv(const uint8_t* codes, const uint16_t* scale, const uint16_t* zero, int group, int rows,
+            int cols, const uint16_t* x, float* y, int batch, void* stream);
+
+/* q4_gemv with x in 8 bits, as lvq_rms_norm and lvq_silu_mul write it:
+ *   x        int8 or e4m3 [batch][cols], x_type LVQ_I8 or LVQ_E4M3
+ *   x_scale  fp32 [batch][H], H = ceil(cols/x_group): the value of column c is
+ *            x_scale[b][c/x_group] * x[b][c]
+ *   x_group  32, 64, 128, 256, or 0 for one scale per batch row (H = 1)
+ * int8 products are summed in 32-bit integers over 32 columns, then in fp32.
+ * LVQ_E_SHAPE for any other x_type or x_group; otherwise as q4_gemv. */
+int q4_gemv_q8(const uint8_t* codes, const uint16_t* scale, const uint16_t* zero, int group,
+               int rows, int cols, const void* x, int x_type, const float* x_scale, int x_group,
+               float* y, int batch, void* stream);
+
+/* Root-mean-square norm of a residual stream, between two projections:
+ *   h = x + residual                       (fp32; h = x when residual is NULL)
+ *   residual_out = h                       (rounded once; skipped when NULL)
+ *   out = h * (mean_c(h^2) + eps)^-1/2 * weight
+ *   x            fp32, fp16 or bf16 (x_type) [rows] rows of cols values,
+ *                x_stride values from one row's start to the next's
+ *                (x_stride >= cols)
+ *   residual     [rows][cols] of residual_type (fp32, fp16 or bf16), or NULL
+ *   residual_out [rows][cols] of residual_type, or NULL; may be residual itself
+ *   weight       [cols] of weight_type (fp32, fp16 or bf16), or NULL for ones
+ *   out          [rows][cols] of out_type: fp16 (rounded once from fp32), or 8
+ *                bits, LVQ_I8 or LVQ_E4M3, with
+ *   out_scale    fp32 [rows][H], H = ceil(cols/out_group), out_group 32, 64,
+ *                128, 256 or 0 for one scale per row: with a the largest
+ *                magnitude of the group's fp32 results and M the type's largest
+ *                value (127 or 448), out_scale = a / M and the codes are the
+ *                results times M / a, rounded to the nearest (ties to even).  A
+ *                group whose a is below 2^-100 gets scale 0 and zero codes, one
+ *                that holds a NaN or an infinity zero codes and a scale that is
+ *                not finite.  NULL and out_group 0 for fp16.
+ * The statistics and the results before the rounding are fp32.  rows is any
+ * number >= 0, cols <= 32768.  x needs the alignment of its type only (it may
+ * be a slice of a wider buffer); every other pointer 16 bytes.  No output may overlap an input
+ * or another output, residual_out == residual excepted (LVQ_E_SHAPE). */
+int lvq_rms_norm(const void* x, int x_type, int64_t x_stride, const void* residual,
+                 int residual_type, void* residual_out, const void* weight, int weight_type,
+                 float eps, int rows, int cols, void* out, int out_type, float* out_scale,
+                 int out_group, void* stream);
+
+/* Gated activation between the gate/up projections and the down projection:
+ *   out = gate / (1 + exp(-gate)) * up        (fp32, rounded once)
+ *   gate, up   fp32, fp16 or bf16 (in_type) rows of cols values, in_stride
+ *              values apart (gate and up may be the halves of one matrix's
+ *              output, in_stride = 2 * cols); in_stride >= cols
+ *   out, out_type, out_scale, out_group as lvq_rms_norm
+ * cols <= 65536, with one scale per row cols <= 32768; otherwise limits,
+ * alignment (gate and up as x there) and errors as lvq_rms_norm. */
+int lvq_silu_mul(const void* gate, const void* up, int in_type, int64_t in_stride, int rows,
+                 int cols, void* out, int out_type, float* out_scale, int out_group,
+                 void* stream);
 
 /* Activation rotation before a GEMV whose weights are stored in a rotated
  * basis.  arXiv 2609.02652 (the incoherence-rotated basis; the paragraph on

@@ -20,6 +20,9 @@ gemv    f64 reconstruction of W for every arm (Leech, BPDQ, bitshift trellis,
 layout  the expected logical planes of a Leech block and an independent
         unpacker of the packed blob the expander writes.
 rotate  the activation rotation (H kron Q)(S x) with its error bound.
+q4      f64 weights of the 4-bit format, values of 8-bit activations.
+norm    the root-mean-square norm, the gated activation and the 8-bit rounding
+        with group scales, each with its error bound.
 index   the 47-bit rank / unrank of the m <= 12 ball, the 48-bit word and
         shape-gain dequantisation.
 

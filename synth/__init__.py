@@ -26,6 +26,8 @@ or checkpoint is involved):
          drawn like cfg 3.
   cfg 5  a Qwen3-8B-shaped stack of 36 layers x {q, k, v, o, gate, up, down}
          drawn like cfg 3.
+  cfg 7  4-bit codes with group scales and zeros, 8-bit activations, and the
+         inputs of the norm and the gated activation, of any shape.
 Scales are fp16(|N(0,1)| * 0.02); x is fp16 N(0,1); fp16 rounding is
 round-to-nearest-even.
 """
@@ -310,6 +312,32 @@ def trellis_matrix(rows: int, cols: int, cfg: int = 4) -> dict:
     table = fp16_bits(rng_for(0, cfg, ARR_TABLE).standard_normal(1 << 16))
     scale = fp16_bits(np.abs(rng_for(0, cfg, ARR_SCALE, rows, cols).standard_normal(rows)) * 0.02)
     return {"bits": bits, "table": table, "scale": scale, "rows": rows, "cols": cols}
+
+
+def q4_matrix(rows: int, cols: int, group: int, zeros: bool, key=()) -> dict:
+    """4-bit workload: codes uint8 [R][16 ceil(K/32)] (two columns per byte; the
+    padding of a row is random too), scale fp16 bits [R][G] of 0.01 to 0.03, zero
+    fp16 bits [R][G] (whole numbers 4..11 and, one in four, halves between) or
+    None.  group 0: one scale per row."""
+    base = [0, 7] + list(key)
+    n = -(-cols // group) if group else 1
+    codes = rng_for(*base, ARR_COORDS, rows, cols).integers(
+        0, 256, (rows, -(-cols // 32) * 16)).astype(np.uint8)
+    scale = fp16_bits(0.01 + 0.02 * rng_for(*base, ARR_SCALE, rows, cols).random((rows, n)))
+    zero = None
+    if zeros:
+        r = rng_for(*base, ARR_ZERO, rows, cols)
+        zero = fp16_bits(r.integers(4, 12, (rows, n)) + 0.5 * (r.random((rows, n)) < 0.25))
+    return {"codes": codes, "scale": scale, "zero": zero, "rows": rows, "cols": cols,
+            "group": group}
+
+
+def hidden(rows: int, cols: int, key=()) -> np.ndarray:
+    """Hidden states, float64 [rows][cols]: N(0, 1), one column in 500 times 20."""
+    r = rng_for(0, 7, *key, ARR_X, rows, cols)
+    v = r.standard_normal((rows, cols))
+    v[:, r.random(cols) < 0.002] *= 20
+    return v
 
 
 def qwen3_8b_matrix(layer: int, matrix: int) -> dict:
