@@ -1,10 +1,31 @@
 // 4-bit matvec with group scales (q4_gemv, q4_gemv_q8).
 //
-//   y[b][r] = sum_g s_rg (sum_(c in g) q_rc x_bc - z_rg sum_(c in g) x_bc)
+//   y[b][r] = sum_u s_ru (sum_(c in u) q_rc x_bc - z_ru sum_(c in u) x_bc)
 //
-// One wave per row; a lane takes units of 32 columns (16 bytes of codes), 64
-// units apart, multiplies in fp32 and applies the unit's scale to the unit's
-// sum.  The first, plain form of the kernel.
+// over the units u of 32 columns (16 bytes of codes), inside which scale and
+// zero are constant.  The inner sums run on the matrix cores: the 4x4x4 MFMA in
+// 16 blocks multiplies, per instruction, 16 independent 4 (batch) x 4 (columns)
+// by 4 (columns) x 4 (rows) products, which is the shape of a matvec of up to
+// four batch rows.  Lane l holds row l % 4 of a quad of rows and unit l / 4 of
+// a step of 16 units: its 16 bytes of codes are its own B operands, the x of
+// its unit (batch row l % 4) its A operands, and the result leaves in lane l the
+// four batch sums of its own row and unit, so scale and zero are applied in the
+// lane that loaded them, in fp32, once per unit.
+//
+// No conversion of the codes to floats: a 4-bit value in the lowest bits of an
+// fp16 (or four bits higher) is a subnormal, the value times 2^-24 (2^-20).
+// Per 8 codes one shift and four masks give two A x B operands (columns 0, 4,
+// 2, 6 and 1, 5, 3, 7 of the eight; x is stored in LDS in that order), and two
+// accumulators keep the two powers of two apart.  For int8 x two masks and a
+// shift give the codes as bytes and the sums are exact 32-bit integers.
+//
+// The weights are the bytes (4.1 to 5 bits each): 4 flops per byte at batch 1.
+// Each wave streams 1 KiB of codes per step (4 rows x 256 contiguous bytes)
+// through a ring of register sets, kQ4Ring steps in flight; x and the sums of x
+// over every unit sit in LDS.  A quad's steps are split over S waves of a
+// workgroup where rows are few, joined in LDS in a fixed order.
+
+#include <type_traits>
 
 #include "common.h"
 
@@ -32,61 +53,378 @@ struct Q4Args {
   float* y;
 };
 
-__device__ __forceinline__ float f16_to_f32(uint16_t b) {
-  return (float)__builtin_bit_cast(_Float16, b);
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+typedef float float4_t __attribute__((ext_vector_type(4)));
+typedef int int4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef float float2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kQ4Ring = 6;     // steps in flight per wave
+constexpr int kQ4Waves = 16;   // waves per workgroup at most
+constexpr int kStepUnits = 16; // units of 32 columns per step
+constexpr int kXAhead = 4;     // x chunks a wave requests at a time
+
+// LDS: x, then per unit and batch row the sum of x (f16), or x's scale and its
+// product with that sum, then a wave's partial results.
+constexpr int sum_stride(int B) { return B == 3 ? 4 : B; }
+constexpr size_t x_step_bytes(int B, int X) { return (X == kQ4I8 ? 512 : 1024) * (size_t)B; }
+constexpr size_t sum_step_bytes(int B) { return kStepUnits * (size_t)sum_stride(B) * 4; }
+inline size_t q4_lds_bytes(int B, int X, int steps) {
+  return steps * (x_step_bytes(B, X) + sum_step_bytes(B) * (X == kQ4F16 ? 1 : 2)) +
+         kQ4Waves * 4 * (size_t)B * 4;
+}
+
+__device__ __forceinline__ float f16_to_f32(uint32_t b) {
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)b);
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t q4_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes,
+                                           0x00020000);
+}
+
+// ---------------------------------------------------------------- x into LDS
+
+// Eight columns of a batch row as they lie in memory (16 bytes of fp16, or 8),
+// zeros past the row's end; rx: the row.  Rows whose length is no multiple of
+// eight are read value by value (their starts are not aligned).
+template <int X, bool VEC>
+__device__ __forceinline__ u32x4_t load_x8(__amdgpu_buffer_rsrc_t rx, int c) {
+  u32x4_t v = {0, 0, 0, 0};
+  if constexpr (VEC && X == kQ4F16) {
+    v = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rx, c * 2, 0, 0));
+  } else if constexpr (VEC) {
+    const auto h = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rx, c, 0, 0));
+    v.x = h.x, v.y = h.y;
+  } else if constexpr (X == kQ4F16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i >> 1] |= (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rx, (c + i) * 2, 0, 0)
+                   << (16 * (i & 1));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i >> 2] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rx, c + i, 0, 0)
+                   << (8 * (i & 3));
+  }
+  return v;
+}
+
+// The pairs (x0, x4) (x2, x6) (x1, x5) (x3, x7) of eight fp16.
+__device__ __forceinline__ u32x4_t pair_order(u32x4_t d) {
+  return u32x4_t{__builtin_amdgcn_perm(d.z, d.x, 0x05040100u),
+                 __builtin_amdgcn_perm(d.w, d.y, 0x05040100u),
+                 __builtin_amdgcn_perm(d.z, d.x, 0x07060302u),
+                 __builtin_amdgcn_perm(d.w, d.y, 0x07060302u)};
+}
+
+// Eight columns (word w of unit u of step t, batch row bb) into LDS, and, from
+// the quad of lanes that holds a unit, the unit's sums.
+template <int B, int X>
+__device__ __forceinline__ void put_x8(const Q4Args& a, uint8_t* xs, float* sums, float* scaled,
+                                       u32x4_t v, int bb, int t, int lane) {
+  const int ul = lane >> 2, w = lane & 3;
+  float sum;
+  if constexpr (X == kQ4I8) {
+    // even and odd columns apart, as masking the codes' bytes leaves them
+    const u32x2_t o = {__builtin_amdgcn_perm(v.y, v.x, 0x06040200u),
+                       __builtin_amdgcn_perm(v.y, v.x, 0x07050301u)};
+    *(u32x2_t*)(xs + (size_t)t * x_step_bytes(B, X) + (((w >> 1) * 16 + ul) * B + bb) * 16 +
+                (w & 1) * 8) = o;
+    const int s = __builtin_amdgcn_sdot4((int)v.x, 0x01010101, 0, false);
+    sum = (float)__builtin_amdgcn_sdot4((int)v.y, 0x01010101, s, false);
+  } else {
+    u32x4_t h = v;
+    if constexpr (X == kQ4E4M3) {  // every e4m3 value is an fp16 value
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[i], false);
+        const float2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[i], true);
+        h[2 * i] = __builtin_bit_cast(uint32_t, lvq_half2{(_Float16)lo.x, (_Float16)lo.y});
+        h[2 * i + 1] = __builtin_bit_cast(uint32_t, lvq_half2{(_Float16)hi.x, (_Float16)hi.y});
+      }
+    }
+    *(u32x4_t*)(xs + (size_t)t * x_step_bytes(B, X) + ((w * 16 + ul) * B + bb) * 16) =
+        pair_order(h);
+    constexpr uint32_t kOnes = 0x3C003C00u;
+    sum = dot2(h.x, kOnes, dot2(h.y, kOnes, dot2(h.z, kOnes, dot2(h.w, kOnes, 0.f))));
+  }
+  sum = dpp_add<0x4E, 0xF>(dpp_add<0xB1, 0xF>(sum));  // the quad's four words
+  if (w == 0) {
+    const int u = t * kStepUnits + ul, at = u * sum_stride(B) + bb;
+    if constexpr (X != kQ4I8) sum *= 0x1p-24f;  // the scale of the subnormal codes
+    if constexpr (X == kQ4F16) {
+      sums[at] = sum;
+    } else {
+      const float s =
+          u < a.nunits ? a.xscale[(size_t)bb * a.xgroups + (u >> a.xshift)] : 0.f;
+      scaled[at] = s;
+      sums[at] = s * sum;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+// v plus its counterparts in the other 15 blocks of four lanes: rotations inside
+// a row of 16 lanes, then rows swapped pairwise.  Each step adds the same two
+// values on both sides (blocks two apart first, then the two pair sums), so
+// every lane ends with the same bits.
+__device__ __forceinline__ float sum_blocks(float v) {
+  v = dpp_add<0x128, 0xF>(v);  // row_ror:8
+  v = dpp_add<0x124, 0xF>(v);  // row_ror:4
+  uint32_t u = __builtin_bit_cast(uint32_t, v);
+  auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  v = __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
+  u = __builtin_bit_cast(uint32_t, v);
+  auto q = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, (uint32_t)q[0]) + __builtin_bit_cast(float, (uint32_t)q[1]);
+}
+
+template <bool Z>
+struct Q4Step {  // one step of a wave: a lane's 32 codes, its scale and zero
+  u32x4_t w;
+  uint16_t s, z;
+};
+
+// S waves of a workgroup share a quad of rows: wave ks of them takes the steps
+// ks, ks + S, ...  Quads go round the workgroups, so a last, partly filled
+// round is spread over all of them.  With S > 1 there is one round.
+template <int B, int X, bool Z>
+__global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a, int steps, int S) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  uint8_t* xs = smem;
+  float* sums = (float*)(smem + steps * x_step_bytes(B, X));
+  float* scaled = sums + steps * (sum_step_bytes(B) / 4);
+  float* join = X == kQ4F16 ? scaled : scaled + steps * (sum_step_bytes(B) / 4);
+
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nw = blockDim.x / kWave;
+  const int quads = (a.rows + 3) / 4;
+  const int slots = nw / S, ks = wv % S;
+  const int q0 = (wv / S) * gridDim.x + blockIdx.x, qstride = slots * gridDim.x;
+  const int per = (steps - ks + S - 1) / S;  // this wave's steps of a quad
+  const int mine = q0 < quads ? (quads - 1 - q0) / qstride + 1 : 0;
+  const int items = mine * per;
+
+  // 1. the ring of steps: one sequence of loads without a branch, those past
+  //    the wave's last aimed at an empty buffer
+  Q4Step<Z> ring[kQ4Ring];
+  int lq = q0, lt = ks, left = items;  // the next step to load
+  const int ul = lane >> 2, r4 = lane & 3;
+  const int row_bytes = a.nunits * 16;
+  const int lane_off = r4 * row_bytes + ul * 16;
+  auto load = [&](Q4Step<Z>& st) {
+    const int row = lq * 4;
+    const uint32_t n = left > 0 ? (uint32_t)(a.rows - row < 4 ? a.rows - row : 4) : 0u;
+    const size_t qrow = left > 0 ? (size_t)row : 0;
+    const int u = lt * kStepUnits + ul;
+    // a unit past the row's end: an offset past every buffer, by the sign bit
+    // of the difference (a select becomes a branch around the load)
+    const int past = (a.nunits - 1 - u) & (int)0x80000000;
+    st.w = __builtin_bit_cast(
+        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                     q4_rsrc(a.codes + qrow * row_bytes, n * row_bytes), lane_off | past,
+                     lt * (kStepUnits * 16), 2));
+    const int moff = ((r4 * a.groups + (u >> a.gshift)) * 2) | past;
+    st.s = __builtin_amdgcn_raw_buffer_load_b16(
+        q4_rsrc(a.scale + qrow * a.groups, n * a.groups * 2), moff, 0, 0);
+    if constexpr (Z)
+      st.z = __builtin_amdgcn_raw_buffer_load_b16(
+          q4_rsrc(a.zero + qrow * a.groups, n * a.groups * 2), moff, 0, 0);
+    --left;
+    lt += S;
+    if (lt >= steps) lt = ks, lq += qstride;
+  };
+
+  // 2. x: each wave takes chunks of 64 x 8 columns (one step of one batch row),
+  //    kXAhead requested at a time; the ring's first loads go out behind the
+  //    last of them, so the wait for x does not include the weights
+  const int chunks = B * steps;
+  u32x4_t xv[kXAhead];
+  // chunk i is step i - bb steps of batch row bb; past the last, nothing
+  auto row_of = [&](int i) {
+    int bb = 0;
+#pragma unroll
+    for (int k = 1; k < B; ++k) bb += i >= k * steps;
+    return bb;
+  };
+  auto load_chunks = [&](int i0, auto vec) {
+#pragma unroll
+    for (int k = 0; k < kXAhead; ++k) {
+      const int i = i0 + k * nw, bb = row_of(i), t = i - bb * steps;
+      constexpr int E = X == kQ4F16 ? 2 : 1;
+      const auto rx = q4_rsrc((const uint8_t*)a.x + (size_t)bb * a.cols * E,
+                              i < chunks ? a.cols * E : 0);
+      xv[k] = load_x8<X, decltype(vec)::value>(rx, (t * 64 + lane) * 8);
+    }
+  };
+  auto put_chunks = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kXAhead; ++k) {
+      const int i = i0 + k * nw, bb = row_of(i);
+      if (i < chunks) put_x8<B, X>(a, xs, sums, scaled, xv[k], bb, i - bb * steps, lane);
+    }
+  };
+  auto load_any = [&](int i0) {
+    if (a.cols % 8 == 0) load_chunks(i0, std::true_type{});
+    else load_chunks(i0, std::false_type{});
+  };
+  int i0 = wv;
+  load_any(i0);
+  for (; i0 + kXAhead * nw < chunks; i0 += kXAhead * nw) {
+    put_chunks(i0);
+    load_any(i0 + kXAhead * nw);
+  }
+#pragma unroll
+  for (int d = 0; d < kQ4Ring; ++d) load(ring[d]);
+  put_chunks(i0);
+  __syncthreads();
+
+  // 3. the steps
+  const uint8_t* xl = xs + (ul * B + (r4 < B ? r4 : 0)) * 16;
+  const float* sl = sums + ul * sum_stride(B);
+  const float* tl = scaled + ul * sum_stride(B);
+  float acc[B];
+#pragma unroll
+  for (int bb = 0; bb < B; ++bb) acc[bb] = 0.f;
+  int cq = q0, ct = ks;  // the step being multiplied
+
+  auto multiply = [&](const Q4Step<Z>& st) {
+    const uint8_t* xt = xl + (size_t)ct * x_step_bytes(B, X);
+    float v[B];
+    if constexpr (X == kQ4I8) {
+      int4_t c = {0, 0, 0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4_t x = *(const u32x4_t*)(xt + h * 256 * B);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t w = st.w[2 * h + k];
+          c = __builtin_amdgcn_mfma_i32_4x4x4i8((int)x[2 * k], (int)(w & 0x0F0F0F0Fu), c, 0, 0, 0);
+          c = __builtin_amdgcn_mfma_i32_4x4x4i8((int)x[2 * k + 1], (int)((w >> 4) & 0x0F0F0F0Fu), c,
+                                                0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int bb = 0; bb < B; ++bb) v[bb] = (float)c[bb];
+    } else {
+      float4_t lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const u32x4_t x = *(const u32x4_t*)(xt + k * 256 * B);
+        const uint32_t w = st.w[k], w8 = w >> 8;
+        lo = __builtin_amdgcn_mfma_f32_4x4x4f16(
+            __builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}),
+            __builtin_bit_cast(half4_t, u32x2_t{w & 0x000F000Fu, w8 & 0x000F000Fu}), lo, 0, 0, 0);
+        hi = __builtin_amdgcn_mfma_f32_4x4x4f16(
+            __builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}),
+            __builtin_bit_cast(half4_t, u32x2_t{w & 0x00F000F0u, w8 & 0x00F000F0u}), hi, 0, 0, 0);
+      }
+#pragma unroll
+      for (int bb = 0; bb < B; ++bb) v[bb] = __builtin_fmaf(hi[bb], 0.0625f, lo[bb]);
+    }
+    const float s = f16_to_f32(st.s);
+    const float z = Z ? f16_to_f32(st.z) : 8.f;
+    const float* sx = sl + ct * (kStepUnits * sum_stride(B));
+    const float* tx = tl + ct * (kStepUnits * sum_stride(B));
+#pragma unroll
+    for (int bb = 0; bb < B; ++bb) {
+      if constexpr (X != kQ4F16) v[bb] *= tx[bb];
+      acc[bb] = __builtin_fmaf(s, __builtin_fmaf(-z, sx[bb], v[bb]), acc[bb]);
+    }
+  };
+  // lane 4 bb + i < 4 B: the sum of row i of the quad, batch row bb
+  auto total = [&]() {
+    float r = 0.f;
+#pragma unroll
+    for (int bb = 0; bb < B; ++bb) {
+      const float t = sum_blocks(acc[bb]);
+      r = ul == bb ? t : r;
+      acc[bb] = 0.f;
+    }
+    return r;
+  };
+  auto store = [&](int quad, float r) {
+    const int row = quad * 4 + r4;
+    if (lane < 4 * B && row < a.rows)
+      a.y[(size_t)ul * a.rows + row] = X == kQ4I8 ? r : r * 0x1p24f;
+  };
+
+  // the loads of the loop are one sequence without branches, so every wait
+  // counts exactly the ones behind it; only the arithmetic is skipped past the
+  // last step
+  for (int j = 0; j < items; j += kQ4Ring) {
+#pragma unroll
+    for (int d = 0; d < kQ4Ring; ++d) {
+      if (j + d < items) {
+        multiply(ring[d]);
+        ct += S;
+        if (ct >= steps) {
+          if (S == 1) store(cq, total());
+          ct = ks, cq += qstride;
+        }
+      }
+      load(ring[d]);
+    }
+  }
+  if (S > 1) {
+    const float r = total();
+    if (lane < 4 * B) join[wv * (4 * B) + lane] = r;
+    __syncthreads();
+    if (ks == 0 && mine && lane < 4 * B) {
+      float sum = r;
+      for (int k = 1; k < S; ++k) sum += join[(wv + k) * (4 * B) + lane];
+      store(q0, sum);
+    }
+  }
+}
+
+// Waves that share a quad, waves per workgroup and workgroups.  The chip holds
+// 16 waves per CU of this kernel: S is the largest power of two that still
+// lets every quad start at once and leaves each wave a step.
+struct Q4Shape {
+  int S, waves, wgs;
+};
+Q4Shape q4_shape(int rows, int steps, int cus) {
+  const long long quads = ((long long)rows + 3) / 4, capacity = (long long)cus * kQ4Waves;
+  Q4Shape h;
+  h.S = 1;
+  while (h.S < kQ4Waves && h.S * 2 <= steps && quads * h.S * 2 <= capacity) h.S *= 2;
+  h.waves = kQ4Waves;
+  while (h.waves > h.S && h.waves > 1 && quads * h.S < (long long)cus * h.waves) h.waves /= 2;
+  const long long slots = h.waves / h.S, need = (quads + slots - 1) / slots;
+  h.wgs = (int)(h.S > 1 || need < cus ? need : cus);
+  return h;
+}
+
+template <int B, int X, bool Z>
+int launch_q4_one(const Q4Args& a, hipStream_t st) {
+  const int steps = (a.nunits + kStepUnits - 1) / kStepUnits;
+  const size_t lds = q4_lds_bytes(B, X, steps);
+  if (lds > device_lds_bytes()) return LVQ_E_SHAPE;
+  const Q4Shape h = q4_shape(a.rows, steps, device_cus());
+  clear_hip_error();
+  hipLaunchKernelGGL((q4_gemv_kernel<B, X, Z>), dim3(h.wgs), dim3(h.waves * kWave), lds, st, a,
+                     steps, h.S);
+  return launch_status();
 }
 
 template <int B, int X>
-__global__ void __launch_bounds__(256) q4_gemv_kernel(Q4Args a) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= a.rows) return;
-  float acc[B];
-  for (int bb = 0; bb < B; ++bb) acc[bb] = 0.f;
-  for (int u = lane; u < a.nunits; u += kWave) {
-    const uint4 w = ((const uint4*)a.codes)[(size_t)row * a.nunits + u];
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-    const size_t g = (size_t)row * a.groups + (u >> a.gshift);
-    const float s = f16_to_f32(a.scale[g]);
-    const float z = a.zero ? f16_to_f32(a.zero[g]) : 8.f;
-    float t[B];
-    for (int bb = 0; bb < B; ++bb) t[bb] = 0.f;
-    for (int n = 0; n < 32; ++n) {
-      const int c = u * 32 + n;
-      if (c >= a.cols) break;
-      const float q = (float)((ww[n >> 3] >> (4 * (n & 7))) & 15u) - z;
-      for (int bb = 0; bb < B; ++bb) {
-        const size_t i = (size_t)bb * a.cols + c;
-        float xv;
-        if (X == kQ4F16) xv = f16_to_f32(((const uint16_t*)a.x)[i]);
-        else if (X == kQ4I8) xv = (float)((const int8_t*)a.x)[i];
-        else xv = __builtin_amdgcn_cvt_f32_fp8(((const uint8_t*)a.x)[i], 0);
-        t[bb] += q * xv;
-      }
-    }
-    for (int bb = 0; bb < B; ++bb) {
-      float sx = s;
-      if (X != kQ4F16) sx *= a.xscale[(size_t)bb * a.xgroups + (u >> a.xshift)];
-      acc[bb] += sx * t[bb];
-    }
-  }
-  for (int bb = 0; bb < B; ++bb) {
-    const float tot = wave_sum_lane63(acc[bb]);
-    if (lane == kWave - 1) a.y[(size_t)bb * a.rows + row] = tot;
-  }
+int launch_q4_batch(const Q4Args& a, hipStream_t st) {
+  return a.zero ? launch_q4_one<B, X, true>(a, st) : launch_q4_one<B, X, false>(a, st);
 }
 
 template <int X>
 int launch_q4(const Q4Args& a, int batch, hipStream_t st) {
-  const dim3 grid((unsigned)((a.rows + 3) / 4)), block(256);
-  clear_hip_error();
   switch (batch) {
-    case 1: hipLaunchKernelGGL((q4_gemv_kernel<1, X>), grid, block, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((q4_gemv_kernel<2, X>), grid, block, 0, st, a); break;
-    case 3: hipLaunchKernelGGL((q4_gemv_kernel<3, X>), grid, block, 0, st, a); break;
-    default: hipLaunchKernelGGL((q4_gemv_kernel<4, X>), grid, block, 0, st, a); break;
+    case 1: return launch_q4_batch<1, X>(a, st);
+    case 2: return launch_q4_batch<2, X>(a, st);
+    case 3: return launch_q4_batch<3, X>(a, st);
+    default: return launch_q4_batch<4, X>(a, st);
   }
-  return launch_status();
 }
 
 // The checks both entry points make, and the launch.
