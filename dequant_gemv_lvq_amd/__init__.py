@@ -383,47 +383,63 @@ def fp16_gemv(w, rows: int, cols: int, x, y, batch: int = 1, stream=None):
 
 try:
     import torch as _torch
+    _Tensor = _torch.Tensor
     _TYPES = {_torch.float32: LVQ_F32, _torch.float16: LVQ_F16, _torch.bfloat16: LVQ_BF16,
               _torch.int8: LVQ_I8, _torch.float8_e4m3fn: LVQ_E4M3}
     # fp16 bit patterns are also accepted as 16-bit integers, codes as any bytes
-    _F16_BITS = (_torch.float16, _torch.int16, getattr(_torch, "uint16", None))
-    _BYTES = (_torch.uint8, _torch.int8, _torch.int32, getattr(_torch, "uint32", None))
+    _F16_BITS = (_torch.float16, _torch.int16, _torch.uint16)
+    _BYTES = (_torch.uint8, _torch.int8, _torch.int32, _torch.uint32)
     _F32 = (_torch.float32,)
     _FLOATS = (_torch.float32, _torch.float16, _torch.bfloat16)
     _EIGHT = (_torch.int8, _torch.float8_e4m3fn)
     _OUTS = (_torch.float16,) + _EIGHT
-except ImportError:  # raw addresses only
+except ImportError:  # the functions below that read a type from a tensor need it
     _torch = None
+
+    class _Tensor:
+        pass
     _TYPES = {}
     _F16_BITS = _BYTES = _F32 = _FLOATS = _EIGHT = _OUTS = ()
 
 
-def _tensor(t, name, types):
-    """Address of a torch tensor on the current device, of one of `types`."""
-    if not hasattr(t, "data_ptr"):
+def _here(stream):
+    """(current device, stream) of a call; stream None is torch's current one.
+    Without a GPU: a device that no tensor is on."""
+    try:
+        # torch's own bindings: current_stream() would cost as much as the launch
+        dev = _torch._C._cuda_getDevice()
+        if stream is None:
+            return dev, _torch._C._cuda_getCurrentRawStream(dev)
+    except Exception:
+        dev = -2
+    return dev, _stream(stream)
+
+
+def _refuse(t, name, types, nbytes, dev):
+    if not isinstance(t, _Tensor):
         raise TypeError("%s must be a tensor on the GPU" % name)
     if not t.is_cuda:
         raise ValueError("%s must be on the GPU" % name)
-    if t.get_device() != _torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError("%s is on another device than the current one" % name)
     if t.dtype not in types:
         raise ValueError("%s has type %s" % (name, t.dtype))
-    return t.data_ptr()
-
-
-def _array(t, name, types, nbytes: int):
-    """Address of a contiguous tensor of at least nbytes bytes (checked, so that
-    the kernel never reads or writes past it), of an int (a raw address, not
-    checked) or of None."""
-    if t is None or isinstance(t, int):
-        return t
-    p = _tensor(t, name, types)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if t.numel() * t.element_size() < nbytes:
-        raise LvqError(LVQ_E_SHAPE, "%s: %s holds %d of %d bytes" % (
-            strerror(LVQ_E_SHAPE), name, t.numel() * t.element_size(), nbytes))
-    return p
+    raise LvqError(LVQ_E_SHAPE, "%s: %s holds %d of %d bytes" % (
+        strerror(LVQ_E_SHAPE), name, t.nbytes, nbytes))
+
+
+def _array(t, name, types, nbytes, dev):
+    """Address of a contiguous tensor of one of `types`, on device dev, of at
+    least nbytes bytes (checked, so that the kernel never reads or writes past
+    it), of an int (a raw address, not checked) or of None."""
+    if t is None or t.__class__ is int:
+        return t
+    if (not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype not in types
+            or not t.is_contiguous() or t.nbytes < nbytes):
+        _refuse(t, name, types, nbytes, dev)
+    return t.data_ptr()
 
 
 def _n_groups(cols: int, group: int) -> int:
@@ -435,12 +451,15 @@ def q4_gemv(codes, scale, zero, group: int, rows: int, cols: int, x, y, batch: i
     """y = W x, W 4-bit codes with a scale (and a zero, or None for 8) per group
     of columns (32, 64, 128, 256, or 0: one per row); x fp16, y fp32."""
     group, rows, cols, batch = int(group), int(rows), int(cols), int(batch)
+    dev, stream = _here(stream)
     meta = rows * _n_groups(cols, group) * 2
-    _check(_lib.q4_gemv(_array(codes, "codes", _BYTES, rows * (-(-cols // 32) * 16)),
-                        _array(scale, "scale", _F16_BITS, meta),
-                        _array(zero, "zero", _F16_BITS, meta), group, rows, cols,
-                        _array(x, "x", _F16_BITS, batch * cols * 2),
-                        _array(y, "y", _F32, batch * rows * 4), batch, _stream(stream)))
+    e = _lib.q4_gemv(_array(codes, "codes", _BYTES, rows * (-(-cols // 32) * 16), dev),
+                     _array(scale, "scale", _F16_BITS, meta, dev),
+                     _array(zero, "zero", _F16_BITS, meta, dev), group, rows, cols,
+                     _array(x, "x", _F16_BITS, batch * cols * 2, dev),
+                     _array(y, "y", _F32, batch * rows * 4, dev), batch, stream)
+    if e:
+        _check(e)
 
 
 def q4_gemv_q8(codes, scale, zero, group: int, rows: int, cols: int, x, x_scale, x_group: int, y,
@@ -449,34 +468,40 @@ def q4_gemv_q8(codes, scale, zero, group: int, rows: int, cols: int, x, x_scale,
     scales, one per x_group columns of a batch row (0: one per batch row)."""
     group, rows, cols, batch = int(group), int(rows), int(cols), int(batch)
     x_group = int(x_group)
+    dev, stream = _here(stream)
+    if not isinstance(x, _Tensor):  # its type says how to read it: no raw address
+        _refuse(x, "x", _EIGHT, 0, dev)
     meta = rows * _n_groups(cols, group) * 2
-    _tensor(x, "x", _EIGHT)  # its type says how to read it: no raw address
-    _check(_lib.q4_gemv_q8(_array(codes, "codes", _BYTES, rows * (-(-cols // 32) * 16)),
-                           _array(scale, "scale", _F16_BITS, meta),
-                           _array(zero, "zero", _F16_BITS, meta), group, rows, cols,
-                           _array(x, "x", _EIGHT, batch * cols), _TYPES[x.dtype],
-                           _array(x_scale, "x_scale", _F32, batch * _n_groups(cols, x_group) * 4),
-                           x_group, _array(y, "y", _F32, batch * rows * 4), batch,
-                           _stream(stream)))
+    xp = _array(x, "x", _EIGHT, batch * cols, dev)
+    e = _lib.q4_gemv_q8(_array(codes, "codes", _BYTES, rows * (-(-cols // 32) * 16), dev),
+                        _array(scale, "scale", _F16_BITS, meta, dev),
+                        _array(zero, "zero", _F16_BITS, meta, dev), group, rows, cols, xp,
+                        _TYPES[x.dtype],
+                        _array(x_scale, "x_scale", _F32, batch * _n_groups(cols, x_group) * 4,
+                               dev),
+                        x_group, _array(y, "y", _F32, batch * rows * 4, dev), batch, stream)
+    if e:
+        _check(e)
 
 
-def _rows_of(t, name):
+def _rows_of(t, name, dev):
     """(address, type, rows, cols, row stride) of a 2-D tensor of floats whose
     columns are adjacent."""
-    p = _tensor(t, name, _FLOATS)
+    if not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype not in _FLOATS:
+        _refuse(t, name, _FLOATS, 0, dev)
     if t.dim() != 2:
         raise ValueError("%s must have two dimensions, rows and columns" % name)
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    (rows, cols), (stride, one) = t.shape, t.stride()
+    if cols > 1 and one != 1:
         raise ValueError("%s must have adjacent columns" % name)
-    return p, _TYPES[t.dtype], rows, cols, t.stride(0) if rows > 1 else cols
+    return t.data_ptr(), _TYPES[t.dtype], rows, cols, stride if rows > 1 else cols
 
 
-def _out_of(out, scale, group, rows, cols):
-    op = _tensor(out, "out", _OUTS)
-    _array(out, "out", _OUTS, rows * cols * out.element_size())
-    return op, _TYPES[out.dtype], _array(scale, "scale", _F32,
-                                         rows * _n_groups(cols, group) * 4)
+def _typed(t, name, types, count, dev):
+    """(address, type) of a contiguous tensor of count values."""
+    if not isinstance(t, _Tensor):
+        _refuse(t, name, types, 0, dev)
+    return _array(t, name, types, count * t.itemsize, dev), _TYPES.get(t.dtype)
 
 
 def rms_norm(x, residual, weight, eps: float, out, residual_out=None, scale=None, group: int = 0,
@@ -488,22 +513,28 @@ def rms_norm(x, residual, weight, eps: float, out, residual_out=None, scale=None
     residual_out may be None.  out: fp16, or int8 / float8_e4m3fn with scale, one
     fp32 per `group` columns of a row (32, 64, 128, 256, or 0: one per row)."""
     group = int(group)
-    xp, xt, rows, cols, stride = _rows_of(x, "x")
-    rt = LVQ_F32
-    for t in (residual, residual_out):
-        if t is not None:
-            _array(t, "residual", _FLOATS, rows * cols * t.element_size())
-            rt = _TYPES[t.dtype]
-    if residual is not None and residual_out is not None and residual.dtype != residual_out.dtype:
-        raise ValueError("residual and residual_out must have the same type")
-    wp = wt = 0
+    dev, stream = _here(stream)
+    xp, xt, rows, cols, stride = _rows_of(x, "x", dev)
+    n = rows * cols
+    rp = rop = wp = None
+    rt = wt = LVQ_F32
+    if residual is not None:
+        rp, rt = _typed(residual, "residual", _FLOATS, n, dev)
+    if residual_out is residual:
+        rop = rp
+    elif residual_out is not None:
+        rop, rot = _typed(residual_out, "residual_out", _FLOATS, n, dev)
+        if residual is not None and rot != rt:
+            raise ValueError("residual and residual_out must have the same type")
+        rt = rot
     if weight is not None:
-        wp = _array(weight, "weight", _FLOATS, cols * weight.element_size())
-        wt = _TYPES[weight.dtype]
-    op, ot, sp = _out_of(out, scale, group, rows, cols)
-    _check(_lib.lvq_rms_norm(xp, xt, stride, None if residual is None else residual.data_ptr(), rt,
-                             None if residual_out is None else residual_out.data_ptr(), wp or None,
-                             wt, float(eps), rows, cols, op, ot, sp, group, _stream(stream)))
+        wp, wt = _typed(weight, "weight", _FLOATS, cols, dev)
+    op, ot = _typed(out, "out", _OUTS, n, dev)
+    e = _lib.lvq_rms_norm(xp, xt, stride, rp, rt, rop, wp, wt, eps, rows, cols, op, ot,
+                          _array(scale, "scale", _F32, rows * _n_groups(cols, group) * 4, dev),
+                          group, stream)
+    if e:
+        _check(e)
 
 
 def silu_mul(gate, up, out, scale=None, group: int = 0, stream=None):
@@ -511,13 +542,17 @@ def silu_mul(gate, up, out, scale=None, group: int = 0, stream=None):
     (fp32, fp16 or bf16), shape and row stride (for instance the halves of one
     product's output); out, scale and group as in rms_norm()."""
     group = int(group)
-    gp, gt, rows, cols, stride = _rows_of(gate, "gate")
-    up_p, ut, urows, ucols, ustride = _rows_of(up, "up")
-    if (ut, urows, ucols, ustride) != (gt, rows, cols, stride):
+    dev, stream = _here(stream)
+    gp, gt, rows, cols, stride = _rows_of(gate, "gate", dev)
+    up_p, ut, urows, ucols, ustride = _rows_of(up, "up", dev)
+    if ut != gt or urows != rows or ucols != cols or ustride != stride:
         raise ValueError("gate and up must have the same type, shape and row stride")
-    op, ot, sp = _out_of(out, scale, group, rows, cols)
-    _check(_lib.lvq_silu_mul(gp, up_p, gt, stride, rows, cols, op, ot, sp, group,
-                             _stream(stream)))
+    op, ot = _typed(out, "out", _OUTS, rows * cols, dev)
+    e = _lib.lvq_silu_mul(gp, up_p, gt, stride, rows, cols, op, ot,
+                          _array(scale, "scale", _F32, rows * _n_groups(cols, group) * 4, dev),
+                          group, stream)
+    if e:
+        _check(e)
 
 
 def rotate(x, n: int, m: int, sign_words, q, y, batch: int = 1, stream=None):
