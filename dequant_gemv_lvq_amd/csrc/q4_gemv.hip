@@ -51,6 +51,10 @@ struct Q4Args {
   const float* xscale;
   int xshift, xgroups;
   float* y;
+  int batch;
+  // the launch: steps of 16 units per row, quads per workgroup (one more in the
+  // first `extra`), log2 of the waves
+  int steps, quads, extra, wave_shift;
 };
 
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
@@ -60,16 +64,15 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef float float2_t __attribute__((ext_vector_type(2)));
 
-constexpr int kQ4Ring = 6;     // steps in flight per wave
 constexpr int kQ4Waves = 16;   // waves per workgroup at most
 constexpr int kStepUnits = 16; // units of 32 columns per step
-constexpr int kXAhead = 4;     // x chunks a wave requests at a time
+constexpr int kChunk = 4;      // steps a wave loads at a time
+constexpr int kXAhead = 4;     // pieces of x a wave requests at a time
 
 // LDS: x, then per unit and batch row the sum of x (f16), or x's scale and its
-// product with that sum, then a wave's partial results.
-constexpr int sum_stride(int B) { return B == 3 ? 4 : B; }
+// product with that sum, then a partial result per wave.
 constexpr size_t x_step_bytes(int B, int X) { return (X == kQ4I8 ? 512 : 1024) * (size_t)B; }
-constexpr size_t sum_step_bytes(int B) { return kStepUnits * (size_t)sum_stride(B) * 4; }
+constexpr size_t sum_step_bytes(int B) { return kStepUnits * (size_t)B * 4; }
 inline size_t q4_lds_bytes(int B, int X, int steps) {
   return steps * (x_step_bytes(B, X) + sum_step_bytes(B) * (X == kQ4F16 ? 1 : 2)) +
          kQ4Waves * 4 * (size_t)B * 4;
@@ -152,13 +155,13 @@ __device__ __forceinline__ void put_x8(const Q4Args& a, uint8_t* xs, float* sums
   }
   sum = dpp_add<0x4E, 0xF>(dpp_add<0xB1, 0xF>(sum));  // the quad's four words
   if (w == 0) {
-    const int u = t * kStepUnits + ul, at = u * sum_stride(B) + bb;
+    const int u = t * kStepUnits + ul, at = u * B + bb;
     if constexpr (X != kQ4I8) sum *= 0x1p-24f;  // the scale of the subnormal codes
     if constexpr (X == kQ4F16) {
       sums[at] = sum;
     } else {
       const float s =
-          u < a.nunits ? a.xscale[(size_t)bb * a.xgroups + (u >> a.xshift)] : 0.f;
+          u < a.nunits && bb < a.batch ? a.xscale[(size_t)bb * a.xgroups + (u >> a.xshift)] : 0.f;
       scaled[at] = s;
       sums[at] = s * sum;
     }
@@ -182,18 +185,24 @@ __device__ __forceinline__ float sum_blocks(float v) {
   return __builtin_bit_cast(float, (uint32_t)q[0]) + __builtin_bit_cast(float, (uint32_t)q[1]);
 }
 
-template <bool Z>
-struct Q4Step {  // one step of a wave: a lane's 32 codes, its scale and zero
-  u32x4_t w;
-  uint16_t s, z;
+// What a wave has in flight: four steps of codes and the scales (low half) and
+// zeros (high half) of their groups, NS registers of them: 4 / NS steps share
+// one, lane 4 k + r holding the k-th of up to 16 groups of row r.
+template <int NS>
+struct Q4Chunk {
+  u32x4_t w[kChunk];
+  uint16_t s[NS], z[NS];
 };
 
-// S waves of a workgroup share a quad of rows: wave ks of them takes the steps
-// ks, ks + S, ...  Quads go round the workgroups, so a last, partly filled
-// round is spread over all of them.  With S > 1 there is one round.
-template <int B, int X, bool Z>
-__global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a, int steps, int S) {
+// A workgroup takes a run of quads of rows; their steps, one after another, are
+// dealt to its waves in equal contiguous parts.  A quad whose steps lie in more
+// than one wave is joined in LDS at the end, in order, by the wave that holds
+// its first step.  RING: chunks of four steps in flight per wave, 1 where no
+// wave has more than one.
+template <int B, int X, int NS, int RING>
+__global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int steps = a.steps;
   uint8_t* xs = smem;
   float* sums = (float*)(smem + steps * x_step_bytes(B, X));
   float* scaled = sums + steps * (sum_step_bytes(B) / 4);
@@ -201,99 +210,113 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a, int
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nw = blockDim.x / kWave;
-  const int quads = (a.rows + 3) / 4;
-  const int slots = nw / S, ks = wv % S;
-  const int q0 = (wv / S) * gridDim.x + blockIdx.x, qstride = slots * gridDim.x;
-  const int per = (steps - ks + S - 1) / S;  // this wave's steps of a quad
-  const int mine = q0 < quads ? (quads - 1 - q0) / qstride + 1 : 0;
-  const int items = mine * per;
+  const int nw = 1 << a.wave_shift;
 
-  // 1. the ring of steps: one sequence of loads without a branch, those past
-  //    the wave's last aimed at an empty buffer
-  Q4Step<Z> ring[kQ4Ring];
-  int lq = q0, lt = ks, left = items;  // the next step to load
-  const int ul = lane >> 2, r4 = lane & 3;
-  const int row_bytes = a.nunits * 16;
-  const int lane_off = r4 * row_bytes + ul * 16;
-  auto load = [&](Q4Step<Z>& st) {
-    const int row = lq * 4;
-    const uint32_t n = left > 0 ? (uint32_t)(a.rows - row < 4 ? a.rows - row : 4) : 0u;
-    const size_t qrow = left > 0 ? (size_t)row : 0;
-    const int u = lt * kStepUnits + ul;
-    // a unit past the row's end: an offset past every buffer, by the sign bit
-    // of the difference (a select becomes a branch around the load)
-    const int past = (a.nunits - 1 - u) & (int)0x80000000;
-    st.w = __builtin_bit_cast(
-        u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                     q4_rsrc(a.codes + qrow * row_bytes, n * row_bytes), lane_off | past,
-                     lt * (kStepUnits * 16), 2));
-    const int moff = ((r4 * a.groups + (u >> a.gshift)) * 2) | past;
-    st.s = __builtin_amdgcn_raw_buffer_load_b16(
-        q4_rsrc(a.scale + qrow * a.groups, n * a.groups * 2), moff, 0, 0);
-    if constexpr (Z)
-      st.z = __builtin_amdgcn_raw_buffer_load_b16(
-          q4_rsrc(a.zero + qrow * a.groups, n * a.groups * 2), moff, 0, 0);
-    --left;
-    lt += S;
-    if (lt >= steps) lt = ks, lq += qstride;
-  };
-
-  // 2. x: each wave takes chunks of 64 x 8 columns (one step of one batch row),
-  //    kXAhead requested at a time; the ring's first loads go out behind the
+  // 1. x: each wave takes pieces of 64 x 8 columns (one step of one batch row),
+  //    kXAhead requested at a time; the weights' first loads go out behind the
   //    last of them, so the wait for x does not include the weights
-  const int chunks = B * steps;
+  const int pieces = B * steps;  // of batch rows past the batch: zeros
   u32x4_t xv[kXAhead];
-  // chunk i is step i - bb steps of batch row bb; past the last, nothing
   auto row_of = [&](int i) {
     int bb = 0;
 #pragma unroll
     for (int k = 1; k < B; ++k) bb += i >= k * steps;
     return bb;
   };
-  auto load_chunks = [&](int i0, auto vec) {
+  auto load_x = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < kXAhead; ++k) {
       const int i = i0 + k * nw, bb = row_of(i), t = i - bb * steps;
       constexpr int E = X == kQ4F16 ? 2 : 1;
-      const auto rx = q4_rsrc((const uint8_t*)a.x + (size_t)bb * a.cols * E,
-                              i < chunks ? a.cols * E : 0);
-      xv[k] = load_x8<X, decltype(vec)::value>(rx, (t * 64 + lane) * 8);
+      if (i < pieces) {
+        const auto rx = q4_rsrc((const uint8_t*)a.x + (size_t)bb * a.cols * E,
+                                bb < a.batch ? a.cols * E : 0);
+        if (a.cols % 8 == 0) xv[k] = load_x8<X, true>(rx, (t * 64 + lane) * 8);
+        else xv[k] = load_x8<X, false>(rx, (t * 64 + lane) * 8);
+      }
     }
   };
-  auto put_chunks = [&](int i0) {
+  auto put_x = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < kXAhead; ++k) {
       const int i = i0 + k * nw, bb = row_of(i);
-      if (i < chunks) put_x8<B, X>(a, xs, sums, scaled, xv[k], bb, i - bb * steps, lane);
+      if (i < pieces) put_x8<B, X>(a, xs, sums, scaled, xv[k], bb, i - bb * steps, lane);
     }
   };
-  auto load_any = [&](int i0) {
-    if (a.cols % 8 == 0) load_chunks(i0, std::true_type{});
-    else load_chunks(i0, std::false_type{});
-  };
   int i0 = wv;
-  load_any(i0);
-  for (; i0 + kXAhead * nw < chunks; i0 += kXAhead * nw) {
-    put_chunks(i0);
-    load_any(i0 + kXAhead * nw);
+  load_x(i0);
+  for (; i0 + kXAhead * nw < pieces; i0 += kXAhead * nw) {
+    put_x(i0);
+    load_x(i0 + kXAhead * nw);
   }
+
+  // 2. this wave's steps: [first, last) of the workgroup's, from step ct of quad cq
+  const int wg = blockIdx.x;
+  const int quad0 = wg * a.quads + (wg < a.extra ? wg : a.extra);
+  const int total_steps = (a.quads + (wg < a.extra)) * steps;
+  const int per = (total_steps + nw - 1) >> a.wave_shift;
+  const int first = wv * per < total_steps ? wv * per : total_steps;
+  const int last = first + per < total_steps ? first + per : total_steps;
+  const int skip = first / steps;
+  int cq = quad0 + skip, ct = first - skip * steps, left = last - first;
+  int lq = cq, lt = ct, lleft = left;  // where the loads are
+
+  const int ul = lane >> 2, r4 = lane & 3;
+  const int row_bytes = a.nunits * 16;
+  const int lane_off = r4 * row_bytes + ul * 16;
+  auto steps_in_chunk = [&](int t, int rest) {
+    const int n = steps - t < rest ? steps - t : rest;
+    return n < kChunk ? n : kChunk;
+  };
+  auto load = [&](Q4Chunk<NS>& c) {
+    const int n = steps_in_chunk(lt, lleft);
+    const int row = lq * 4, rows = a.rows - row < 4 ? a.rows - row : 4;
+    // the step's offset sits in the base, so that the range check is exact; a
+    // row's last step may run into the next row, against zeros of x
+    const uint8_t* base = a.codes + (size_t)row * row_bytes + lt * (kStepUnits * 16);
+    const uint32_t bytes = rows * row_bytes - lt * (kStepUnits * 16);
 #pragma unroll
-  for (int d = 0; d < kQ4Ring; ++d) load(ring[d]);
-  put_chunks(i0);
+    for (int i = 0; i < kChunk; ++i)
+      c.w[i] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(q4_rsrc(base, i < n ? bytes : 0),
+                                                         lane_off, i * (kStepUnits * 16), 2));
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      const int t = lt + k * (kChunk / NS);
+      const int g = ((t * kStepUnits) >> a.gshift) + ul;
+      // a group past the row's end: an offset past every buffer, by the sign
+      // bit of the difference (a select becomes a branch around the load)
+      const int off =
+          ((r4 * a.groups + g) * 2) | ((a.groups - 1 - g) & (int)0x80000000);
+      const uint32_t n2 = k * (kChunk / NS) < n ? (uint32_t)(rows * a.groups) * 2 : 0;
+      c.s[k] = __builtin_amdgcn_raw_buffer_load_b16(
+          q4_rsrc(a.scale + (size_t)row * a.groups, n2), off, 0, 0);
+      c.z[k] = __builtin_amdgcn_raw_buffer_load_b16(
+          q4_rsrc(a.zero + (size_t)row * a.groups, a.zero ? n2 : 0), off, 0, 0);
+    }
+    lt += n, lleft -= n;
+    if (lt == steps) lt = 0, ++lq;
+  };
+  Q4Chunk<NS> ring[RING];
+#pragma unroll
+  for (int d = 0; d < RING; ++d) load(ring[d]);
+  put_x(i0);
   __syncthreads();
 
   // 3. the steps
   const uint8_t* xl = xs + (ul * B + (r4 < B ? r4 : 0)) * 16;
-  const float* sl = sums + ul * sum_stride(B);
-  const float* tl = scaled + ul * sum_stride(B);
+  const float* sl = sums + ul * B;
+  const float* tl = scaled + ul * B;
+  // lane of a chunk's scale register that holds this lane's group, step 0, and
+  // what a step adds (bytes of a lane index)
+  const int from = (((ul >> a.gshift) << 2) | r4) << 2;
+  const int from_step = (kStepUnits >> a.gshift) << 4;
   float acc[B];
 #pragma unroll
   for (int bb = 0; bb < B; ++bb) acc[bb] = 0.f;
-  int cq = q0, ct = ks;  // the step being multiplied
 
-  auto multiply = [&](const Q4Step<Z>& st) {
-    const uint8_t* xt = xl + (size_t)ct * x_step_bytes(B, X);
+  auto multiply = [&](u32x4_t q, uint32_t sz, int t) {
+    const uint8_t* xt = xl + (size_t)t * x_step_bytes(B, X);
     float v[B];
     if constexpr (X == kQ4I8) {
       int4_t c = {0, 0, 0, 0};
@@ -302,7 +325,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a, int
         const u32x4_t x = *(const u32x4_t*)(xt + h * 256 * B);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const uint32_t w = st.w[2 * h + k];
+          const uint32_t w = q[2 * h + k];
           c = __builtin_amdgcn_mfma_i32_4x4x4i8((int)x[2 * k], (int)(w & 0x0F0F0F0Fu), c, 0, 0, 0);
           c = __builtin_amdgcn_mfma_i32_4x4x4i8((int)x[2 * k + 1], (int)((w >> 4) & 0x0F0F0F0Fu), c,
                                                 0, 0, 0);
@@ -315,7 +338,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a, int
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const u32x4_t x = *(const u32x4_t*)(xt + k * 256 * B);
-        const uint32_t w = st.w[k], w8 = w >> 8;
+        const uint32_t w = q[k], w8 = w >> 8;
         lo = __builtin_amdgcn_mfma_f32_4x4x4f16(
             __builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}),
             __builtin_bit_cast(half4_t, u32x2_t{w & 0x000F000Fu, w8 & 0x000F000Fu}), lo, 0, 0, 0);
@@ -326,10 +349,9 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a, int
 #pragma unroll
       for (int bb = 0; bb < B; ++bb) v[bb] = __builtin_fmaf(hi[bb], 0.0625f, lo[bb]);
     }
-    const float s = f16_to_f32(st.s);
-    const float z = Z ? f16_to_f32(st.z) : 8.f;
-    const float* sx = sl + ct * (kStepUnits * sum_stride(B));
-    const float* tx = tl + ct * (kStepUnits * sum_stride(B));
+    const float s = f16_to_f32(sz), z = f16_to_f32(sz >> 16);
+    const float* sx = sl + t * (kStepUnits * B);
+    const float* tx = tl + t * (kStepUnits * B);
 #pragma unroll
     for (int bb = 0; bb < B; ++bb) {
       if constexpr (X != kQ4F16) v[bb] *= tx[bb];
@@ -349,82 +371,116 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a, int
   };
   auto store = [&](int quad, float r) {
     const int row = quad * 4 + r4;
-    if (lane < 4 * B && row < a.rows)
+    if (ul < a.batch && row < a.rows)
       a.y[(size_t)ul * a.rows + row] = X == kQ4I8 ? r : r * 0x1p24f;
   };
 
-  // the loads of the loop are one sequence without branches, so every wait
-  // counts exactly the ones behind it; only the arithmetic is skipped past the
-  // last step
-  for (int j = 0; j < items; j += kQ4Ring) {
+  float own = 0.f;  // of a quad that starts in this wave and ends in a later one
+  int own_end = 0;  // its end among the workgroup's steps; 0: none
+  bool head = ct != 0;  // this piece of a quad continues an earlier wave's
+  auto consume = [&](const Q4Chunk<NS>& c) {
+    const int n = steps_in_chunk(ct, left);
 #pragma unroll
-    for (int d = 0; d < kQ4Ring; ++d) {
-      if (j + d < items) {
-        multiply(ring[d]);
-        ct += S;
-        if (ct >= steps) {
-          if (S == 1) store(cq, total());
-          ct = ks, cq += qstride;
-        }
+    for (int i = 0; i < kChunk; ++i) {
+      constexpr int SPL = kChunk / NS;
+      if (i < n) {
+        const uint32_t zero = a.zero ? (uint32_t)c.z[i / SPL] : 0x4800u;  // 8.0
+        uint32_t sz = (uint32_t)c.s[i / SPL] | zero << 16;
+        if constexpr (NS < kChunk)
+          sz = (uint32_t)__builtin_amdgcn_ds_bpermute(from + (i % SPL) * from_step, (int)sz);
+        multiply(c.w[i], sz, ct + i);
       }
-      load(ring[d]);
     }
+    ct += n, left -= n;
+    if (ct == steps || left == 0) {  // the end of a quad, or of this wave's part
+      const float r = total();
+      if (head) {
+        if (lane < 4 * B) join[wv * (4 * B) + lane] = r;
+      } else if (ct == steps) {
+        store(cq, r);
+      } else {
+        own = r, own_end = (cq - quad0 + 1) * steps;
+      }
+      if (ct == steps) ct = 0, ++cq;
+      head = false;
+    }
+  };
+  if constexpr (RING == 1) {
+    if (left > 0) consume(ring[0]);
+  } else {
+    while (lleft > 0) {  // the ring is full, and a load follows each chunk
+      consume(ring[0]);
+      load(ring[0]);
+      consume(ring[1]);
+      load(ring[1]);
+    }
+    if (left > 0) consume(ring[0]);
+    if (left > 0) consume(ring[1]);
   }
-  if (S > 1) {
-    const float r = total();
-    if (lane < 4 * B) join[wv * (4 * B) + lane] = r;
+  if (per % steps) {  // the same in every wave: some quad lies in several
     __syncthreads();
-    if (ks == 0 && mine && lane < 4 * B) {
-      float sum = r;
-      for (int k = 1; k < S; ++k) sum += join[(wv + k) * (4 * B) + lane];
-      store(q0, sum);
+    if (own_end) {
+      for (int v = wv + 1; v * per < own_end; ++v)
+        if (lane < 4 * B) own += join[v * (4 * B) + lane];
+      store(own_end / steps - 1 + quad0, own);
     }
   }
 }
 
-// Waves that share a quad, waves per workgroup and workgroups.  The chip holds
-// 16 waves per CU of this kernel: S is the largest power of two that still
-// lets every quad start at once and leaves each wave a step.
-struct Q4Shape {
-  int S, waves, wgs;
-};
-Q4Shape q4_shape(int rows, int steps, int cus) {
-  const long long quads = ((long long)rows + 3) / 4, capacity = (long long)cus * kQ4Waves;
-  Q4Shape h;
-  h.S = 1;
-  while (h.S < kQ4Waves && h.S * 2 <= steps && quads * h.S * 2 <= capacity) h.S *= 2;
-  h.waves = kQ4Waves;
-  while (h.waves > h.S && h.waves > 1 && quads * h.S < (long long)cus * h.waves) h.waves /= 2;
-  const long long slots = h.waves / h.S, need = (quads + slots - 1) / slots;
-  h.wgs = (int)(h.S > 1 || need < cus ? need : cus);
-  return h;
-}
-
-template <int B, int X, bool Z>
-int launch_q4_one(const Q4Args& a, hipStream_t st) {
-  const int steps = (a.nunits + kStepUnits - 1) / kStepUnits;
-  const size_t lds = q4_lds_bytes(B, X, steps);
+template <int B, int X, int NS>
+int launch_q4_ring(Q4Args a, hipStream_t st) {
+  a.steps = (a.nunits + kStepUnits - 1) / kStepUnits;
+  const size_t lds = q4_lds_bytes(B, X, a.steps);
   if (lds > device_lds_bytes()) return LVQ_E_SHAPE;
-  const Q4Shape h = q4_shape(a.rows, steps, device_cus());
+  // One workgroup per CU, the quads dealt evenly; as many waves, up to 16, as
+  // have a chunk of four steps each.
+  const int cus = device_cus();
+  const int quads = (int)(((long long)a.rows + 3) / 4);
+  const int wgs = quads < cus ? quads : cus;
+  a.quads = quads / wgs, a.extra = quads % wgs;
+  const long long most = (long long)(a.quads + (a.extra != 0)) * a.steps;
+  a.wave_shift = 0;
+  while ((1 << a.wave_shift) < kQ4Waves && (long long)kChunk << a.wave_shift < most)
+    ++a.wave_shift;
+  // one chunk per wave: no more than four steps, and none across two quads
+  auto one_chunk = [&](int quads_of_wg) {
+    const long long per = ((long long)quads_of_wg * a.steps + (1 << a.wave_shift) - 1) >> a.wave_shift;
+    return per <= kChunk && (quads_of_wg == 1 || a.steps % per == 0);
+  };
+  const dim3 grid(wgs), block(kWave << a.wave_shift);
   clear_hip_error();
-  hipLaunchKernelGGL((q4_gemv_kernel<B, X, Z>), dim3(h.wgs), dim3(h.waves * kWave), lds, st, a,
-                     steps, h.S);
+  if (one_chunk(a.quads) && (!a.extra || one_chunk(a.quads + 1)))
+    hipLaunchKernelGGL((q4_gemv_kernel<B, X, NS, 1>), grid, block, lds, st, a);
+  else
+    hipLaunchKernelGGL((q4_gemv_kernel<B, X, NS, 2>), grid, block, lds, st, a);
   return launch_status();
 }
 
 template <int B, int X>
 int launch_q4_batch(const Q4Args& a, hipStream_t st) {
-  return a.zero ? launch_q4_one<B, X, true>(a, st) : launch_q4_one<B, X, false>(a, st);
+  return a.gshift == 0   ? launch_q4_ring<B, X, 4>(a, st)
+         : a.gshift == 1 ? launch_q4_ring<B, X, 2>(a, st)
+                         : launch_q4_ring<B, X, 1>(a, st);
 }
 
+// Three batch rows run as four (the fourth zeros) where their x fits in LDS,
+// else as two and one.
 template <int X>
-int launch_q4(const Q4Args& a, int batch, hipStream_t st) {
-  switch (batch) {
-    case 1: return launch_q4_batch<1, X>(a, st);
-    case 2: return launch_q4_batch<2, X>(a, st);
-    case 3: return launch_q4_batch<3, X>(a, st);
-    default: return launch_q4_batch<4, X>(a, st);
+int launch_q4(Q4Args a, hipStream_t st) {
+  const int steps = (a.nunits + kStepUnits - 1) / kStepUnits;
+  if (a.batch == 1) return launch_q4_batch<1, X>(a, st);
+  if (a.batch == 2) return launch_q4_batch<2, X>(a, st);
+  if (a.batch == 3 && q4_lds_bytes(4, X, steps) > device_lds_bytes()) {
+    a.batch = 2;
+    const int e = launch_q4_batch<2, X>(a, st);
+    if (e) return e;
+    a.batch = 1;
+    a.x = (const uint8_t*)a.x + (size_t)2 * a.cols * (X == kQ4F16 ? 2 : 1);
+    if (X != kQ4F16) a.xscale += (size_t)2 * a.xgroups;
+    a.y += (size_t)2 * a.rows;
+    return launch_q4_batch<1, X>(a, st);
   }
+  return launch_q4_batch<4, X>(a, st);
 }
 
 // The checks both entry points make, and the launch.
@@ -455,9 +511,10 @@ int q4_run(const uint8_t* codes, const uint16_t* scale, const uint16_t* zero, in
   a.x = x, a.xscale = x_scale;
   a.xshift = xs, a.xgroups = group_count(cols, x_group);
   a.y = y;
-  if (xkind == kQ4F16) return launch_q4<kQ4F16>(a, batch, st);
-  if (xkind == kQ4I8) return launch_q4<kQ4I8>(a, batch, st);
-  return launch_q4<kQ4E4M3>(a, batch, st);
+  a.batch = batch;
+  if (xkind == kQ4F16) return launch_q4<kQ4F16>(a, st);
+  if (xkind == kQ4I8) return launch_q4<kQ4I8>(a, st);
+  return launch_q4<kQ4E4M3>(a, st);
 }
 
 }  // namespace lvq
