@@ -67,7 +67,7 @@ typedef float float2_t __attribute__((ext_vector_type(2)));
 constexpr int kQ4Waves = 16;   // waves per workgroup at most
 constexpr int kStepUnits = 16; // units of 32 columns per step
 constexpr int kChunk = 4;      // steps a wave loads at a time
-constexpr int kXAhead = 4;     // pieces of x a wave requests at a time
+constexpr int kXAhead = 6;     // pieces of x a wave requests at a time
 
 // LDS: x, then per unit and batch row the sum of x (f16), or x's scale and its
 // product with that sum, then a partial result per wave.
@@ -123,10 +123,10 @@ __device__ __forceinline__ u32x4_t pair_order(u32x4_t d) {
 }
 
 // Eight columns (word w of unit u of step t, batch row bb) into LDS, and, from
-// the quad of lanes that holds a unit, the unit's sums.
+// the quad of lanes that holds a unit, the unit's sums.  s: the scale of the unit.
 template <int B, int X>
 __device__ __forceinline__ void put_x8(const Q4Args& a, uint8_t* xs, float* sums, float* scaled,
-                                       u32x4_t v, int bb, int t, int lane) {
+                                       u32x4_t v, float s, int bb, int t, int lane) {
   const int ul = lane >> 2, w = lane & 3;
   float sum;
   if constexpr (X == kQ4I8) {
@@ -160,8 +160,6 @@ __device__ __forceinline__ void put_x8(const Q4Args& a, uint8_t* xs, float* sums
     if constexpr (X == kQ4F16) {
       sums[at] = sum;
     } else {
-      const float s =
-          u < a.nunits && bb < a.batch ? a.xscale[(size_t)bb * a.xgroups + (u >> a.xshift)] : 0.f;
       scaled[at] = s;
       sums[at] = s * sum;
     }
@@ -194,11 +192,13 @@ struct Q4Chunk {
   uint16_t s[NS], z[NS];
 };
 
-// A workgroup takes a run of quads of rows; their steps, one after another, are
-// dealt to its waves in equal contiguous parts.  A quad whose steps lie in more
-// than one wave is joined in LDS at the end, in order, by the wave that holds
-// its first step.  RING: chunks of four steps in flight per wave, 1 where no
-// wave has more than one.
+// Quads of rows go round the workgroups, and a workgroup's go round its waves,
+// so that the whole chip reads one window of neighbouring rows at a time (with a
+// run of quads per wave, streams a large power of two apart, 131072x4096 took 48
+// instead of 43 us); of the last round, the steps are dealt to the waves in
+// equal contiguous parts.  A quad whose steps lie in more than one wave is
+// joined in LDS at the end, in order, by the wave that holds its first step.
+// RING: chunks of four steps in flight per wave, 1 where no wave has more.
 template <int B, int X, int NS, int RING>
 __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   //    last of them, so the wait for x does not include the weights
   const int pieces = B * steps;  // of batch rows past the batch: zeros
   u32x4_t xv[kXAhead];
+  float xsc[kXAhead];
   auto row_of = [&](int i) {
     int bb = 0;
 #pragma unroll
@@ -233,6 +234,13 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
                                 bb < a.batch ? a.cols * E : 0);
         if (a.cols % 8 == 0) xv[k] = load_x8<X, true>(rx, (t * 64 + lane) * 8);
         else xv[k] = load_x8<X, false>(rx, (t * 64 + lane) * 8);
+        if constexpr (X != kQ4F16) {  // past the last unit: a group past the row's, or x is zero
+          const auto rs = q4_rsrc(a.xscale + (size_t)bb * a.xgroups,
+                                  bb < a.batch ? a.xgroups * 4 : 0);
+          xsc[k] = __builtin_bit_cast(
+              float, __builtin_amdgcn_raw_buffer_load_b32(
+                         rs, ((t * kStepUnits + (lane >> 2)) >> a.xshift) * 4, 0, 0));
+        }
       }
     }
   };
@@ -240,7 +248,8 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
 #pragma unroll
     for (int k = 0; k < kXAhead; ++k) {
       const int i = i0 + k * nw, bb = row_of(i);
-      if (i < pieces) put_x8<B, X>(a, xs, sums, scaled, xv[k], bb, i - bb * steps, lane);
+      if (i < pieces) put_x8<B, X>(a, xs, sums, scaled, xv[k], xsc[k], bb, i - bb * steps,
+                                     lane);
     }
   };
   int i0 = wv;
@@ -250,36 +259,46 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
     load_x(i0 + kXAhead * nw);
   }
 
-  // 2. this wave's steps: [first, last) of the workgroup's, from step ct of quad cq
-  const int wg = blockIdx.x;
-  const int quad0 = wg * a.quads + (wg < a.extra ? wg : a.extra);
-  const int total_steps = (a.quads + (wg < a.extra)) * steps;
-  const int per = (total_steps + nw - 1) >> a.wave_shift;
-  const int first = wv * per < total_steps ? wv * per : total_steps;
-  const int last = first + per < total_steps ? first + per : total_steps;
+  // 2. this wave's steps: whole quads, one in nw of the workgroup's; of the
+  //    fewer than nw that remain, the steps [first, last)
+  const int stride = gridDim.x;
+  const int quads = a.quads + ((int)blockIdx.x < a.extra);
+  const int whole = quads >> a.wave_shift, rest0 = quads - (quads & (nw - 1));
+  const int rest_steps = (quads - rest0) * steps;
+  const int per = (rest_steps + nw - 1) >> a.wave_shift;
+  const int first = wv * per < rest_steps ? wv * per : rest_steps;
+  const int last = first + per < rest_steps ? first + per : rest_steps;
   const int skip = first / steps;
-  int cq = quad0 + skip, ct = first - skip * steps, left = last - first;
-  int lq = cq, lt = ct, lleft = left;  // where the loads are
+  const int q2 = (int)blockIdx.x + (rest0 + skip) * stride, t2 = first - skip * steps;
+  struct Cursor {
+    int quad, t, whole, left;  // whole: whole quads to go, this one included
+  };
+  Cursor at = {(int)blockIdx.x + wv * stride, 0, whole, whole * steps + last - first};
+  if (whole == 0) at.quad = q2, at.t = t2;
+  auto advance = [&](Cursor& c, int n) {  // returns whether a quad ended
+    c.t += n, c.left -= n;
+    if (c.t < steps) return false;
+    --c.whole;
+    c.quad = c.whole > 0 ? c.quad + nw * stride : c.whole == 0 ? q2 : c.quad + stride;
+    c.t = c.whole == 0 ? t2 : 0;
+    return true;
+  };
+  auto steps_in_chunk = [&](const Cursor& c) {
+    const int n = steps - c.t < c.left ? steps - c.t : c.left;
+    return n < kChunk ? n : kChunk;
+  };
+  Cursor ld = at;  // where the loads are
 
   const int ul = lane >> 2, r4 = lane & 3;
   const int row_bytes = a.nunits * 16;
   const int lane_off = r4 * row_bytes + ul * 16;
-  auto steps_in_chunk = [&](int t, int rest) {
-    const int n = steps - t < rest ? steps - t : rest;
-    return n < kChunk ? n : kChunk;
-  };
   auto load = [&](Q4Chunk<NS>& c) {
-    const int n = steps_in_chunk(lt, lleft);
-    const int row = lq * 4, rows = a.rows - row < 4 ? a.rows - row : 4;
+    const int n = steps_in_chunk(ld), lt = ld.t;
+    const int row = ld.quad * 4, rows = a.rows - row < 4 ? a.rows - row : 4;
     // the step's offset sits in the base, so that the range check is exact; a
     // row's last step may run into the next row, against zeros of x
     const uint8_t* base = a.codes + (size_t)row * row_bytes + lt * (kStepUnits * 16);
     const uint32_t bytes = rows * row_bytes - lt * (kStepUnits * 16);
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i)
-      c.w[i] = __builtin_bit_cast(
-          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(q4_rsrc(base, i < n ? bytes : 0),
-                                                         lane_off, i * (kStepUnits * 16), 2));
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
       const int t = lt + k * (kChunk / NS);
@@ -291,11 +310,16 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
       const uint32_t n2 = k * (kChunk / NS) < n ? (uint32_t)(rows * a.groups) * 2 : 0;
       c.s[k] = __builtin_amdgcn_raw_buffer_load_b16(
           q4_rsrc(a.scale + (size_t)row * a.groups, n2), off, 0, 0);
-      c.z[k] = __builtin_amdgcn_raw_buffer_load_b16(
-          q4_rsrc(a.zero + (size_t)row * a.groups, a.zero ? n2 : 0), off, 0, 0);
+      if (a.zero)
+        c.z[k] = __builtin_amdgcn_raw_buffer_load_b16(
+            q4_rsrc(a.zero + (size_t)row * a.groups, n2), off, 0, 0);
     }
-    lt += n, lleft -= n;
-    if (lt == steps) lt = 0, ++lq;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i)
+      c.w[i] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(q4_rsrc(base, i < n ? bytes : 0),
+                                                         lane_off, i * (kStepUnits * 16), 2));
+    advance(ld, n);
   };
   Q4Chunk<NS> ring[RING];
 #pragma unroll
@@ -376,10 +400,9 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   };
 
   float own = 0.f;  // of a quad that starts in this wave and ends in a later one
-  int own_end = 0;  // its end among the workgroup's steps; 0: none
-  bool head = ct != 0;  // this piece of a quad continues an earlier wave's
+  int own_quad = -1;
   auto consume = [&](const Q4Chunk<NS>& c) {
-    const int n = steps_in_chunk(ct, left);
+    const int n = steps_in_chunk(at);
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
       constexpr int SPL = kChunk / NS;
@@ -388,41 +411,43 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
         uint32_t sz = (uint32_t)c.s[i / SPL] | zero << 16;
         if constexpr (NS < kChunk)
           sz = (uint32_t)__builtin_amdgcn_ds_bpermute(from + (i % SPL) * from_step, (int)sz);
-        multiply(c.w[i], sz, ct + i);
+        multiply(c.w[i], sz, at.t + i);
       }
     }
-    ct += n, left -= n;
-    if (ct == steps || left == 0) {  // the end of a quad, or of this wave's part
+    const int quad = at.quad;
+    // a piece that continues an earlier wave's: the first of the divided quads
+    const bool head = at.whole <= 0 && quad == q2 && t2 != 0;
+    const bool ended = advance(at, n);
+    if (ended || at.left == 0) {
       const float r = total();
       if (head) {
         if (lane < 4 * B) join[wv * (4 * B) + lane] = r;
-      } else if (ct == steps) {
-        store(cq, r);
+      } else if (ended) {
+        store(quad, r);
       } else {
-        own = r, own_end = (cq - quad0 + 1) * steps;
+        own = r, own_quad = quad;
       }
-      if (ct == steps) ct = 0, ++cq;
-      head = false;
     }
   };
   if constexpr (RING == 1) {
-    if (left > 0) consume(ring[0]);
+    if (at.left > 0) consume(ring[0]);
   } else {
-    while (lleft > 0) {  // the ring is full, and a load follows each chunk
+    while (ld.left > 0) {  // the ring is full, and a load follows each chunk
       consume(ring[0]);
       load(ring[0]);
       consume(ring[1]);
       load(ring[1]);
     }
-    if (left > 0) consume(ring[0]);
-    if (left > 0) consume(ring[1]);
+    if (at.left > 0) consume(ring[0]);
+    if (at.left > 0) consume(ring[1]);
   }
   if (per % steps) {  // the same in every wave: some quad lies in several
     __syncthreads();
-    if (own_end) {
-      for (int v = wv + 1; v * per < own_end; ++v)
+    if (own_quad >= 0) {
+      const int end = (last + steps - 1) / steps * steps;  // of the quad, among the divided steps
+      for (int v = wv + 1; v * per < end && v * per < rest_steps; ++v)
         if (lane < 4 * B) own += join[v * (4 * B) + lane];
-      store(own_end / steps - 1 + quad0, own);
+      store(own_quad, own);
     }
   }
 }
@@ -444,7 +469,9 @@ int launch_q4_ring(Q4Args a, hipStream_t st) {
     ++a.wave_shift;
   // one chunk per wave: no more than four steps, and none across two quads
   auto one_chunk = [&](int quads_of_wg) {
-    const long long per = ((long long)quads_of_wg * a.steps + (1 << a.wave_shift) - 1) >> a.wave_shift;
+    const int nw = 1 << a.wave_shift;
+    if (quads_of_wg >= nw) return quads_of_wg == nw && a.steps <= kChunk;
+    const int per = (quads_of_wg * a.steps + nw - 1) / nw;
     return per <= kChunk && (quads_of_wg == 1 || a.steps % per == 0);
   };
   const dim3 grid(wgs), block(kWave << a.wave_shift);
