@@ -52,9 +52,14 @@ struct Q4Args {
   int xshift, xgroups;
   float* y;
   int batch;
-  // the launch: steps of 16 units per row, quads per workgroup (one more in the
-  // first `extra`), log2 of the waves
-  int steps, quads, extra, wave_shift;
+  // the launch: steps of 16 units per row; how a workgroup's quads are dealt,
+  // for the first `extra` workgroups, which have one more, and for the others
+  // (the numbers of waves and workgroups are here too: the kernel's own arguments
+  // arrive with one load, the launch's dimensions with another behind it)
+  int steps, waves, wgs, extra;
+  struct Deal {
+    int quads, whole, per;  // quads, whole ones per wave, divided steps per wave
+  } more, fewer;
 };
 
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
@@ -71,10 +76,16 @@ constexpr int kXAhead = 6;     // pieces of x a wave requests at a time
 
 // LDS: x, then per unit and batch row the sum of x (f16), or x's scale and its
 // product with that sum, then a partial result per wave.
-constexpr size_t x_step_bytes(int B, int X) { return (X == kQ4I8 ? 512 : 1024) * (size_t)B; }
+//
+// x of a step: a slab of 16-byte pieces per word of a unit (f16; per pair of
+// words for int8), unit by unit, batch rows together.  A wave reads a slab in
+// one run; slabs are 16 bytes further apart than they are long, or the four
+// lanes that write a unit's words would write the same banks.
+constexpr int slab_bytes(int B) { return 256 * B + 16; }
+constexpr int x_step_bytes(int B, int X) { return (X == kQ4I8 ? 2 : 4) * slab_bytes(B); }
 constexpr size_t sum_step_bytes(int B) { return kStepUnits * (size_t)B * 4; }
 inline size_t q4_lds_bytes(int B, int X, int steps) {
-  return steps * (x_step_bytes(B, X) + sum_step_bytes(B) * (X == kQ4F16 ? 1 : 2)) +
+  return (size_t)steps * (x_step_bytes(B, X) + sum_step_bytes(B) * (X == kQ4F16 ? 1 : 2)) +
          kQ4Waves * 4 * (size_t)B * 4;
 }
 
@@ -133,7 +144,7 @@ __device__ __forceinline__ void put_x8(const Q4Args& a, uint8_t* xs, float* sums
     // even and odd columns apart, as masking the codes' bytes leaves them
     const u32x2_t o = {__builtin_amdgcn_perm(v.y, v.x, 0x06040200u),
                        __builtin_amdgcn_perm(v.y, v.x, 0x07050301u)};
-    *(u32x2_t*)(xs + (size_t)t * x_step_bytes(B, X) + (((w >> 1) * 16 + ul) * B + bb) * 16 +
+    *(u32x2_t*)(xs + t * x_step_bytes(B, X) + (w >> 1) * slab_bytes(B) + (ul * B + bb) * 16 +
                 (w & 1) * 8) = o;
     const int s = __builtin_amdgcn_sdot4((int)v.x, 0x01010101, 0, false);
     sum = (float)__builtin_amdgcn_sdot4((int)v.y, 0x01010101, s, false);
@@ -148,7 +159,7 @@ __device__ __forceinline__ void put_x8(const Q4Args& a, uint8_t* xs, float* sums
         h[2 * i + 1] = __builtin_bit_cast(uint32_t, lvq_half2{(_Float16)hi.x, (_Float16)hi.y});
       }
     }
-    *(u32x4_t*)(xs + (size_t)t * x_step_bytes(B, X) + ((w * 16 + ul) * B + bb) * 16) =
+    *(u32x4_t*)(xs + t * x_step_bytes(B, X) + w * slab_bytes(B) + (ul * B + bb) * 16) =
         pair_order(h);
     constexpr uint32_t kOnes = 0x3C003C00u;
     sum = dot2(h.x, kOnes, dot2(h.y, kOnes, dot2(h.z, kOnes, dot2(h.w, kOnes, 0.f))));
@@ -195,11 +206,11 @@ struct Q4Chunk {
 // Quads of rows go round the workgroups, and a workgroup's go round its waves,
 // so that the whole chip reads one window of neighbouring rows at a time (with a
 // run of quads per wave, streams a large power of two apart, 131072x4096 took 48
-// instead of 43 us); of the last round, the steps are dealt to the waves in
+// instead of 45 us); of the last round, the steps are dealt to the waves in
 // equal contiguous parts.  A quad whose steps lie in more than one wave is
 // joined in LDS at the end, in order, by the wave that holds its first step.
 // RING: chunks of four steps in flight per wave, 1 where no wave has more.
-template <int B, int X, int NS, int RING>
+template <int B, int X, int NS, bool Z, int RING>
 __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int steps = a.steps;
@@ -210,7 +221,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nw = 1 << a.wave_shift;
+  const int nw = a.waves;
 
   // 1. x: each wave takes pieces of 64 x 8 columns (one step of one batch row),
   //    kXAhead requested at a time; the weights' first loads go out behind the
@@ -218,54 +229,54 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   const int pieces = B * steps;  // of batch rows past the batch: zeros
   u32x4_t xv[kXAhead];
   float xsc[kXAhead];
-  auto row_of = [&](int i) {
-    int bb = 0;
-#pragma unroll
-    for (int k = 1; k < B; ++k) bb += i >= k * steps;
-    return bb;
+  auto load_x = [&](int i, auto vec, u32x4_t& v, float& s) {
+    const int bb = i % B, t = i / B;
+    constexpr int E = X == kQ4F16 ? 2 : 1;
+    v = load_x8<X, decltype(vec)::value>(
+        q4_rsrc((const uint8_t*)a.x + (size_t)bb * a.cols * E, bb < a.batch ? a.cols * E : 0),
+        (t * 64 + lane) * 8);
+    if constexpr (X != kQ4F16)  // past the last unit: a group past the row's, or x is zero
+      s = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(
+                     q4_rsrc(a.xscale + (size_t)bb * a.xgroups, bb < a.batch ? a.xgroups * 4 : 0),
+                     ((t * kStepUnits + (lane >> 2)) >> a.xshift) * 4, 0, 0));
   };
-  auto load_x = [&](int i0) {
+  auto load_ahead = [&](int i0) {
 #pragma unroll
-    for (int k = 0; k < kXAhead; ++k) {
-      const int i = i0 + k * nw, bb = row_of(i), t = i - bb * steps;
-      constexpr int E = X == kQ4F16 ? 2 : 1;
-      if (i < pieces) {
-        const auto rx = q4_rsrc((const uint8_t*)a.x + (size_t)bb * a.cols * E,
-                                bb < a.batch ? a.cols * E : 0);
-        if (a.cols % 8 == 0) xv[k] = load_x8<X, true>(rx, (t * 64 + lane) * 8);
-        else xv[k] = load_x8<X, false>(rx, (t * 64 + lane) * 8);
-        if constexpr (X != kQ4F16) {  // past the last unit: a group past the row's, or x is zero
-          const auto rs = q4_rsrc(a.xscale + (size_t)bb * a.xgroups,
-                                  bb < a.batch ? a.xgroups * 4 : 0);
-          xsc[k] = __builtin_bit_cast(
-              float, __builtin_amdgcn_raw_buffer_load_b32(
-                         rs, ((t * kStepUnits + (lane >> 2)) >> a.xshift) * 4, 0, 0));
-        }
-      }
-    }
+    for (int k = 0; k < kXAhead; ++k)
+      if (i0 + k * nw < pieces) load_x(i0 + k * nw, std::true_type{}, xv[k], xsc[k]);
   };
-  auto put_x = [&](int i0) {
+  auto put_x = [&](int i, u32x4_t v, float s) {
+    put_x8<B, X>(a, xs, sums, scaled, v, s, i % B, i / B, lane);
+  };
+  auto put_ahead = [&](int i0) {
 #pragma unroll
-    for (int k = 0; k < kXAhead; ++k) {
-      const int i = i0 + k * nw, bb = row_of(i);
-      if (i < pieces) put_x8<B, X>(a, xs, sums, scaled, xv[k], xsc[k], bb, i - bb * steps,
-                                     lane);
-    }
+    for (int k = 0; k < kXAhead; ++k)
+      if (i0 + k * nw < pieces) put_x(i0 + k * nw, xv[k], xsc[k]);
   };
   int i0 = wv;
-  load_x(i0);
-  for (; i0 + kXAhead * nw < pieces; i0 += kXAhead * nw) {
-    put_x(i0);
-    load_x(i0 + kXAhead * nw);
+  if (a.cols % 8) {  // rows that do not start aligned: all of x at once, nothing left for later
+    for (; i0 < pieces; i0 += nw) {
+      u32x4_t v;
+      float s = 0.f;
+      load_x(i0, std::false_type{}, v, s);
+      put_x(i0, v, s);
+    }
+  } else {
+    load_ahead(i0);
+    for (; i0 + kXAhead * nw < pieces; i0 += kXAhead * nw) {
+      put_ahead(i0);
+      load_ahead(i0 + kXAhead * nw);
+    }
   }
 
   // 2. this wave's steps: whole quads, one in nw of the workgroup's; of the
   //    fewer than nw that remain, the steps [first, last)
-  const int stride = gridDim.x;
-  const int quads = a.quads + ((int)blockIdx.x < a.extra);
-  const int whole = quads >> a.wave_shift, rest0 = quads - (quads & (nw - 1));
-  const int rest_steps = (quads - rest0) * steps;
-  const int per = (rest_steps + nw - 1) >> a.wave_shift;
+  const int stride = a.wgs;
+  const bool more = (int)blockIdx.x < a.extra;
+  const int whole = more ? a.more.whole : a.fewer.whole, rest0 = whole * nw;
+  const int per = more ? a.more.per : a.fewer.per;
+  const int rest_steps = ((more ? a.more.quads : a.fewer.quads) - rest0) * steps;
   const int first = wv * per < rest_steps ? wv * per : rest_steps;
   const int last = first + per < rest_steps ? first + per : rest_steps;
   const int skip = first / steps;
@@ -291,7 +302,10 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
 
   const int ul = lane >> 2, r4 = lane & 3;
   const int row_bytes = a.nunits * 16;
-  const int lane_off = r4 * row_bytes + ul * 16;
+  int lane_off = r4 * row_bytes + ul * 16;
+  // formed here: between the loads, the compiler's 64-bit multiply-add can take
+  // a load's result register as its unused half, and wait for it
+  asm volatile("" : "+v"(lane_off));
   auto load = [&](Q4Chunk<NS>& c) {
     const int n = steps_in_chunk(ld), lt = ld.t;
     const int row = ld.quad * 4, rows = a.rows - row < 4 ? a.rows - row : 4;
@@ -310,10 +324,11 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
       const uint32_t n2 = k * (kChunk / NS) < n ? (uint32_t)(rows * a.groups) * 2 : 0;
       c.s[k] = __builtin_amdgcn_raw_buffer_load_b16(
           q4_rsrc(a.scale + (size_t)row * a.groups, n2), off, 0, 0);
-      if (a.zero)
+      if constexpr (Z)
         c.z[k] = __builtin_amdgcn_raw_buffer_load_b16(
             q4_rsrc(a.zero + (size_t)row * a.groups, n2), off, 0, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);  // the scales first: they are waited for first
 #pragma unroll
     for (int i = 0; i < kChunk; ++i)
       c.w[i] = __builtin_bit_cast(
@@ -324,7 +339,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   Q4Chunk<NS> ring[RING];
 #pragma unroll
   for (int d = 0; d < RING; ++d) load(ring[d]);
-  put_x(i0);
+  put_ahead(i0);
   __syncthreads();
 
   // 3. the steps
@@ -340,13 +355,13 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   for (int bb = 0; bb < B; ++bb) acc[bb] = 0.f;
 
   auto multiply = [&](u32x4_t q, uint32_t sz, int t) {
-    const uint8_t* xt = xl + (size_t)t * x_step_bytes(B, X);
+    const uint8_t* xt = xl + t * x_step_bytes(B, X);
     float v[B];
     if constexpr (X == kQ4I8) {
       int4_t c = {0, 0, 0, 0};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const u32x4_t x = *(const u32x4_t*)(xt + h * 256 * B);
+        const u32x4_t x = *(const u32x4_t*)(xt + h * slab_bytes(B));
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const uint32_t w = q[2 * h + k];
@@ -361,7 +376,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
       float4_t lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const u32x4_t x = *(const u32x4_t*)(xt + k * 256 * B);
+        const u32x4_t x = *(const u32x4_t*)(xt + k * slab_bytes(B));
         const uint32_t w = q[k], w8 = w >> 8;
         lo = __builtin_amdgcn_mfma_f32_4x4x4f16(
             __builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}),
@@ -407,8 +422,15 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
     for (int i = 0; i < kChunk; ++i) {
       constexpr int SPL = kChunk / NS;
       if (i < n) {
-        const uint32_t zero = a.zero ? (uint32_t)c.z[i / SPL] : 0x4800u;  // 8.0
-        uint32_t sz = (uint32_t)c.s[i / SPL] | zero << 16;
+        // through an empty statement: widened where it was loaded, the wait for
+        // the load would be there too
+        uint16_t scale = c.s[i / SPL], zero = 0x4800;  // 8.0
+        asm volatile("" : "+v"(scale));
+        if constexpr (Z) {
+          zero = c.z[i / SPL];
+          asm volatile("" : "+v"(zero));
+        }
+        uint32_t sz = (uint32_t)scale | (uint32_t)zero << 16;
         if constexpr (NS < kChunk)
           sz = (uint32_t)__builtin_amdgcn_ds_bpermute(from + (i % SPL) * from_step, (int)sz);
         multiply(c.w[i], sz, at.t + i);
@@ -432,7 +454,9 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   if constexpr (RING == 1) {
     if (at.left > 0) consume(ring[0]);
   } else {
-    while (ld.left > 0) {  // the ring is full, and a load follows each chunk
+    // the loads of the loop are one sequence without branches, so that each
+    // wait counts exactly the loads behind the one it is for
+    while (ld.left > 0) {  // both chunks hold steps, and a load follows each
       consume(ring[0]);
       load(ring[0]);
       consume(ring[1]);
@@ -452,42 +476,65 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   }
 }
 
-template <int B, int X, int NS>
+// How the quads of a workgroup are dealt to nw waves, and the chunks that the wave
+// with most requests (an even number where it goes round its ring of two).
+inline Q4Args::Deal q4_deal(int quads, int steps, int nw, int* chunks) {
+  Q4Args::Deal d;
+  d.quads = quads, d.whole = quads / nw;
+  const long long rest = (long long)(quads - d.whole * nw) * steps;
+  d.per = (int)((rest + nw - 1) / nw);
+  *chunks = d.whole * ((steps + kChunk - 1) / kChunk);
+  // a part that crosses a quad's end may take a chunk more
+  if (d.per) *chunks += (d.per + kChunk - 1) / kChunk + (rest > steps && steps % d.per != 0);
+  if (*chunks > 1) *chunks += *chunks & 1;
+  return d;
+}
+
+template <int B, int X, int NS, bool Z>
 int launch_q4_ring(Q4Args a, hipStream_t st) {
   a.steps = (a.nunits + kStepUnits - 1) / kStepUnits;
   const size_t lds = q4_lds_bytes(B, X, a.steps);
   if (lds > device_lds_bytes()) return LVQ_E_SHAPE;
-  // One workgroup per CU, the quads dealt evenly; as many waves, up to 16, as
-  // have a chunk of four steps each.
+  // One workgroup per CU, the quads dealt evenly.  Waves: as many, up to 16, as
+  // need the fewest chunks in all (a chunk cut short still costs its loads:
+  // 4096x12288 as 12 waves of two full chunks instead of 16 of four steps and
+  // two), but enough to bring x in.
   const int cus = device_cus();
   const int quads = (int)(((long long)a.rows + 3) / 4);
   const int wgs = quads < cus ? quads : cus;
-  a.quads = quads / wgs, a.extra = quads % wgs;
-  const long long most = (long long)(a.quads + (a.extra != 0)) * a.steps;
-  a.wave_shift = 0;
-  while ((1 << a.wave_shift) < kQ4Waves && (long long)kChunk << a.wave_shift < most)
-    ++a.wave_shift;
-  // one chunk per wave: no more than four steps, and none across two quads
-  auto one_chunk = [&](int quads_of_wg) {
-    const int nw = 1 << a.wave_shift;
-    if (quads_of_wg >= nw) return quads_of_wg == nw && a.steps <= kChunk;
-    const int per = (quads_of_wg * a.steps + nw - 1) / nw;
-    return per <= kChunk && (quads_of_wg == 1 || a.steps % per == 0);
-  };
-  const dim3 grid(wgs), block(kWave << a.wave_shift);
+  a.wgs = wgs, a.extra = quads % wgs;
+  const int most = quads / wgs + (a.extra != 0);
+  const int least = (B * a.steps + 2 * kXAhead - 1) / (2 * kXAhead);
+  int nw = 1, chunks = 0;
+  long long best = -1;
+  for (int n = least < kQ4Waves ? least : kQ4Waves; n <= kQ4Waves; ++n) {
+    int c;
+    q4_deal(most, a.steps, n, &c);
+    if (best < 0 || (long long)c * n <= best) best = (long long)c * n, nw = n, chunks = c;
+  }
+  a.waves = nw;
+  int c;
+  a.more = q4_deal(quads / wgs + 1, a.steps, nw, &c);
+  if (a.extra && c > chunks) chunks = c;
+  a.fewer = q4_deal(quads / wgs, a.steps, nw, &c);
+  if (c > chunks) chunks = c;
+  const dim3 grid(wgs), block(kWave * nw);
   clear_hip_error();
-  if (one_chunk(a.quads) && (!a.extra || one_chunk(a.quads + 1)))
-    hipLaunchKernelGGL((q4_gemv_kernel<B, X, NS, 1>), grid, block, lds, st, a);
-  else
-    hipLaunchKernelGGL((q4_gemv_kernel<B, X, NS, 2>), grid, block, lds, st, a);
+  if (chunks == 1) hipLaunchKernelGGL((q4_gemv_kernel<B, X, NS, Z, 1>), grid, block, lds, st, a);
+  else hipLaunchKernelGGL((q4_gemv_kernel<B, X, NS, Z, 2>), grid, block, lds, st, a);
   return launch_status();
+}
+
+template <int B, int X, bool Z>
+int launch_q4_groups(const Q4Args& a, hipStream_t st) {
+  return a.gshift == 0   ? launch_q4_ring<B, X, 4, Z>(a, st)
+         : a.gshift == 1 ? launch_q4_ring<B, X, 2, Z>(a, st)
+                         : launch_q4_ring<B, X, 1, Z>(a, st);
 }
 
 template <int B, int X>
 int launch_q4_batch(const Q4Args& a, hipStream_t st) {
-  return a.gshift == 0   ? launch_q4_ring<B, X, 4>(a, st)
-         : a.gshift == 1 ? launch_q4_ring<B, X, 2>(a, st)
-                         : launch_q4_ring<B, X, 1>(a, st);
+  return a.zero ? launch_q4_groups<B, X, true>(a, st) : launch_q4_groups<B, X, false>(a, st);
 }
 
 // Three batch rows run as four (the fourth zeros) where their x fits in LDS,
