@@ -12,18 +12,22 @@
 // four batch sums of its own row and unit, so scale and zero are applied in the
 // lane that loaded them, in fp32, once per unit.
 //
-// No conversion of the codes to floats: a 4-bit value in the lowest bits of an
-// fp16 (or four bits higher) is a subnormal, the value times 2^-24 (2^-20).
-// Per 8 codes one shift and four masks give two A x B operands (columns 0, 4,
-// 2, 6 and 1, 5, 3, 7 of the eight; x is stored in LDS in that order), and two
-// accumulators keep the two powers of two apart.  For int8 x two masks and a
-// shift give the codes as bytes and the sums are exact 32-bit integers.
+// No conversion of the codes to floats: a 4-bit value in bits 4..7 of an fp16 is
+// a subnormal, the value times 2^-20.  Per 8 codes three shifts and four masks
+// give two operands (columns 0, 4, 2, 6 and 1, 5, 3, 7 of the eight; x is stored
+// in LDS in that order).  The position matters: the matrix core aligns a
+// product by the exponents as stored, and a subnormal's leading zeros push its
+// bits off the lower end of the sum.  With the values in bits 0..3 (five
+// operations per 8 codes instead of seven) the error against 64 bits was 4e-6 to
+// 9e-6 of the result's norm, in bits 4..7 it is 0.7e-7 to 3e-7, in bits 6..9 (eight
+// operations) 0.7e-7 to 1e-7; the middle one is below what an fp32 product of
+// unpacked weights has.  For int8 x two masks and a shift give the codes as
+// bytes and the sums are exact 32-bit integers.
 //
 // The weights are the bytes (4.1 to 5 bits each): 4 flops per byte at batch 1.
 // Each wave streams 1 KiB of codes per step (4 rows x 256 contiguous bytes)
-// through a ring of register sets, kQ4Ring steps in flight; x and the sums of x
-// over every unit sit in LDS.  A quad's steps are split over S waves of a
-// workgroup where rows are few, joined in LDS in a fixed order.
+// in chunks of four, two chunks in flight; x and the sums of x over every unit
+// sit in LDS.
 
 #include <type_traits>
 
@@ -69,6 +73,7 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef float float2_t __attribute__((ext_vector_type(2)));
 
+constexpr float kCodeUnit = 0x1p-20f;  // what a code's lowest bit is worth as an fp16 subnormal
 constexpr int kQ4Waves = 16;   // waves per workgroup at most
 constexpr int kStepUnits = 16; // units of 32 columns per step
 constexpr int kChunk = 4;      // steps a wave loads at a time
@@ -167,7 +172,7 @@ __device__ __forceinline__ void put_x8(const Q4Args& a, uint8_t* xs, float* sums
   sum = dpp_add<0x4E, 0xF>(dpp_add<0xB1, 0xF>(sum));  // the quad's four words
   if (w == 0) {
     const int u = t * kStepUnits + ul, at = u * B + bb;
-    if constexpr (X != kQ4I8) sum *= 0x1p-24f;  // the scale of the subnormal codes
+    if constexpr (X != kQ4I8) sum *= kCodeUnit;
     if constexpr (X == kQ4F16) {
       sums[at] = sum;
     } else {
@@ -377,16 +382,17 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const u32x4_t x = *(const u32x4_t*)(xt + k * slab_bytes(B));
-        const uint32_t w = q[k], w8 = w >> 8;
+        const uint32_t w = q[k];
+        constexpr uint32_t m = 0x00F000F0u;
         lo = __builtin_amdgcn_mfma_f32_4x4x4f16(
             __builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}),
-            __builtin_bit_cast(half4_t, u32x2_t{w & 0x000F000Fu, w8 & 0x000F000Fu}), lo, 0, 0, 0);
+            __builtin_bit_cast(half4_t, u32x2_t{(w << 4) & m, (w >> 4) & m}), lo, 0, 0, 0);
         hi = __builtin_amdgcn_mfma_f32_4x4x4f16(
             __builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}),
-            __builtin_bit_cast(half4_t, u32x2_t{w & 0x00F000F0u, w8 & 0x00F000F0u}), hi, 0, 0, 0);
+            __builtin_bit_cast(half4_t, u32x2_t{w & m, (w >> 8) & m}), hi, 0, 0, 0);
       }
 #pragma unroll
-      for (int bb = 0; bb < B; ++bb) v[bb] = __builtin_fmaf(hi[bb], 0.0625f, lo[bb]);
+      for (int bb = 0; bb < B; ++bb) v[bb] = lo[bb] + hi[bb];
     }
     const float s = f16_to_f32(sz), z = f16_to_f32(sz >> 16);
     const float* sx = sl + t * (kStepUnits * B);
@@ -411,7 +417,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   auto store = [&](int quad, float r) {
     const int row = quad * 4 + r4;
     if (ul < a.batch && row < a.rows)
-      a.y[(size_t)ul * a.rows + row] = X == kQ4I8 ? r : r * 0x1p24f;
+      a.y[(size_t)ul * a.rows + row] = X == kQ4I8 ? r : r * (1.f / kCodeUnit);
   };
 
   float own = 0.f;  // of a quad that starts in this wave and ends in a later one

@@ -242,3 +242,27 @@ def test_random_shapes():
             xg = int(r.choice([0, 32, 64, 128, 256]))
             x, s = _x8(kind, batch, cols, xg, i)
             _check(d, x, batch, kind, s, xg)
+
+
+@pytest.mark.parametrize("kind", ["f16", "i8", "e4m3"])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_precision_is_that_of_fp32(kind, zeros):
+    """The error's norm against the result's.  Terms are random, so a unit's sum of
+    32 and the sum over units both grow as a root and their roundings add as a
+    root too: about 2^-24 relative, and 2^-21 where the alignment of a product in
+    the matrix core drops up to three bits of it (codes in bits 4..7 of ten).
+    Twice that is allowed; a code three bits lower would give 2^-17."""
+    rows, cols = 2048, 4096
+    d = synth.q4_matrix(rows, cols, 128, zeros, key=(11,))
+    w, _ = oq.weights(d["codes"], d["scale"], d["zero"], rows, cols, 128)
+    if kind == "f16":
+        x, s = synth.fp16_bits(synth.hidden(4, cols, key=(11,))), None
+        xf = og.f16(x)
+    else:
+        x, s = _x8(kind, 4, cols, 128, 11)
+        xf = oq.activations(x, kind, s, cols, 128)
+    y64 = xf @ w.T
+    y = _run(d, x, 4, kind, s, 128)
+    r = float(np.linalg.norm(y - y64) / np.linalg.norm(y64))
+    print("precision %s %s: %.3g" % (kind, zeros, r), flush=True)
+    assert r <= 2.0 ** -20
