@@ -19,9 +19,9 @@
 // product by the exponents as stored, and a subnormal's leading zeros push its
 // bits off the lower end of the sum.  With the values in bits 0..3 (five
 // operations per 8 codes instead of seven) the error against 64 bits was 4e-6 to
-// 9e-6 of the result's norm, in bits 4..7 it is 0.7e-7 to 3e-7, in bits 6..9 (eight
+// 9e-6 of the result's norm, in bits 4..7 it is 0.9e-7 to 4e-7, in bits 6..9 (eight
 // operations) 0.7e-7 to 1e-7; the middle one is below what an fp32 product of
-// unpacked weights has.  For int8 x two masks and a shift give the codes as
+// unpacked weights has.  The sum starts from minus zero times the unit's sum of x.  For int8 x two masks and a shift give the codes as
 // bytes and the sums are exact 32-bit integers.
 //
 // The weights are the bytes (4.1 to 5 bits each): 4 flops per byte at batch 1.
@@ -79,8 +79,8 @@ constexpr int kStepUnits = 16; // units of 32 columns per step
 constexpr int kChunk = 4;      // steps a wave loads at a time
 constexpr int kXAhead = 6;     // pieces of x a wave requests at a time
 
-// LDS: x, then per unit and batch row the sum of x (f16), or x's scale and its
-// product with that sum, then a partial result per wave.
+// LDS: x, then per unit and batch row the sum of x (see put_x8), then (8-bit x)
+// its scale, then a partial result per wave.
 //
 // x of a step: a slab of 16-byte pieces per word of a unit (f16; per pair of
 // words for int8), unit by unit, batch rows together.  A wave reads a slab in
@@ -139,9 +139,10 @@ __device__ __forceinline__ u32x4_t pair_order(u32x4_t d) {
 }
 
 // Eight columns (word w of unit u of step t, batch row bb) into LDS, and, from
-// the quad of lanes that holds a unit, the unit's sums.  s: the scale of the unit.
-template <int B, int X>
-__device__ __forceinline__ void put_x8(const Q4Args& a, uint8_t* xs, float* sums, float* scaled,
+// the quad of lanes that holds a unit, minus the unit's sum (with zeros), or
+// minus eight times it, as the matrix core's sum takes it, and its scale s.
+template <int B, int X, bool Z>
+__device__ __forceinline__ void put_x8(uint8_t* xs, float* sums, float* scaled,
                                        u32x4_t v, float s, int bb, int t, int lane) {
   const int ul = lane >> 2, w = lane & 3;
   float sum;
@@ -172,13 +173,10 @@ __device__ __forceinline__ void put_x8(const Q4Args& a, uint8_t* xs, float* sums
   sum = dpp_add<0x4E, 0xF>(dpp_add<0xB1, 0xF>(sum));  // the quad's four words
   if (w == 0) {
     const int u = t * kStepUnits + ul, at = u * B + bb;
-    if constexpr (X != kQ4I8) sum *= kCodeUnit;
-    if constexpr (X == kQ4F16) {
-      sums[at] = sum;
-    } else {
-      scaled[at] = s;
-      sums[at] = s * sum;
-    }
+    sum *= (Z ? -1.f : -8.f) * (X == kQ4I8 ? 1.f : kCodeUnit);
+    if constexpr (X == kQ4I8 && !Z) sum = __builtin_bit_cast(float, (int)sum);  // a whole number
+    sums[at] = sum;
+    if constexpr (X != kQ4F16) scaled[at] = s;
   }
 }
 
@@ -252,7 +250,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
       if (i0 + k * nw < pieces) load_x(i0 + k * nw, std::true_type{}, xv[k], xsc[k]);
   };
   auto put_x = [&](int i, u32x4_t v, float s) {
-    put_x8<B, X>(a, xs, sums, scaled, v, s, i % B, i / B, lane);
+    put_x8<B, X, Z>(xs, sums, scaled, v, s, i % B, i / B, lane);
   };
   auto put_ahead = [&](int i0) {
 #pragma unroll
@@ -361,9 +359,14 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
 
   auto multiply = [&](u32x4_t q, uint32_t sz, int t) {
     const uint8_t* xt = xl + t * x_step_bytes(B, X);
+    const float s = f16_to_f32(sz), z = f16_to_f32(sz >> 16);
+    const float* sx = sl + t * (kStepUnits * B);
+    const float* tx = tl + t * (kStepUnits * B);
     float v[B];
     if constexpr (X == kQ4I8) {
-      int4_t c = {0, 0, 0, 0};
+      int4_t c;
+#pragma unroll
+      for (int bb = 0; bb < B; ++bb) c[bb] = Z ? 0 : __builtin_bit_cast(int, sx[bb]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const u32x4_t x = *(const u32x4_t*)(xt + h * slab_bytes(B));
@@ -376,31 +379,31 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
         }
       }
 #pragma unroll
-      for (int bb = 0; bb < B; ++bb) v[bb] = (float)c[bb];
+      for (int bb = 0; bb < B; ++bb) v[bb] = Z ? __builtin_fmaf(z, sx[bb], (float)c[bb]) : (float)c[bb];
     } else {
-      float4_t lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+      // one chain of sums, from -z sum x
+      float4_t c;
+#pragma unroll
+      for (int bb = 0; bb < B; ++bb) c[bb] = Z ? z * sx[bb] : sx[bb];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const u32x4_t x = *(const u32x4_t*)(xt + k * slab_bytes(B));
         const uint32_t w = q[k];
         constexpr uint32_t m = 0x00F000F0u;
-        lo = __builtin_amdgcn_mfma_f32_4x4x4f16(
+        c = __builtin_amdgcn_mfma_f32_4x4x4f16(
             __builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}),
-            __builtin_bit_cast(half4_t, u32x2_t{(w << 4) & m, (w >> 4) & m}), lo, 0, 0, 0);
-        hi = __builtin_amdgcn_mfma_f32_4x4x4f16(
+            __builtin_bit_cast(half4_t, u32x2_t{(w << 4) & m, (w >> 4) & m}), c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_4x4x4f16(
             __builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}),
-            __builtin_bit_cast(half4_t, u32x2_t{w & m, (w >> 8) & m}), hi, 0, 0, 0);
+            __builtin_bit_cast(half4_t, u32x2_t{w & m, (w >> 8) & m}), c, 0, 0, 0);
       }
 #pragma unroll
-      for (int bb = 0; bb < B; ++bb) v[bb] = lo[bb] + hi[bb];
+      for (int bb = 0; bb < B; ++bb) v[bb] = c[bb];
     }
-    const float s = f16_to_f32(sz), z = f16_to_f32(sz >> 16);
-    const float* sx = sl + t * (kStepUnits * B);
-    const float* tx = tl + t * (kStepUnits * B);
 #pragma unroll
     for (int bb = 0; bb < B; ++bb) {
-      if constexpr (X != kQ4F16) v[bb] *= tx[bb];
-      acc[bb] = __builtin_fmaf(s, __builtin_fmaf(-z, sx[bb], v[bb]), acc[bb]);
+      const float f = X == kQ4F16 ? s : s * tx[bb];
+      acc[bb] = __builtin_fmaf(f, v[bb], acc[bb]);
     }
   };
   // lane 4 bb + i < 4 B: the sum of row i of the quad, batch row bb
@@ -424,23 +427,28 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   int own_quad = -1;
   auto consume = [&](const Q4Chunk<NS>& c) {
     const int n = steps_in_chunk(at);
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
+    auto step = [&](int i) {
       constexpr int SPL = kChunk / NS;
-      if (i < n) {
-        // through an empty statement: widened where it was loaded, the wait for
-        // the load would be there too
-        uint16_t scale = c.s[i / SPL], zero = 0x4800;  // 8.0
-        asm volatile("" : "+v"(scale));
-        if constexpr (Z) {
-          zero = c.z[i / SPL];
-          asm volatile("" : "+v"(zero));
-        }
-        uint32_t sz = (uint32_t)scale | (uint32_t)zero << 16;
-        if constexpr (NS < kChunk)
-          sz = (uint32_t)__builtin_amdgcn_ds_bpermute(from + (i % SPL) * from_step, (int)sz);
-        multiply(c.w[i], sz, at.t + i);
+      // through an empty statement: widened where it was loaded, the wait for
+      // the load would be there too
+      uint16_t scale = c.s[i / SPL], zero = 0x4800;  // 8.0
+      asm volatile("" : "+v"(scale));
+      if constexpr (Z) {
+        zero = c.z[i / SPL];
+        asm volatile("" : "+v"(zero));
       }
+      uint32_t sz = (uint32_t)scale | (uint32_t)zero << 16;
+      if constexpr (NS < kChunk)
+        sz = (uint32_t)__builtin_amdgcn_ds_bpermute(from + (i % SPL) * from_step, (int)sz);
+      multiply(c.w[i], sz, at.t + i);
+    };
+    if (n == kChunk) {  // one block of code: the reads of a step overlap the step before
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) step(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunk - 1; ++i)
+        if (i < n) step(i);
     }
     const int quad = at.quad;
     // a piece that continues an earlier wave's: the first of the divided quads
