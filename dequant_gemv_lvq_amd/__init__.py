@@ -436,10 +436,13 @@ def _array(t, name, types, nbytes, dev):
     it), of an int (a raw address, not checked) or of None."""
     if t is None or t.__class__ is int:
         return t
-    if (not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype not in types
-            or not t.is_contiguous() or t.nbytes < nbytes):
-        _refuse(t, name, types, nbytes, dev)
-    return t.data_ptr()
+    try:
+        if (t.dtype in types and t.get_device() == dev and t.nbytes >= nbytes
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, types, nbytes, dev)
 
 
 def _n_groups(cols: int, group: int) -> int:
@@ -469,14 +472,11 @@ def q4_gemv_q8(codes, scale, zero, group: int, rows: int, cols: int, x, x_scale,
     group, rows, cols, batch = int(group), int(rows), int(cols), int(batch)
     x_group = int(x_group)
     dev, stream = _here(stream)
-    if not isinstance(x, _Tensor):  # its type says how to read it: no raw address
-        _refuse(x, "x", _EIGHT, 0, dev)
+    xp, xt = _typed(x, "x", _EIGHT, batch * cols, dev)  # its type says how to read it
     meta = rows * _n_groups(cols, group) * 2
-    xp = _array(x, "x", _EIGHT, batch * cols, dev)
     e = _lib.q4_gemv_q8(_array(codes, "codes", _BYTES, rows * (-(-cols // 32) * 16), dev),
                         _array(scale, "scale", _F16_BITS, meta, dev),
-                        _array(zero, "zero", _F16_BITS, meta, dev), group, rows, cols, xp,
-                        _TYPES[x.dtype],
+                        _array(zero, "zero", _F16_BITS, meta, dev), group, rows, cols, xp, xt,
                         _array(x_scale, "x_scale", _F32, batch * _n_groups(cols, x_group) * 4,
                                dev),
                         x_group, _array(y, "y", _F32, batch * rows * 4, dev), batch, stream)
@@ -487,21 +487,27 @@ def q4_gemv_q8(codes, scale, zero, group: int, rows: int, cols: int, x, x_scale,
 def _rows_of(t, name, dev):
     """(address, type, rows, cols, row stride) of a 2-D tensor of floats whose
     columns are adjacent."""
-    if not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype not in _FLOATS:
+    if not isinstance(t, _Tensor) or t.dtype not in _FLOATS or t.get_device() != dev:
         _refuse(t, name, _FLOATS, 0, dev)
-    if t.dim() != 2:
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2:
         raise ValueError("%s must have two dimensions, rows and columns" % name)
-    (rows, cols), (stride, one) = t.shape, t.stride()
-    if cols > 1 and one != 1:
+    rows, cols = shape
+    if strides[1] != 1 and cols > 1:
         raise ValueError("%s must have adjacent columns" % name)
-    return t.data_ptr(), _TYPES[t.dtype], rows, cols, stride if rows > 1 else cols
+    return t.data_ptr(), _TYPES[t.dtype], rows, cols, strides[0] if rows > 1 else cols
 
 
 def _typed(t, name, types, count, dev):
-    """(address, type) of a contiguous tensor of count values."""
-    if not isinstance(t, _Tensor):
-        _refuse(t, name, types, 0, dev)
-    return _array(t, name, types, count * t.itemsize, dev), _TYPES.get(t.dtype)
+    """(address, type) of a contiguous tensor of at least count values."""
+    try:
+        kind = t.dtype
+        if (kind in types and t.get_device() == dev and t.numel() >= count
+                and t.is_contiguous()):
+            return t.data_ptr(), _TYPES[kind]
+    except AttributeError:
+        pass
+    _refuse(t, name, types, count * getattr(t, "itemsize", 1), dev)
 
 
 def rms_norm(x, residual, weight, eps: float, out, residual_out=None, scale=None, group: int = 0,
