@@ -149,14 +149,55 @@ __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
   return v > m ? v : m;
 }
 
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = dpp_max<0xB1, 0xF>(v);   // the pairing of wave_sum_lane63
+// Sum and maximum over each aligned group of L = 16, 32 or 64 lanes, in all of
+// them: quad swaps and mirrors inside a row of 16, then rows swapped pairwise.
+// Every step adds the same two values on both sides, so all lanes get the same
+// bits.
+__device__ __forceinline__ uint32_t swap16(uint32_t v, uint32_t* other) {
+  auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  *other = p[1];
+  return p[0];
+}
+__device__ __forceinline__ uint32_t swap32(uint32_t v, uint32_t* other) {
+  auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  *other = p[1];
+  return p[0];
+}
+
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v = dpp_add<0xB1, 0xF>(v);
+  v = dpp_add<0x4E, 0xF>(v);
+  v = dpp_add<0x141, 0xF>(v);
+  v = dpp_add<0x140, 0xF>(v);
+  uint32_t o;
+  if constexpr (L >= 32) {
+    v = __builtin_bit_cast(float, swap16(__builtin_bit_cast(uint32_t, v), &o));
+    v += __builtin_bit_cast(float, o);
+  }
+  if constexpr (L >= 64) {
+    v = __builtin_bit_cast(float, swap32(__builtin_bit_cast(uint32_t, v), &o));
+    v += __builtin_bit_cast(float, o);
+  }
+  return v;
+}
+
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  v = dpp_max<0xB1, 0xF>(v);
   v = dpp_max<0x4E, 0xF>(v);
   v = dpp_max<0x141, 0xF>(v);
   v = dpp_max<0x140, 0xF>(v);
-  v = dpp_max<0x142, 0xA>(v);
-  v = dpp_max<0x143, 0xC>(v);
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
+  uint32_t o;
+  if constexpr (L >= 32) {
+    v = swap16(v, &o);
+    v = v > o ? v : o;
+  }
+  if constexpr (L >= 64) {
+    v = swap32(v, &o);
+    v = v > o ? v : o;
+  }
+  return v;
 }
 
 // Maximum over the aligned group of `lanes` (4, 8, 16 or 32) lanes.
@@ -166,8 +207,9 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v, int lanes) {
   if (lanes >= 8) v = dpp_max<0x141, 0xF>(v);
   if (lanes >= 16) v = dpp_max<0x140, 0xF>(v);
   if (lanes >= 32) {
-    const uint32_t m = (uint32_t)__shfl_xor((int)v, 16, kWave);
-    v = v > m ? v : m;
+    uint32_t o;
+    v = swap16(v, &o);
+    v = v > o ? v : o;
   }
   return v;
 }
@@ -181,17 +223,18 @@ struct Out {
 };
 
 // Writes a row's results o[k] (columns 8 (t + k n) .. + 7 belong to thread t of
-// the n that share the row).  WAVE: those threads are lanes of one wave.  red:
-// LDS words, one per wave of the workgroup, not in use by any thread.
-template <int NV, bool WAVE>
+// the n that share the row); cols: a.cols, or 0 in lanes without a row.  LANES:
+// the n are 16, 32 or 64 lanes of a wave; 0: a workgroup.  red: LDS words, one
+// per wave of the workgroup, not in use by any thread.
+template <int NV, int LANES>
 __device__ __forceinline__ void emit(const Out& a, size_t row, const float (&o)[NV][kChunk], int t,
-                                     int n, uint32_t* red) {
+                                     int n, int cols, uint32_t* red) {
   if (a.type == LVQ_F16) {
     uint16_t* p = (uint16_t*)a.out + row * a.cols;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * n) * kChunk;
-      if (c < a.cols) store_chunk(p, LVQ_F16, c, a.cols, o[k]);
+      if (c < cols) store_chunk(p, LVQ_F16, c, cols, o[k]);
     }
     return;
   }
@@ -209,8 +252,8 @@ __device__ __forceinline__ void emit(const Out& a, size_t row, const float (&o)[
     uint32_t m = top[0];
 #pragma unroll
     for (int k = 1; k < NV; ++k) m = m > top[k] ? m : top[k];
-    m = wave_max(m);
-    if constexpr (!WAVE) {
+    m = lanes_max<LANES ? LANES : kWave>(m);
+    if constexpr (LANES == 0) {
       if ((t & (kWave - 1)) == 0) red[t / kWave] = m;
       __syncthreads();
       m = red[0];
@@ -227,7 +270,7 @@ __device__ __forceinline__ void emit(const Out& a, size_t row, const float (&o)[
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (t + k * n) * kChunk;
-    if (c >= a.cols) continue;
+    if (c >= cols) continue;
     const float m = __builtin_bit_cast(float, top[k]);
     // below 2^-100 the reciprocal leaves the fp32 range; NaN compares false
     const bool ok = top[k] < 0x7F800000u && m >= 0x1p-100f;
@@ -251,14 +294,14 @@ __device__ __forceinline__ void emit(const Out& a, size_t row, const float (&o)[
       q = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
       hi = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], q, true);
     }
-    if (c + kChunk <= a.cols) {
+    if (c + kChunk <= cols) {
       const uint32_t q[2] = {lo, hi};
       __builtin_memcpy(p + c, q, sizeof(q));
     } else {
       const int e = opaque(c);
 #pragma unroll
       for (int i = 0; i < kChunk; ++i)
-        if (e + i < a.cols) p[e + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+        if (e + i < cols) p[e + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
     }
     if constexpr (NV > 2) __builtin_amdgcn_sched_barrier(0);
   }
@@ -291,21 +334,31 @@ __device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&w)
   }
 }
 
-// A row per workgroup, or per wave where 64 lanes hold one (WAVE).  Rows are
-// taken a grid apart.
-template <int TX, int TR, int NV, bool WAVE>
-__global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
+// A row per workgroup, or per 16, 32 or 64 lanes of a wave where they hold one
+// (LANES).  Rows are taken a grid apart.
+template <int TX, int TR, int NV, int LANES>
+__global__ void __launch_bounds__(LANES ? 256 : kRowThreads) rms_norm_kernel(NormArgs a) {
   __shared__ uint32_t red[2][2][kRowThreads / kWave];
   const int lane = threadIdx.x & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nw = blockDim.x / kWave;
-  const int t = WAVE ? lane : (int)threadIdx.x;
-  const int n = WAVE ? kWave : (int)blockDim.x;
-  const int64_t step = WAVE ? (int64_t)gridDim.x * nw : gridDim.x;
+  constexpr int kRows = LANES ? kWave / LANES : 1;  // of a wave
+  const int t = LANES ? lane % LANES : (int)threadIdx.x;
+  const int n = LANES ? LANES : (int)blockDim.x;
+  const int64_t step = LANES ? (int64_t)gridDim.x * nw * kRows : gridDim.x;
   constexpr int kResBytes = TR == LVQ_F32 ? 4 : 2;
+  // up to two chunks per thread: the weights are read once, ahead of the rows
+  // (they are the same columns of every row); more would not fit beside the row
+  float wt[NV][kChunk];
+  if constexpr (NV <= 2) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) load_weight(a, (t + k * n) * kChunk, wt[k]);
+  }
   int turn = 0;
-  for (int64_t row = WAVE ? (int64_t)blockIdx.x * nw + wv : blockIdx.x; row < a.rows;
-       row += step, turn ^= 1) {
+  for (int64_t row0 = LANES ? ((int64_t)blockIdx.x * nw + wv) * kRows : blockIdx.x;
+       row0 < a.rows; row0 += step, turn ^= 1) {
+    const int64_t row = LANES ? row0 + lane / (LANES ? LANES : 1) : row0;
+    const int cols = kRows == 1 || row < a.rows ? a.cols : 0;  // 0: these lanes have no row
     const uint8_t* xr = (const uint8_t*)a.x + row * a.x_stride;
     const uint8_t* rr = (const uint8_t*)a.residual + (size_t)row * a.cols * kResBytes;
     // up to two chunks per thread: every load goes out before the first is
@@ -319,8 +372,8 @@ __global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int k = 0; k < G; ++k) {
         const int c = (t + (k0 + k) * n) * kChunk;
-        xc[k] = load_chunk<TX>(xr, c, a.cols);
-        if constexpr (TR != kNone) rc[k] = load_chunk<TR>(rr, c, a.cols);
+        xc[k] = load_chunk<TX>(xr, c, cols);
+        if constexpr (TR != kNone) rc[k] = load_chunk<TR>(rr, c, cols);
       }
 #pragma unroll
       for (int k = 0; k < G; ++k) {
@@ -343,14 +396,12 @@ __global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int c = (t + k * n) * kChunk;
-        if (c < a.cols) store_chunk(ro, a.residual_type, c, a.cols, h[k]);
+        if (c < cols) store_chunk(ro, a.residual_type, c, cols, h[k]);
         if constexpr (NV > 2) __builtin_amdgcn_sched_barrier(0);
       }
     }
-    part = wave_sum_lane63(part);
-    float sum = __builtin_bit_cast(
-        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, part), kWave - 1));
-    if constexpr (!WAVE) {
+    float sum = lanes_sum<LANES ? LANES : kWave>(part);
+    if constexpr (LANES == 0) {
       // two sets of LDS words, used in turn: a wave can be at most one barrier
       // ahead of another, so it never writes a set that is still being read
       float* rs = (float*)red[turn][0];
@@ -362,46 +413,54 @@ __global__ void __launch_bounds__(kRowThreads) rms_norm_kernel(NormArgs a) {
     const float inv = rsqrtf(sum / (float)a.cols + a.eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      float w[kChunk];
-      load_weight(a, (t + k * n) * kChunk, w);
+      if constexpr (NV > 2) load_weight(a, (t + k * n) * kChunk, wt[k]);
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) h[k][i] = h[k][i] * inv * w[i];
+      for (int i = 0; i < kChunk; ++i) h[k][i] = h[k][i] * inv * wt[k][i];
       if constexpr (NV > 2) __builtin_amdgcn_sched_barrier(0);
     }
-    emit<NV, WAVE>(a.out, (size_t)row, h, t, n, red[turn][1]);
+    emit<NV, LANES>(a.out, (size_t)row, h, t, n, cols, red[turn][1]);
   }
 }
 
-// Threads and chunks per thread of a row kernel: a wave per row up to 512
-// columns, else a workgroup per row.
+// Lanes or threads that share a row and chunks per thread.  Up to 512 columns 16,
+// 32 or 64 lanes; above, a workgroup with one chunk per thread for few rows (the
+// shortest way through one row), two for many (fewer waves meet at a row's
+// barriers and each has more loads in flight: 2048x8192 int8 25.5 us with 512
+// threads and two chunks, 36.9 with 1024 and one, 29.5 with 256 and four;
+// 8192x4096 44.5 against 45.9), four where 1024 threads need them.
 struct RowShape {
-  int nv, threads;
-  bool wave;
+  int nv, threads, lanes;
 };
-RowShape row_shape(int cols) {
+RowShape row_shape(int rows, int cols, int group) {
   const int chunks = (cols + kChunk - 1) / kChunk;
-  if (chunks <= kWave) return {1, 256, true};
-  int nv = 1;
-  while (chunks > nv * kRowThreads) nv *= 2;
-  const int threads = ((chunks + nv - 1) / nv + kWave - 1) / kWave * kWave;
-  return {nv, threads, false};
+  if (chunks <= kWave)  // a row's lanes hold whole groups: 256 columns are 32 lanes
+    return {1, 256, chunks <= 16 && group <= 128 ? 16 : chunks <= 32 ? 32 : 64};
+  const int nv = chunks > 2 * kRowThreads ? 4
+                 : chunks > kRowThreads || (rows >= device_cus() && chunks > 256) ? 2 : 1;
+  return {nv, ((chunks + nv - 1) / nv + kWave - 1) / kWave * kWave, 0};
 }
 
+// As many workgroups as the chip holds at once (lanes), or four times that, so
+// that those which end early are followed by others (32768x128: 8.4 us against
+// 11.9; 8192x4096: 51.0 against 45.9).
 unsigned row_grid(int rows, const RowShape& s) {
-  long long wgs = s.wave ? ((long long)rows + s.threads / kWave - 1) / (s.threads / kWave) : rows;
-  const long long most = (long long)device_cus() * (2048 / s.threads) * 4;
+  const int per = s.lanes ? s.threads / s.lanes : 1;
+  const long long wgs = ((long long)rows + per - 1) / per;
+  const long long most = (long long)device_cus() * (2048 / s.threads) * (s.lanes ? 1 : 4);
   return (unsigned)(wgs < most ? wgs : most);
 }
 
 template <int TX, int TR>
 int launch_norm_row(const NormArgs& a, hipStream_t st) {
-  const RowShape s = row_shape(a.cols);
+  const RowShape s = row_shape(a.rows, a.cols, a.out.group);
   const dim3 grid(row_grid(a.rows, s)), block(s.threads);
   clear_hip_error();
-  if (s.wave) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 1, true>), grid, block, 0, st, a);
-  else if (s.nv == 1) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 1, false>), grid, block, 0, st, a);
-  else if (s.nv == 2) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 2, false>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 4, false>), grid, block, 0, st, a);
+  if (s.lanes == 16) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 1, 16>), grid, block, 0, st, a);
+  else if (s.lanes == 32) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 1, 32>), grid, block, 0, st, a);
+  else if (s.lanes == 64) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 1, 64>), grid, block, 0, st, a);
+  else if (s.nv == 1) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 1, 0>), grid, block, 0, st, a);
+  else if (s.nv == 2) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 2, 0>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 4, 0>), grid, block, 0, st, a);
   return launch_status();
 }
 
@@ -437,31 +496,35 @@ __device__ __forceinline__ void silu_chunk(const Chunk<T>& gc, const Chunk<T>& u
   }
 }
 
-// A row per workgroup or wave: for one scale per row.
-template <int T, int NV, bool WAVE>
-__global__ void __launch_bounds__(kRowThreads) silu_row_kernel(SiluArgs a) {
+// One scale per row: a row per workgroup or per 16, 32 or 64 lanes.
+template <int T, int NV, int LANES>
+__global__ void __launch_bounds__(LANES ? 256 : kRowThreads) silu_row_kernel(SiluArgs a) {
   __shared__ uint32_t red[2][kRowThreads / kWave];
+  const int lane = threadIdx.x & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nw = blockDim.x / kWave;
-  const int t = WAVE ? (int)(threadIdx.x & (kWave - 1)) : (int)threadIdx.x;
-  const int n = WAVE ? kWave : (int)blockDim.x;
-  const int64_t step = WAVE ? (int64_t)gridDim.x * nw : gridDim.x;
+  constexpr int kRows = LANES ? kWave / LANES : 1;  // of a wave
+  const int t = LANES ? lane % LANES : (int)threadIdx.x;
+  const int n = LANES ? LANES : (int)blockDim.x;
+  const int64_t step = LANES ? (int64_t)gridDim.x * nw * kRows : gridDim.x;
   int turn = 0;
-  for (int64_t row = WAVE ? (int64_t)blockIdx.x * nw + wv : blockIdx.x; row < a.rows;
-       row += step, turn ^= 1) {
+  for (int64_t row0 = LANES ? ((int64_t)blockIdx.x * nw + wv) * kRows : blockIdx.x;
+       row0 < a.rows; row0 += step, turn ^= 1) {
+    const int64_t row = LANES ? row0 + lane / (LANES ? LANES : 1) : row0;
+    const int cols = kRows == 1 || row < a.rows ? a.cols : 0;  // 0: these lanes have no row
     const uint8_t* gr = (const uint8_t*)a.gate + row * a.stride;
     const uint8_t* ur = (const uint8_t*)a.up + row * a.stride;
     Chunk<T> gc[NV], uc[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * n) * kChunk;
-      gc[k] = load_chunk<T>(gr, c, a.cols);
-      uc[k] = load_chunk<T>(ur, c, a.cols);
+      gc[k] = load_chunk<T>(gr, c, cols);
+      uc[k] = load_chunk<T>(ur, c, cols);
     }
     float o[NV][kChunk];
 #pragma unroll
     for (int k = 0; k < NV; ++k) silu_chunk<T>(gc[k], uc[k], o[k]);
-    emit<NV, WAVE>(a.out, (size_t)row, o, t, n, red[turn]);
+    emit<NV, LANES>(a.out, (size_t)row, o, t, n, cols, red[turn]);
   }
 }
 
@@ -475,14 +538,12 @@ __global__ void __launch_bounds__(256) silu_flat_kernel(SiluArgs a) {
     const int64_t block = i / a.segs;
     const int64_t row = block * per + (threadIdx.x >> a.seg_shift);
     const int chunk = (int)(i - block * a.segs) * seg + (threadIdx.x & (seg - 1));
-    const int c = row < a.rows ? chunk * kChunk : a.cols;  // a.cols: nothing of this tile
-    const int64_t r = row < a.rows ? row : 0;
-    const uint8_t* gr = (const uint8_t*)a.gate + r * a.stride;
-    const uint8_t* ur = (const uint8_t*)a.up + r * a.stride;
+    const int c = chunk * kChunk, cols = row < a.rows ? a.cols : 0;  // 0: no row here
+    const uint8_t* gr = (const uint8_t*)a.gate + row * a.stride;
+    const uint8_t* ur = (const uint8_t*)a.up + row * a.stride;
     float o[1][kChunk];
-    silu_chunk<T>(load_chunk<T>(gr, c, a.cols), load_chunk<T>(ur, c, a.cols), o[0]);
-    emit<1, true>(a.out, (size_t)r, o, c < a.cols ? chunk : (a.cols + kChunk - 1) / kChunk, 0,
-                  nullptr);
+    silu_chunk<T>(load_chunk<T>(gr, c, cols), load_chunk<T>(ur, c, cols), o[0]);
+    emit<1, kWave>(a.out, (size_t)row, o, chunk, 0, cols, nullptr);
   }
 }
 
@@ -490,12 +551,14 @@ template <int T>
 int launch_silu(SiluArgs& a, hipStream_t st) {
   clear_hip_error();
   if (a.out.type != LVQ_F16 && a.out.group == 0) {
-    const RowShape s = row_shape(a.cols);
+    const RowShape s = row_shape(a.rows, a.cols, a.out.group);
     const dim3 grid(row_grid(a.rows, s)), block(s.threads);
-    if (s.wave) hipLaunchKernelGGL((silu_row_kernel<T, 1, true>), grid, block, 0, st, a);
-    else if (s.nv == 1) hipLaunchKernelGGL((silu_row_kernel<T, 1, false>), grid, block, 0, st, a);
-    else if (s.nv == 2) hipLaunchKernelGGL((silu_row_kernel<T, 2, false>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((silu_row_kernel<T, 4, false>), grid, block, 0, st, a);
+    if (s.lanes == 16) hipLaunchKernelGGL((silu_row_kernel<T, 1, 16>), grid, block, 0, st, a);
+    else if (s.lanes == 32) hipLaunchKernelGGL((silu_row_kernel<T, 1, 32>), grid, block, 0, st, a);
+    else if (s.lanes == 64) hipLaunchKernelGGL((silu_row_kernel<T, 1, 64>), grid, block, 0, st, a);
+    else if (s.nv == 1) hipLaunchKernelGGL((silu_row_kernel<T, 1, 0>), grid, block, 0, st, a);
+    else if (s.nv == 2) hipLaunchKernelGGL((silu_row_kernel<T, 2, 0>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((silu_row_kernel<T, 4, 0>), grid, block, 0, st, a);
     return launch_status();
   }
   const int chunks = (a.cols + kChunk - 1) / kChunk;
