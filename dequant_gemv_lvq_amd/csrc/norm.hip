@@ -596,6 +596,11 @@ int check_out(void* out, int out_type, float* out_scale, int out_group, int rows
   return LVQ_OK;
 }
 
+// Whether `rows` rows `stride` values apart (stride >= cols) can be addressed.
+inline bool stride_ok(int rows, int64_t stride) {
+  return stride <= (INT64_MAX >> 4) / (rows > 0 ? rows : 1);
+}
+
 struct Range {
   const void* p;
   size_t n;
@@ -613,7 +618,8 @@ extern "C" int lvq_rms_norm(const void* x, int x_type, int64_t x_stride, const v
                             int residual_type, void* residual_out, const void* weight,
                             int weight_type, float eps, int rows, int cols, void* out,
                             int out_type, float* out_scale, int out_group, void* stream) {
-  if (rows < 0 || cols < 0 || cols > kMaxRowCols || x_stride < cols) return LVQ_E_SHAPE;
+  if (rows < 0 || cols < 0 || cols > kMaxRowCols || x_stride < cols || !stride_ok(rows, x_stride))
+    return LVQ_E_SHAPE;
   if (!float_type(x_type) || ((residual || residual_out) && !float_type(residual_type)) ||
       (weight && !float_type(weight_type)))
     return LVQ_E_SHAPE;
@@ -653,7 +659,8 @@ extern "C" int lvq_rms_norm(const void* x, int x_type, int64_t x_stride, const v
 extern "C" int lvq_silu_mul(const void* gate, const void* up, int in_type, int64_t in_stride,
                             int rows, int cols, void* out, int out_type, float* out_scale,
                             int out_group, void* stream) {
-  if (rows < 0 || cols < 0 || cols > kMaxCols || in_stride < cols || !float_type(in_type))
+  if (rows < 0 || cols < 0 || cols > kMaxCols || in_stride < cols ||
+      !stride_ok(rows, in_stride) || !float_type(in_type))
     return LVQ_E_SHAPE;
   if (cols > kMaxRowCols && out_type != LVQ_F16 && out_group == 0) return LVQ_E_SHAPE;
   SiluArgs a;

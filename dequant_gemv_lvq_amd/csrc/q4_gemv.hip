@@ -588,8 +588,11 @@ int q4_run(const uint8_t* codes, const uint16_t* scale, const uint16_t* zero, in
   if ((long long)batch * cols > 65536) return LVQ_E_SHAPE;
   if (rows == 0) return LVQ_OK;
   const size_t ybytes = (size_t)batch * rows * 4;
+  const size_t meta = (size_t)rows * group_count(cols, group) * 2;
   if (ranges_overlap(y, ybytes, x, (size_t)batch * cols * (xkind == kQ4F16 ? 2 : 1)) ||
-      ranges_overlap(y, ybytes, x_scale, (size_t)batch * group_count(cols, x_group) * 4))
+      ranges_overlap(y, ybytes, x_scale, (size_t)batch * group_count(cols, x_group) * 4) ||
+      ranges_overlap(y, ybytes, codes, (size_t)rows * ((cols + 31) / 32) * 16) ||
+      ranges_overlap(y, ybytes, scale, meta) || ranges_overlap(y, ybytes, zero, meta))
     return LVQ_E_SHAPE;
   if (cols == 0) return zero_output(y, (size_t)batch * rows, st);
   Q4Args a;

@@ -387,9 +387,12 @@ int fp16_gemv(const uint16_t* W, int rows, int cols, const uint16_t* x, float* y
  *   group  columns per scale: 32, 64, 128, 256, or 0 for one scale per row
  *          (G = 1); the last group of a row may be short
  * cols is any number with batch * cols <= 65536.  LVQ_E_SHAPE for any other
- * size or group; LVQ_E_SHAPE too when y overlaps x (or x_scale).  A row's result is the same
- * from run to run and at every batch; the order of its sum depends on the
- * matrix's shape and the device. */
+ * size or group, and when y overlaps an input.  The products of a group are
+ * summed with the codes as they are and the zero is applied to the sum of x, so
+ * an infinity in x gives NaN; other batch rows, and the other rows' results
+ * where a scale or zero is not finite, are not touched by it.  A row's result is
+ * the same from run to run and whatever the batch; the order of its sum depends
+ * on the matrix's shape and the device. */
 int q4_gemv(const uint8_t* codes, const uint16_t* scale, const uint16_t* zero, int group, int rows,
             int cols, const uint16_t* x, float* y, int batch, void* stream);
 

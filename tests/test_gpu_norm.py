@@ -75,7 +75,8 @@ def _norm(rows, cols, x="f32", residual="f16", weight="f16", out="f16", group=0,
 
 SHAPES = [(1, 1), (1, 7), (3, 8), (5, 33), (2, 64), (9, 128), (1, 511), (7, 512), (2, 513),
           (4, 1000), (1, 4096), (4, 4096), (3, 8192), (2, 8193), (1, 16384), (2, 20001),
-          (1, 32768), (700, 128), (300, 1024), (2049, 64)]
+          (1, 32768), (700, 128), (300, 1024), (2049, 64),
+          (301, 4096), (257, 8200), (1025, 200), (4099, 96), (2050, 400)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)

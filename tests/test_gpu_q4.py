@@ -189,6 +189,16 @@ def test_batch_rows_equal_single_calls():
             assert np.array_equal(_run(d, x[b:b + 1], 1)[0], all4[b])
 
 
+def test_infinite_x_is_nan_in_its_batch_row_only():
+    rows, cols = 12, 96
+    d = synth.q4_matrix(rows, cols, 32, False)
+    x = synth.activations(cols, 2, 7)
+    clean = _run(d, x, 2)
+    x[0, 50] = 0x7C00
+    y = _run(d, x, 2)
+    assert not np.isfinite(y[0]).any() and np.array_equal(y[1], clean[1])
+
+
 def test_zero_columns_and_rows():
     y = torch.full((8,), 5.0, device=DEV)
     some = torch.zeros(64, dtype=torch.uint8, device=DEV)

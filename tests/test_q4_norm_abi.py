@@ -38,6 +38,9 @@ def test_q4_refusals(call):
         assert call(**{name: at + 8}) == E.LVQ_E_ALIGN
     assert call(y=X + 64) == E.LVQ_E_SHAPE  # y inside x
     assert call(x=Y + 16) == E.LVQ_E_SHAPE
+    assert call(codes=Y + 16) == E.LVQ_E_SHAPE and call(scale=Y) == E.LVQ_E_SHAPE
+    assert call(zero=Y) == E.LVQ_E_SHAPE
+    assert call(y=C + 8 * 64 - 16) == E.LVQ_E_SHAPE  # the last codes of eight rows
     assert call(rows=0) == E.LVQ_OK and call(rows=0, codes=None, x=None) == E.LVQ_OK
 
 
@@ -75,6 +78,7 @@ def test_transform_refusals(call):
         assert call(x_type=t) == E.LVQ_E_SHAPE
     assert call(rows=-1) == E.LVQ_E_SHAPE and call(cols=-1) == E.LVQ_E_SHAPE
     assert call(stride=127) == E.LVQ_E_SHAPE
+    assert call(stride=2 ** 60) == E.LVQ_E_SHAPE and call(stride=2 ** 63 - 1) == E.LVQ_E_SHAPE
     assert call(cols=32769, stride=32769) == E.LVQ_E_SHAPE
     assert call(cols=65537, stride=65537, group=32) == E.LVQ_E_SHAPE
     for name in ("x", "out", "scale"):
