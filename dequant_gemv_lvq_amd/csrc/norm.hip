@@ -219,7 +219,8 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v, int lanes) {
 struct Out {
   void* out;
   float* scale;
-  int type, group, groups, cols;
+  int cols;
+  uint16_t type, group;
 };
 
 // Writes a row's results o[k] (columns 8 (t + k n) .. + 7 belong to thread t of
@@ -276,7 +277,7 @@ __device__ __forceinline__ void emit(const Out& a, size_t row, const float (&o)[
     const bool ok = top[k] < 0x7F800000u && m >= 0x1p-100f;
     const float inv = ok ? most / m : 0.f;
     if (a.group == 0 ? c == 0 : (c & (a.group - 1)) == 0)
-      a.scale[row * a.groups + (a.group == 0 ? 0 : c / a.group)] =
+      a.scale[a.group == 0 ? row : row * ((a.cols + a.group - 1) / a.group) + c / a.group] =
           ok ? m / most : top[k] < 0x7F800000u ? 0.f : m;
     uint32_t lo = 0, hi = 0;
     float v[kChunk];
@@ -309,28 +310,33 @@ __device__ __forceinline__ void emit(const Out& a, size_t row, const float (&o)[
 
 // ---------------------------------------------------------------- rms_norm
 
+// The kernels' arguments are under 128 bytes, the launch's own dimensions among
+// them (read through the language's variables they bring 200 bytes of hidden
+// arguments along): in a plain program a launch with 112 bytes of arguments costs
+// the host 2.9 us, one with 128 or more 3.6.
 struct NormArgs {
   const void* x;
   int64_t x_stride;  // bytes
   const void* residual;
   void* residual_out;
   const void* weight;
-  int residual_type, weight_type;
   float eps;
-  int rows, cols;
+  int rows, grid;
+  uint16_t residual_type, weight_type, threads;
   Out out;
 };
+static_assert(sizeof(NormArgs) <= 112, "launches of 128 bytes and more are slower");
 
 __device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&w)[kChunk]) {
   if (!a.weight) {
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) w[i] = 1.f;
   } else if (a.weight_type == LVQ_F32) {
-    unpack(load_chunk<LVQ_F32>(a.weight, c, a.cols), w);
+    unpack(load_chunk<LVQ_F32>(a.weight, c, a.out.cols), w);
   } else if (a.weight_type == LVQ_F16) {
-    unpack(load_chunk<LVQ_F16>(a.weight, c, a.cols), w);
+    unpack(load_chunk<LVQ_F16>(a.weight, c, a.out.cols), w);
   } else {
-    unpack(load_chunk<LVQ_BF16>(a.weight, c, a.cols), w);
+    unpack(load_chunk<LVQ_BF16>(a.weight, c, a.out.cols), w);
   }
 }
 
@@ -341,11 +347,11 @@ __global__ void __launch_bounds__(LANES ? 256 : kRowThreads) rms_norm_kernel(Nor
   __shared__ uint32_t red[2][2][kRowThreads / kWave];
   const int lane = threadIdx.x & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nw = blockDim.x / kWave;
+  const int nw = a.threads / kWave;
   constexpr int kRows = LANES ? kWave / LANES : 1;  // of a wave
   const int t = LANES ? lane % LANES : (int)threadIdx.x;
-  const int n = LANES ? LANES : (int)blockDim.x;
-  const int64_t step = LANES ? (int64_t)gridDim.x * nw * kRows : gridDim.x;
+  const int n = LANES ? LANES : (int)a.threads;
+  const int64_t step = LANES ? (int64_t)a.grid * nw * kRows : a.grid;
   constexpr int kResBytes = TR == LVQ_F32 ? 4 : 2;
   // up to two chunks per thread: the weights are read once, ahead of the rows
   // (they are the same columns of every row); more would not fit beside the row
@@ -358,9 +364,9 @@ __global__ void __launch_bounds__(LANES ? 256 : kRowThreads) rms_norm_kernel(Nor
   for (int64_t row0 = LANES ? ((int64_t)blockIdx.x * nw + wv) * kRows : blockIdx.x;
        row0 < a.rows; row0 += step, turn ^= 1) {
     const int64_t row = LANES ? row0 + lane / (LANES ? LANES : 1) : row0;
-    const int cols = kRows == 1 || row < a.rows ? a.cols : 0;  // 0: these lanes have no row
+    const int cols = kRows == 1 || row < a.rows ? a.out.cols : 0;  // 0: these lanes have no row
     const uint8_t* xr = (const uint8_t*)a.x + row * a.x_stride;
-    const uint8_t* rr = (const uint8_t*)a.residual + (size_t)row * a.cols * kResBytes;
+    const uint8_t* rr = (const uint8_t*)a.residual + (size_t)row * a.out.cols * kResBytes;
     // up to two chunks per thread: every load goes out before the first is
     // used; more: two at a time, or the raw values would not fit in registers
     constexpr int G = NV < 2 ? NV : 2;
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__(LANES ? 256 : kRowThreads) rms_norm_kernel(Nor
     }
     if (a.residual_out) {
       uint8_t* ro = (uint8_t*)a.residual_out +
-                    (size_t)row * a.cols * (a.residual_type == LVQ_F32 ? 4 : 2);
+                    (size_t)row * a.out.cols * (a.residual_type == LVQ_F32 ? 4 : 2);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int c = (t + k * n) * kChunk;
@@ -410,7 +416,7 @@ __global__ void __launch_bounds__(LANES ? 256 : kRowThreads) rms_norm_kernel(Nor
       sum = rs[0];
       for (int w = 1; w < nw; ++w) sum += rs[w];
     }
-    const float inv = rsqrtf(sum / (float)a.cols + a.eps);
+    const float inv = rsqrtf(sum / (float)a.out.cols + a.eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if constexpr (NV > 2) load_weight(a, (t + k * n) * kChunk, wt[k]);
@@ -443,17 +449,18 @@ RowShape row_shape(int rows, int cols, int group) {
 // As many workgroups as the chip holds at once (lanes), or four times that, so
 // that those which end early are followed by others (32768x128: 8.4 us against
 // 11.9; 8192x4096: 51.0 against 45.9).
-unsigned row_grid(int rows, const RowShape& s) {
+int row_grid(int rows, const RowShape& s) {
   const int per = s.lanes ? s.threads / s.lanes : 1;
   const long long wgs = ((long long)rows + per - 1) / per;
   const long long most = (long long)device_cus() * (2048 / s.threads) * (s.lanes ? 1 : 4);
-  return (unsigned)(wgs < most ? wgs : most);
+  return (int)(wgs < most ? wgs : most);
 }
 
 template <int TX, int TR>
-int launch_norm_row(const NormArgs& a, hipStream_t st) {
-  const RowShape s = row_shape(a.rows, a.cols, a.out.group);
-  const dim3 grid(row_grid(a.rows, s)), block(s.threads);
+int launch_norm_row(NormArgs a, hipStream_t st) {
+  const RowShape s = row_shape(a.rows, a.out.cols, a.out.group);
+  a.grid = row_grid(a.rows, s), a.threads = (uint16_t)s.threads;
+  const dim3 grid(a.grid), block(s.threads);
   clear_hip_error();
   if (s.lanes == 16) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 1, 16>), grid, block, 0, st, a);
   else if (s.lanes == 32) hipLaunchKernelGGL((rms_norm_kernel<TX, TR, 1, 32>), grid, block, 0, st, a);
@@ -477,9 +484,11 @@ int launch_norm(const NormArgs& a, hipStream_t st) {
 struct SiluArgs {
   const void *gate, *up;
   int64_t stride;  // bytes
-  int rows, cols, seg_shift, segs;
+  int rows, grid, segs;
+  uint16_t seg_shift, threads;
   Out out;
 };
+static_assert(sizeof(SiluArgs) <= 112, "launches of 128 bytes and more are slower");
 
 template <int T>
 __device__ __forceinline__ void silu_chunk(const Chunk<T>& gc, const Chunk<T>& uc,
@@ -502,16 +511,16 @@ __global__ void __launch_bounds__(LANES ? 256 : kRowThreads) silu_row_kernel(Sil
   __shared__ uint32_t red[2][kRowThreads / kWave];
   const int lane = threadIdx.x & (kWave - 1);
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nw = blockDim.x / kWave;
+  const int nw = a.threads / kWave;
   constexpr int kRows = LANES ? kWave / LANES : 1;  // of a wave
   const int t = LANES ? lane % LANES : (int)threadIdx.x;
-  const int n = LANES ? LANES : (int)blockDim.x;
-  const int64_t step = LANES ? (int64_t)gridDim.x * nw * kRows : gridDim.x;
+  const int n = LANES ? LANES : (int)a.threads;
+  const int64_t step = LANES ? (int64_t)a.grid * nw * kRows : a.grid;
   int turn = 0;
   for (int64_t row0 = LANES ? ((int64_t)blockIdx.x * nw + wv) * kRows : blockIdx.x;
        row0 < a.rows; row0 += step, turn ^= 1) {
     const int64_t row = LANES ? row0 + lane / (LANES ? LANES : 1) : row0;
-    const int cols = kRows == 1 || row < a.rows ? a.cols : 0;  // 0: these lanes have no row
+    const int cols = kRows == 1 || row < a.rows ? a.out.cols : 0;  // 0: these lanes have no row
     const uint8_t* gr = (const uint8_t*)a.gate + row * a.stride;
     const uint8_t* ur = (const uint8_t*)a.up + row * a.stride;
     Chunk<T> gc[NV], uc[NV];
@@ -534,11 +543,11 @@ template <int T>
 __global__ void __launch_bounds__(256) silu_flat_kernel(SiluArgs a) {
   const int seg = 1 << a.seg_shift, per = 256 >> a.seg_shift;
   const int64_t tiles = ((int64_t)a.rows + per - 1) / per * a.segs;
-  for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+  for (int64_t i = blockIdx.x; i < tiles; i += a.grid) {
     const int64_t block = i / a.segs;
     const int64_t row = block * per + (threadIdx.x >> a.seg_shift);
     const int chunk = (int)(i - block * a.segs) * seg + (threadIdx.x & (seg - 1));
-    const int c = chunk * kChunk, cols = row < a.rows ? a.cols : 0;  // 0: no row here
+    const int c = chunk * kChunk, cols = row < a.rows ? a.out.cols : 0;  // 0: no row here
     const uint8_t* gr = (const uint8_t*)a.gate + row * a.stride;
     const uint8_t* ur = (const uint8_t*)a.up + row * a.stride;
     float o[1][kChunk];
@@ -551,8 +560,9 @@ template <int T>
 int launch_silu(SiluArgs& a, hipStream_t st) {
   clear_hip_error();
   if (a.out.type != LVQ_F16 && a.out.group == 0) {
-    const RowShape s = row_shape(a.rows, a.cols, a.out.group);
-    const dim3 grid(row_grid(a.rows, s)), block(s.threads);
+    const RowShape s = row_shape(a.rows, a.out.cols, a.out.group);
+    a.grid = row_grid(a.rows, s), a.threads = (uint16_t)s.threads;
+    const dim3 grid(a.grid), block(s.threads);
     if (s.lanes == 16) hipLaunchKernelGGL((silu_row_kernel<T, 1, 16>), grid, block, 0, st, a);
     else if (s.lanes == 32) hipLaunchKernelGGL((silu_row_kernel<T, 1, 32>), grid, block, 0, st, a);
     else if (s.lanes == 64) hipLaunchKernelGGL((silu_row_kernel<T, 1, 64>), grid, block, 0, st, a);
@@ -561,15 +571,15 @@ int launch_silu(SiluArgs& a, hipStream_t st) {
     else hipLaunchKernelGGL((silu_row_kernel<T, 4, 0>), grid, block, 0, st, a);
     return launch_status();
   }
-  const int chunks = (a.cols + kChunk - 1) / kChunk;
+  const int chunks = (a.out.cols + kChunk - 1) / kChunk;
   a.seg_shift = 5;  // at least the 32 lanes of the widest group
   while (a.seg_shift < 8 && (1 << a.seg_shift) < chunks) ++a.seg_shift;
   a.segs = (chunks + (1 << a.seg_shift) - 1) >> a.seg_shift;
   const int per = 256 >> a.seg_shift;
   const long long tiles = ((long long)a.rows + per - 1) / per * a.segs;
   const long long most = (long long)device_cus() * 32;
-  const dim3 grid((unsigned)(tiles < most ? tiles : most));
-  hipLaunchKernelGGL(silu_flat_kernel<T>, grid, dim3(256), 0, st, a);
+  a.grid = (int)(tiles < most ? tiles : most), a.threads = 256;
+  hipLaunchKernelGGL(silu_flat_kernel<T>, dim3(a.grid), dim3(256), 0, st, a);
   return launch_status();
 }
 
@@ -578,6 +588,9 @@ int launch_silu(SiluArgs& a, hipStream_t st) {
 inline bool float_type(int t) { return t == LVQ_F32 || t == LVQ_F16 || t == LVQ_BF16; }
 inline size_t type_bytes(int t) { return t == LVQ_F32 ? 4 : t == LVQ_I8 || t == LVQ_E4M3 ? 1 : 2; }
 inline bool aligned_to(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
+
+// Scales per row of 8-bit outputs.
+inline int scale_count(const Out& o) { return o.group ? (o.cols + o.group - 1) / o.group : 1; }
 
 // The output arguments both entry points share; fills *o.
 int check_out(void* out, int out_type, float* out_scale, int out_group, int rows, int cols,
@@ -590,9 +603,8 @@ int check_out(void* out, int out_type, float* out_scale, int out_group, int rows
   if (!eight && out_scale) return LVQ_E_SHAPE;
   if (rows && cols && (!out || (eight && !out_scale))) return LVQ_E_NULL;
   if (!aligned16(out) || !aligned16(out_scale)) return LVQ_E_ALIGN;
-  o->out = out, o->scale = out_scale, o->type = out_type, o->group = out_group;
-  o->groups = out_group ? (cols + out_group - 1) / out_group : 1;
-  o->cols = cols;
+  o->out = out, o->scale = out_scale, o->cols = cols;
+  o->type = (uint16_t)out_type, o->group = (uint16_t)out_group;
   return LVQ_OK;
 }
 
@@ -637,7 +649,7 @@ extern "C" int lvq_rms_norm(const void* x, int x_type, int64_t x_stride, const v
                        {weight, weight ? (size_t)cols * type_bytes(weight_type) : 0}};
   const Range made[3] = {{residual_out, residual_out ? all * type_bytes(residual_type) : 0},
                          {out, all * type_bytes(out_type)},
-                         {out_scale, out_scale ? (size_t)rows * a.out.groups * 4 : 0}};
+                         {out_scale, out_scale ? (size_t)rows * scale_count(a.out) * 4 : 0}};
   for (int i = 0; i < 3; ++i) {
     for (int j = 0; j < 3; ++j) {
       const bool same_stream = i == 0 && j == 1 && residual == residual_out;
@@ -647,9 +659,9 @@ extern "C" int lvq_rms_norm(const void* x, int x_type, int64_t x_stride, const v
     }
   }
   a.x = x, a.x_stride = x_stride * (int64_t)type_bytes(x_type);
-  a.residual = residual, a.residual_out = residual_out, a.residual_type = residual_type;
-  a.weight = weight, a.weight_type = weight_type, a.eps = eps;
-  a.rows = rows, a.cols = cols;
+  a.residual = residual, a.residual_out = residual_out;
+  a.residual_type = (uint16_t)residual_type, a.weight = weight;
+  a.weight_type = (uint16_t)weight_type, a.eps = eps, a.rows = rows;
   hipStream_t st = (hipStream_t)stream;
   if (x_type == LVQ_F32) return launch_norm<LVQ_F32>(a, st);
   if (x_type == LVQ_F16) return launch_norm<LVQ_F16>(a, st);
@@ -673,13 +685,13 @@ extern "C" int lvq_silu_mul(const void* gate, const void* up, int in_type, int64
   const size_t in_bytes = strided_bytes(rows, cols, in_stride, in_type);
   const Range in[2] = {{gate, in_bytes}, {up, in_bytes}};
   const Range made[2] = {{out, (size_t)rows * cols * type_bytes(out_type)},
-                         {out_scale, out_scale ? (size_t)rows * a.out.groups * 4 : 0}};
+                         {out_scale, out_scale ? (size_t)rows * scale_count(a.out) * 4 : 0}};
   for (int i = 0; i < 2; ++i)
     for (int j = 0; j < 2; ++j)
       if (ranges_overlap(made[i].p, made[i].n, in[j].p, in[j].n)) return LVQ_E_SHAPE;
   if (ranges_overlap(made[0].p, made[0].n, made[1].p, made[1].n)) return LVQ_E_SHAPE;
   a.gate = gate, a.up = up, a.stride = in_stride * (int64_t)tb;
-  a.rows = rows, a.cols = cols, a.seg_shift = 8, a.segs = 1;
+  a.rows = rows, a.seg_shift = 8, a.segs = 1;
   hipStream_t st = (hipStream_t)stream;
   if (in_type == LVQ_F32) return launch_silu<LVQ_F32>(a, st);
   if (in_type == LVQ_F16) return launch_silu<LVQ_F16>(a, st);

@@ -46,25 +46,45 @@ inline int group_shift(int group) {
 }
 inline int group_count(int cols, int group) { return group ? (cols + group - 1) / group : 1; }
 
+// What a call hands to the launch.
+struct Q4Call {
+  const uint8_t* codes;
+  const uint16_t* scale;
+  const uint16_t* zero;
+  int gshift, rows, cols;
+  const void* x;
+  const float* xscale;
+  int xshift;
+  float* y;
+  int batch;
+};
+
+// The kernel's arguments: under 128 bytes, and the launch's own dimensions among
+// them (read through the language's variables they bring 200 bytes of hidden
+// arguments along).  In a plain program a launch with 112 bytes of arguments
+// costs the host 2.9 us, one with 128 or more 3.6.
 struct Q4Args {
   const uint8_t* codes;
   const uint16_t* scale;
   const uint16_t* zero;
-  int gshift, groups, rows, cols, nunits;
   const void* x;
   const float* xscale;
-  int xshift, xgroups;
   float* y;
-  int batch;
-  // the launch: steps of 16 units per row; how a workgroup's quads are dealt,
-  // for the first `extra` workgroups, which have one more, and for the others
-  // (the numbers of waves and workgroups are here too: the kernel's own arguments
-  // arrive with one load, the launch's dimensions with another behind it)
-  int steps, waves, wgs, extra;
-  struct Deal {
-    int quads, whole, per;  // quads, whole ones per wave, divided steps per wave
-  } more, fewer;
+  int rows, cols, nunits, steps, groups, waves;
+  uint8_t gshift, xshift;
+  uint16_t batch;
+  // how a workgroup's quads are dealt: whole ones per wave and divided steps per
+  // wave, [0] in the first `extra` workgroups, which have quads + 1, [1] in the others
+  int wgs, extra, quads, whole[2];
+  uint16_t per[2];
 };
+static_assert(sizeof(Q4Args) <= 112, "launches of 128 bytes and more are slower");
+
+inline int units_of(int cols) { return (cols + 31) / 32; }
+inline int steps_of(int cols) { return (units_of(cols) + 15) / 16; }
+__host__ __device__ inline int groups_of(int units, int shift) {  // units > 0
+  return ((units - 1) >> shift) + 1;
+}
 
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
@@ -216,7 +236,7 @@ struct Q4Chunk {
 template <int B, int X, int NS, bool Z, int RING>
 __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  const int steps = a.steps;
+  const int nunits = a.nunits, steps = a.steps, groups = a.groups;
   uint8_t* xs = smem;
   float* sums = (float*)(smem + steps * x_step_bytes(B, X));
   float* scaled = sums + steps * (sum_step_bytes(B) / 4);
@@ -230,6 +250,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   //    kXAhead requested at a time; the weights' first loads go out behind the
   //    last of them, so the wait for x does not include the weights
   const int pieces = B * steps;  // of batch rows past the batch: zeros
+  const int xgroups = groups_of(nunits, a.xshift);
   u32x4_t xv[kXAhead];
   float xsc[kXAhead];
   auto load_x = [&](int i, auto vec, u32x4_t& v, float& s) {
@@ -241,7 +262,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
     if constexpr (X != kQ4F16)  // past the last unit: a group past the row's, or x is zero
       s = __builtin_bit_cast(
           float, __builtin_amdgcn_raw_buffer_load_b32(
-                     q4_rsrc(a.xscale + (size_t)bb * a.xgroups, bb < a.batch ? a.xgroups * 4 : 0),
+                     q4_rsrc(a.xscale + (size_t)bb * xgroups, bb < a.batch ? xgroups * 4 : 0),
                      ((t * kStepUnits + (lane >> 2)) >> a.xshift) * 4, 0, 0));
   };
   auto load_ahead = [&](int i0) {
@@ -277,9 +298,9 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   //    fewer than nw that remain, the steps [first, last)
   const int stride = a.wgs;
   const bool more = (int)blockIdx.x < a.extra;
-  const int whole = more ? a.more.whole : a.fewer.whole, rest0 = whole * nw;
-  const int per = more ? a.more.per : a.fewer.per;
-  const int rest_steps = ((more ? a.more.quads : a.fewer.quads) - rest0) * steps;
+  const int whole = more ? a.whole[0] : a.whole[1], rest0 = whole * nw;
+  const int per = more ? a.per[0] : a.per[1];
+  const int rest_steps = (a.quads + more - rest0) * steps;
   const int first = wv * per < rest_steps ? wv * per : rest_steps;
   const int last = first + per < rest_steps ? first + per : rest_steps;
   const int skip = first / steps;
@@ -304,7 +325,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   Cursor ld = at;  // where the loads are
 
   const int ul = lane >> 2, r4 = lane & 3;
-  const int row_bytes = a.nunits * 16;
+  const int row_bytes = nunits * 16;
   int lane_off = r4 * row_bytes + ul * 16;
   // formed here: between the loads, the compiler's 64-bit multiply-add can take
   // a load's result register as its unused half, and wait for it
@@ -323,13 +344,13 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
       // a group past the row's end: an offset past every buffer, by the sign
       // bit of the difference (a select becomes a branch around the load)
       const int off =
-          ((r4 * a.groups + g) * 2) | ((a.groups - 1 - g) & (int)0x80000000);
-      const uint32_t n2 = k * (kChunk / NS) < n ? (uint32_t)(rows * a.groups) * 2 : 0;
+          ((r4 * groups + g) * 2) | ((groups - 1 - g) & (int)0x80000000);
+      const uint32_t n2 = k * (kChunk / NS) < n ? (uint32_t)(rows * groups) * 2 : 0;
       c.s[k] = __builtin_amdgcn_raw_buffer_load_b16(
-          q4_rsrc(a.scale + (size_t)row * a.groups, n2), off, 0, 0);
+          q4_rsrc(a.scale + (size_t)row * groups, n2), off, 0, 0);
       if constexpr (Z)
         c.z[k] = __builtin_amdgcn_raw_buffer_load_b16(
-            q4_rsrc(a.zero + (size_t)row * a.groups, n2), off, 0, 0);
+            q4_rsrc(a.zero + (size_t)row * groups, n2), off, 0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);  // the scales first: they are waited for first
 #pragma unroll
@@ -492,83 +513,106 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
 
 // How the quads of a workgroup are dealt to nw waves, and the chunks that the wave
 // with most requests (an even number where it goes round its ring of two).
-inline Q4Args::Deal q4_deal(int quads, int steps, int nw, int* chunks) {
-  Q4Args::Deal d;
-  d.quads = quads, d.whole = quads / nw;
-  const long long rest = (long long)(quads - d.whole * nw) * steps;
-  d.per = (int)((rest + nw - 1) / nw);
-  *chunks = d.whole * ((steps + kChunk - 1) / kChunk);
+struct Q4Deal {
+  int whole, per, chunks;
+};
+inline __attribute__((always_inline)) Q4Deal q4_deal(int quads, int steps, int nw) {
+  Q4Deal d;
+  d.whole = quads / nw;
+  const int rest = (quads - d.whole * nw) * steps;
+  d.per = (rest + nw - 1) / nw;
+  d.chunks = d.whole * ((steps + kChunk - 1) / kChunk);
   // a part that crosses a quad's end may take a chunk more
-  if (d.per) *chunks += (d.per + kChunk - 1) / kChunk + (rest > steps && steps % d.per != 0);
-  if (*chunks > 1) *chunks += *chunks & 1;
+  if (d.per) d.chunks += (d.per + kChunk - 1) / kChunk + (rest > steps && steps % d.per != 0);
+  if (d.chunks > 1) d.chunks += d.chunks & 1;
   return d;
 }
 
 template <int B, int X, int NS, bool Z>
-int launch_q4_ring(Q4Args a, hipStream_t st) {
-  a.steps = (a.nunits + kStepUnits - 1) / kStepUnits;
-  const size_t lds = q4_lds_bytes(B, X, a.steps);
-  if (lds > device_lds_bytes()) return LVQ_E_SHAPE;
+int launch_q4_ring(const Q4Call& c, hipStream_t st) {
+  const int steps = steps_of(c.cols);
+  const size_t lds = q4_lds_bytes(B, X, steps);
   // One workgroup per CU, the quads dealt evenly.  Waves: as many, up to 16, as
   // need the fewest chunks in all (a chunk cut short still costs its loads:
   // 4096x12288 as 12 waves of two full chunks instead of 16 of four steps and
   // two), but enough to bring x in.
   const int cus = device_cus();
-  const int quads = (int)(((long long)a.rows + 3) / 4);
-  const int wgs = quads < cus ? quads : cus;
-  a.wgs = wgs, a.extra = quads % wgs;
-  const int most = quads / wgs + (a.extra != 0);
-  const int least = (B * a.steps + 2 * kXAhead - 1) / (2 * kXAhead);
-  int nw = 1, chunks = 0;
+  const int quads = (int)(((long long)c.rows + 3) / 4);
+  Q4Args a;
+  a.codes = c.codes, a.scale = c.scale, a.zero = c.zero;
+  a.x = c.x, a.xscale = c.xscale, a.y = c.y;
+  a.rows = c.rows, a.cols = c.cols, a.nunits = units_of(c.cols), a.steps = steps;
+  a.groups = groups_of(a.nunits, c.gshift), a.gshift = (uint8_t)c.gshift;
+  a.xshift = (uint8_t)c.xshift, a.batch = (uint16_t)c.batch;
+  a.wgs = quads < cus ? quads : cus;
+  a.quads = quads / a.wgs, a.extra = quads % a.wgs;
+  const int most = a.quads + (a.extra != 0);
+  const int least = (B * steps + 2 * kXAhead - 1) / (2 * kXAhead);
+  int nw = kQ4Waves;
   long long best = -1;
-  for (int n = least < kQ4Waves ? least : kQ4Waves; n <= kQ4Waves; ++n) {
-    int c;
-    q4_deal(most, a.steps, n, &c);
-    if (best < 0 || (long long)c * n <= best) best = (long long)c * n, nw = n, chunks = c;
+  auto consider = [&](auto waves) {  // a constant, so that its divisions are none
+    constexpr int n = decltype(waves)::value;
+    if (n < kQ4Waves && n < least) return;
+    const long long cost = (long long)q4_deal(most, steps, n).chunks * n;
+    if (best < 0 || cost < best) best = cost, nw = n;
+  };
+  consider(std::integral_constant<int, 16>{});
+  if (most < 4 * kQ4Waves) {  // with more, 16 waves lose little to the last round
+    consider(std::integral_constant<int, 14>{});
+    consider(std::integral_constant<int, 12>{});
+    consider(std::integral_constant<int, 10>{});
+    consider(std::integral_constant<int, 8>{});
+    consider(std::integral_constant<int, 6>{});
+    consider(std::integral_constant<int, 4>{});
+    consider(std::integral_constant<int, 3>{});
+    consider(std::integral_constant<int, 2>{});
+    consider(std::integral_constant<int, 1>{});
   }
+  const Q4Deal more = q4_deal(a.quads + 1, steps, nw), fewer = q4_deal(a.quads, steps, nw);
   a.waves = nw;
-  int c;
-  a.more = q4_deal(quads / wgs + 1, a.steps, nw, &c);
-  if (a.extra && c > chunks) chunks = c;
-  a.fewer = q4_deal(quads / wgs, a.steps, nw, &c);
-  if (c > chunks) chunks = c;
-  const dim3 grid(wgs), block(kWave * nw);
+  a.whole[0] = more.whole, a.whole[1] = fewer.whole;
+  a.per[0] = (uint16_t)more.per, a.per[1] = (uint16_t)fewer.per;
+  const bool one_chunk = fewer.chunks == 1 && (a.extra == 0 || more.chunks == 1);
+  const dim3 grid(a.wgs), block(kWave * nw);
   clear_hip_error();
-  if (chunks == 1) hipLaunchKernelGGL((q4_gemv_kernel<B, X, NS, Z, 1>), grid, block, lds, st, a);
+  if (one_chunk) hipLaunchKernelGGL((q4_gemv_kernel<B, X, NS, Z, 1>), grid, block, lds, st, a);
   else hipLaunchKernelGGL((q4_gemv_kernel<B, X, NS, Z, 2>), grid, block, lds, st, a);
   return launch_status();
 }
 
 template <int B, int X, bool Z>
-int launch_q4_groups(const Q4Args& a, hipStream_t st) {
-  return a.gshift == 0   ? launch_q4_ring<B, X, 4, Z>(a, st)
-         : a.gshift == 1 ? launch_q4_ring<B, X, 2, Z>(a, st)
-                         : launch_q4_ring<B, X, 1, Z>(a, st);
+int launch_q4_groups(const Q4Call& c, hipStream_t st) {
+  return c.gshift == 0   ? launch_q4_ring<B, X, 4, Z>(c, st)
+         : c.gshift == 1 ? launch_q4_ring<B, X, 2, Z>(c, st)
+                         : launch_q4_ring<B, X, 1, Z>(c, st);
 }
 
 template <int B, int X>
-int launch_q4_batch(const Q4Args& a, hipStream_t st) {
-  return a.zero ? launch_q4_groups<B, X, true>(a, st) : launch_q4_groups<B, X, false>(a, st);
+int launch_q4_batch(const Q4Call& c, hipStream_t st) {
+  return c.zero ? launch_q4_groups<B, X, true>(c, st) : launch_q4_groups<B, X, false>(c, st);
 }
 
 // Three batch rows run as four (the fourth zeros) where their x fits in LDS,
-// else as two and one.
+// else as two and one.  Every other x of batch * cols <= 65536 fits.
 template <int X>
-int launch_q4(Q4Args a, hipStream_t st) {
-  const int steps = (a.nunits + kStepUnits - 1) / kStepUnits;
-  if (a.batch == 1) return launch_q4_batch<1, X>(a, st);
-  if (a.batch == 2) return launch_q4_batch<2, X>(a, st);
-  if (a.batch == 3 && q4_lds_bytes(4, X, steps) > device_lds_bytes()) {
-    a.batch = 2;
-    const int e = launch_q4_batch<2, X>(a, st);
+int launch_q4(Q4Call c, hipStream_t st) {
+  const size_t most = device_lds_bytes();
+  const int steps = steps_of(c.cols);
+  if (c.batch == 3 && q4_lds_bytes(4, X, steps) > most) {
+    c.batch = 2;
+    const int e = launch_q4<X>(c, st);
     if (e) return e;
-    a.batch = 1;
-    a.x = (const uint8_t*)a.x + (size_t)2 * a.cols * (X == kQ4F16 ? 2 : 1);
-    if (X != kQ4F16) a.xscale += (size_t)2 * a.xgroups;
-    a.y += (size_t)2 * a.rows;
-    return launch_q4_batch<1, X>(a, st);
+    c.batch = 1;
+    c.x = (const uint8_t*)c.x + (size_t)2 * c.cols * (X == kQ4F16 ? 2 : 1);
+    if (X != kQ4F16) c.xscale += (size_t)2 * groups_of(units_of(c.cols), c.xshift);
+    c.y += (size_t)2 * c.rows;
+    return launch_q4<X>(c, st);
   }
-  return launch_q4_batch<4, X>(a, st);
+  const int B = c.batch == 3 ? 4 : c.batch;
+  if (q4_lds_bytes(B, X, steps) > most) return LVQ_E_SHAPE;
+  return B == 1   ? launch_q4_batch<1, X>(c, st)
+         : B == 2 ? launch_q4_batch<2, X>(c, st)
+                  : launch_q4_batch<4, X>(c, st);
 }
 
 // The checks both entry points make, and the launch.
@@ -595,17 +639,10 @@ int q4_run(const uint8_t* codes, const uint16_t* scale, const uint16_t* zero, in
       ranges_overlap(y, ybytes, scale, meta) || ranges_overlap(y, ybytes, zero, meta))
     return LVQ_E_SHAPE;
   if (cols == 0) return zero_output(y, (size_t)batch * rows, st);
-  Q4Args a;
-  a.codes = codes, a.scale = scale, a.zero = zero;
-  a.gshift = gs, a.groups = group_count(cols, group);
-  a.rows = rows, a.cols = cols, a.nunits = (cols + 31) / 32;
-  a.x = x, a.xscale = x_scale;
-  a.xshift = xs, a.xgroups = group_count(cols, x_group);
-  a.y = y;
-  a.batch = batch;
-  if (xkind == kQ4F16) return launch_q4<kQ4F16>(a, st);
-  if (xkind == kQ4I8) return launch_q4<kQ4I8>(a, st);
-  return launch_q4<kQ4E4M3>(a, st);
+  const Q4Call c = {codes, scale, zero, gs, rows, cols, x, x_scale, xs, y, batch};
+  if (xkind == kQ4F16) return launch_q4<kQ4F16>(c, st);
+  if (xkind == kQ4I8) return launch_q4<kQ4I8>(c, st);
+  return launch_q4<kQ4E4M3>(c, st);
 }
 
 }  // namespace lvq
