@@ -532,10 +532,13 @@ template <int B, int X, int NS, bool Z>
 int launch_q4_ring(const Q4Call& c, hipStream_t st) {
   const int steps = steps_of(c.cols);
   const size_t lds = q4_lds_bytes(B, X, steps);
-  // One workgroup per CU, the quads dealt evenly.  Waves: as many, up to 16, as
-  // need the fewest chunks in all (a chunk cut short still costs its loads:
-  // 4096x12288 as 12 waves of two full chunks instead of 16 of four steps and
-  // two), but enough to bring x in.
+  // One workgroup per CU, the quads dealt evenly.  Waves: what costs a CU least,
+  // a chunk being about 80 cycles of its load unit (five loads of 16, whether or
+  // not a load cut off returns anything) and 1200 cycles of one wave's time, which
+  // other waves overlap: 4096x12288 takes 12 waves of two full chunks instead of
+  // 16 of four steps and two (batch 4: 10.1 us against 11.1), 4096x4096 takes 8 of
+  // one instead of 16 of half a chunk (3.9 us against 6.1).  And enough to bring
+  // x in.
   const int cus = device_cus();
   const int quads = (int)(((long long)c.rows + 3) / 4);
   Q4Args a;
@@ -553,11 +556,11 @@ int launch_q4_ring(const Q4Call& c, hipStream_t st) {
   auto consider = [&](auto waves) {  // a constant, so that its divisions are none
     constexpr int n = decltype(waves)::value;
     if (n < kQ4Waves && n < least) return;
-    const long long cost = (long long)q4_deal(most, steps, n).chunks * n;
+    const long long cost = (long long)q4_deal(most, steps, n).chunks * (80 * n + 1200);
     if (best < 0 || cost < best) best = cost, nw = n;
   };
   consider(std::integral_constant<int, 16>{});
-  if (most < 4 * kQ4Waves) {  // with more, 16 waves lose little to the last round
+  if (most < 8 * kQ4Waves) {  // with more, 16 waves lose little to the last round
     consider(std::integral_constant<int, 14>{});
     consider(std::integral_constant<int, 12>{});
     consider(std::integral_constant<int, 10>{});
