@@ -126,25 +126,42 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t q4_rsrc(const void* base, uint
 // ---------------------------------------------------------------- x into LDS
 
 // Eight columns of a batch row as they lie in memory (16 bytes of fp16, or 8),
-// zeros past the row's end; rx: the row.  Rows whose length is no multiple of
-// eight are read value by value (their starts are not aligned).
-template <int X, bool VEC>
+// zeros past the row's end.
+//   load_x8    rows of a multiple of eight columns; rx: the row
+//   whole_x8   rows that start anywhere (global memory takes any alignment):
+//              zeros too for the eight that the row's end cuts
+//   cut_x8     those, value by value, zeros in every other lane
+template <int X>
 __device__ __forceinline__ u32x4_t load_x8(__amdgpu_buffer_rsrc_t rx, int c) {
-  u32x4_t v = {0, 0, 0, 0};
-  if constexpr (VEC && X == kQ4F16) {
-    v = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rx, c * 2, 0, 0));
-  } else if constexpr (VEC) {
-    const auto h = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rx, c, 0, 0));
-    v.x = h.x, v.y = h.y;
-  } else if constexpr (X == kQ4F16) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i >> 1] |= (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rx, (c + i) * 2, 0, 0)
-                   << (16 * (i & 1));
+  if constexpr (X == kQ4F16) {
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rx, c * 2, 0, 0));
   } else {
+    const auto h = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rx, c, 0, 0));
+    return u32x4_t{h.x, h.y, 0, 0};
+  }
+}
+
+template <int X>
+__device__ __forceinline__ u32x4_t whole_x8(const uint8_t* row, int c, int cols) {
+  constexpr int E = X == kQ4F16 ? 2 : 1;
+  u32x4_t v = {0, 0, 0, 0};
+  if (c + 8 <= cols) __builtin_memcpy(&v, row + (size_t)c * E, 8 * E);
+  return v;
+}
+
+template <int X>
+__device__ __forceinline__ u32x4_t cut_x8(__amdgpu_buffer_rsrc_t rx, int c, int cols) {
+  constexpr int E = X == kQ4F16 ? 2 : 1;
+  u32x4_t v = {0, 0, 0, 0};
+  const int past = ~(cols - 8 - c) & (int)0x80000000;  // set where all eight are inside
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i >> 2] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rx, c + i, 0, 0)
+  for (int i = 0; i < 8; ++i) {
+    const int at = ((c + i) * E) | past;
+    if constexpr (E == 2)
+      v[i >> 1] |= (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rx, at, 0, 0)
+                   << (16 * (i & 1));
+    else
+      v[i >> 2] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rx, at, 0, 0)
                    << (8 * (i & 3));
   }
   return v;
@@ -253,44 +270,45 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   const int xgroups = groups_of(nunits, a.xshift);
   u32x4_t xv[kXAhead];
   float xsc[kXAhead];
-  auto load_x = [&](int i, auto vec, u32x4_t& v, float& s) {
-    const int bb = i % B, t = i / B;
-    constexpr int E = X == kQ4F16 ? 2 : 1;
-    v = load_x8<X, decltype(vec)::value>(
-        q4_rsrc((const uint8_t*)a.x + (size_t)bb * a.cols * E, bb < a.batch ? a.cols * E : 0),
-        (t * 64 + lane) * 8);
-    if constexpr (X != kQ4F16)  // past the last unit: a group past the row's, or x is zero
-      s = __builtin_bit_cast(
-          float, __builtin_amdgcn_raw_buffer_load_b32(
-                     q4_rsrc(a.xscale + (size_t)bb * xgroups, bb < a.batch ? xgroups * 4 : 0),
-                     ((t * kStepUnits + (lane >> 2)) >> a.xshift) * 4, 0, 0));
-  };
-  auto load_ahead = [&](int i0) {
+  constexpr int E = X == kQ4F16 ? 2 : 1;
+  const bool even = a.cols % 8 == 0;  // every row starts at a piece's alignment
+  auto row_at = [&](int bb) { return (const uint8_t*)a.x + (size_t)bb * a.cols * E; };
+  auto row_of = [&](int bb) { return q4_rsrc(row_at(bb), bb < a.batch ? a.cols * E : 0); };
+  auto load_ahead = [&](int i0, auto is_even) {
 #pragma unroll
-    for (int k = 0; k < kXAhead; ++k)
-      if (i0 + k * nw < pieces) load_x(i0 + k * nw, std::true_type{}, xv[k], xsc[k]);
+    for (int k = 0; k < kXAhead; ++k) {
+      const int i = i0 + k * nw, bb = i % B, t = i / B, c = (t * 64 + lane) * 8;
+      if (i >= pieces) continue;
+      if constexpr (decltype(is_even)::value) xv[k] = load_x8<X>(row_of(bb), c);
+      else xv[k] = whole_x8<X>(row_at(bb), c, bb < a.batch ? a.cols : 0);
+      if constexpr (X != kQ4F16)  // past the last unit: a group past the row's, or x is zero
+        xsc[k] = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(
+                       q4_rsrc(a.xscale + (size_t)bb * xgroups, bb < a.batch ? xgroups * 4 : 0),
+                       ((t * kStepUnits + (lane >> 2)) >> a.xshift) * 4, 0, 0));
+    }
   };
-  auto put_x = [&](int i, u32x4_t v, float s) {
-    put_x8<B, X, Z>(xs, sums, scaled, v, s, i % B, i / B, lane);
-  };
-  auto put_ahead = [&](int i0) {
+  auto put_ahead = [&](int i0, auto is_even) {
 #pragma unroll
-    for (int k = 0; k < kXAhead; ++k)
-      if (i0 + k * nw < pieces) put_x(i0 + k * nw, xv[k], xsc[k]);
+    for (int k = 0; k < kXAhead; ++k) {
+      const int i = i0 + k * nw, bb = i % B, t = i / B;
+      if (i >= pieces) continue;
+      if constexpr (!decltype(is_even)::value)
+        if (t == a.cols / 512) xv[k] |= cut_x8<X>(row_of(bb), (t * 64 + lane) * 8, a.cols);
+      put_x8<B, X, Z>(xs, sums, scaled, xv[k], xsc[k], bb, t, lane);
+    }
   };
   int i0 = wv;
-  if (a.cols % 8) {  // rows that do not start aligned: all of x at once, nothing left for later
-    for (; i0 < pieces; i0 += nw) {
-      u32x4_t v;
-      float s = 0.f;
-      load_x(i0, std::false_type{}, v, s);
-      put_x(i0, v, s);
-    }
-  } else {
-    load_ahead(i0);
+  if (even) {
+    load_ahead(i0, std::true_type{});
     for (; i0 + kXAhead * nw < pieces; i0 += kXAhead * nw) {
-      put_ahead(i0);
-      load_ahead(i0 + kXAhead * nw);
+      put_ahead(i0, std::true_type{});
+      load_ahead(i0 + kXAhead * nw, std::true_type{});
+    }
+  } else {  // all of x here, nothing left for later
+    for (; i0 < pieces; i0 += kXAhead * nw) {
+      load_ahead(i0, std::false_type{});
+      put_ahead(i0, std::false_type{});
     }
   }
 
@@ -363,7 +381,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   Q4Chunk<NS> ring[RING];
 #pragma unroll
   for (int d = 0; d < RING; ++d) load(ring[d]);
-  put_ahead(i0);
+  if (even) put_ahead(i0, std::true_type{});
   __syncthreads();
 
   // 3. the steps
