@@ -556,7 +556,10 @@ int launch_q4_ring(const Q4Call& c, hipStream_t st) {
   // other waves overlap: 4096x12288 takes 12 waves of two full chunks instead of
   // 16 of four steps and two (batch 4: 10.1 us against 11.1), 4096x4096 takes 8 of
   // one instead of 16 of half a chunk (3.9 us against 6.1).  And enough to bring
-  // x in.
+  // in the x of four batch rows, whatever the batch: the waves decide where a
+  // row's steps are divided, and a row's bits are the same in every batch.  (With
+  // the lower bound of batch 1 for all, 1024x12288 batch 4 takes 7.1 us instead
+  // of 6.4; with this one, 1024x16384 batch 1 takes 4.9 instead of 4.6.)
   const int cus = device_cus();
   const int quads = (int)(((long long)c.rows + 3) / 4);
   Q4Args a;
@@ -568,7 +571,7 @@ int launch_q4_ring(const Q4Call& c, hipStream_t st) {
   a.wgs = quads < cus ? quads : cus;
   a.quads = quads / a.wgs, a.extra = quads % a.wgs;
   const int most = a.quads + (a.extra != 0);
-  const int least = (B * steps + 2 * kXAhead - 1) / (2 * kXAhead);
+  const int least = (LVQ_MAX_BATCH * steps + 2 * kXAhead - 1) / (2 * kXAhead);
   int nw = kQ4Waves;
   long long best = -1;
   auto consider = [&](auto waves) {  // a constant, so that its divisions are none

@@ -189,6 +189,23 @@ def test_batch_rows_equal_single_calls():
             assert np.array_equal(_run(d, x[b:b + 1], 1)[0], all4[b])
 
 
+@pytest.mark.parametrize("kind", ["f16", "i8", "e4m3"])
+@pytest.mark.parametrize("rows,cols", [(1024, 12288), (50, 12288), (8, 8192), (16, 16384)])
+def test_a_row_has_the_same_bits_in_every_batch(rows, cols, kind):
+    # few quads of wide rows: a row's steps are divided among the waves, and how
+    # many waves there are must not depend on the batch
+    d = synth.q4_matrix(rows, cols, 128, True)
+    if kind == "f16":
+        x, s = synth.activations(cols, 4, 7, rows=rows), None
+    else:
+        x, s = _x8(kind, 4, cols, 128, rows + cols)
+    single = np.concatenate([_run(d, x[b:b + 1], 1, kind, None if s is None else s[b:b + 1], 128)
+                             for b in range(4)])
+    for batch in (2, 3, 4):
+        got = _run(d, x[:batch], batch, kind, None if s is None else s[:batch], 128)
+        assert np.array_equal(got, single[:batch]), batch
+
+
 def test_infinite_x_is_nan_in_its_batch_row_only():
     rows, cols = 12, 96
     d = synth.q4_matrix(rows, cols, 32, False)
