@@ -25,9 +25,24 @@
 // bytes and the sums are exact 32-bit integers.
 //
 // The weights are the bytes (4.1 to 5 bits each): 4 flops per byte at batch 1.
-// Each wave streams 1 KiB of codes per step (4 rows x 256 contiguous bytes)
-// in chunks of four, two chunks in flight; x and the sums of x over every unit
-// sit in LDS.
+// Each wave streams 1 KiB of codes per step (4 rows x 256 contiguous bytes) in
+// chunks of four, two chunks in flight; x and the sums of x over every unit sit
+// in LDS.  Loads are counted: one of 64 lanes takes a CU's load unit 16 cycles
+// whatever it returns, so the scales and zeros of four steps come with one load
+// each (16 groups x 4 rows, or 16 x 2 bytes a row) and reach their lanes through
+// ds_bpermute, and no load is made for nothing.
+//
+// Measured (GPU time per call in a graph over rotating matrices, one MI355X; a
+// plain read of that many bytes runs at up to 6.4 TB/s, an empty launch 1.8 us):
+// 131072x4096 batch 1 45-47 us, 5.9-6.2 TB/s, bound by that read; 4096x12288
+// batch 1 7.8 us, 12288x4096 7.0 us (3.3 and 3.7 TB/s); 4096x12288 batch 4
+// 10.0-10.5 us, where each CU brings in 96 KiB of x; 4096x4096 3.8-4.3 us,
+// 1024x4096 3.3 us, bound by the launch and two round trips to memory.  Without
+// its arithmetic (a timing variant of an earlier step) 131072x4096 took 42.9 us
+// instead of 45.5-46.2, 12288x4096 6.0 instead of 7.3, 4096x12288 batch 4 8.1
+// instead of 10.2.  A full chunk's block holds 38-40 vector instructions per
+// step at batch 1, 28 of them unpack the codes and 8 are matrix products, and 5
+// LDS reads.
 
 #include <type_traits>
 
@@ -265,7 +280,9 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
 
   // 1. x: each wave takes pieces of 64 x 8 columns (one step of one batch row),
   //    kXAhead requested at a time; the weights' first loads go out behind the
-  //    last of them, so the wait for x does not include the weights
+  //    last of them, so the wait for x does not include the weights (with a
+  //    first chunk of weights ahead of x 4096x12288 at batch 4 takes 11.6 us
+  //    instead of 10.6, with both chunks 12.0)
   const int pieces = B * steps;  // of batch rows past the batch: zeros
   const int xgroups = groups_of(nunits, a.xshift);
   u32x4_t xv[kXAhead];

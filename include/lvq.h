@@ -14,6 +14,10 @@
  * the BPDQ bit-plane format (model card "Qwen3-8B - 2-bit BPDQ (packed)",
  * sections Format and Kernels), a bitshift trellis (blog "Qwen3.8-27B on a 12
  * GB card", section "A trellis is a codebook you walk"), and an fp16 matvec.
+ * Next to them stand the other operators of a decoder block: 4-bit weights with
+ * group scales for the projections that do not stand two bits (fp16 or 8-bit x),
+ * the root-mean-square norm of a residual stream and the gated activation, with
+ * fp16 or 8-bit outputs that the 4-bit arm reads.
  *
  * Conventions shared by every function.
  *   - Return value: LVQ_OK (0) or a negative LVQ_E_* code.  No exception or
