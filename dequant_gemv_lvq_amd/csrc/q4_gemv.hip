@@ -415,7 +415,10 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
 
   auto multiply = [&](u32x4_t q, uint32_t sz, int t) {
     const uint8_t* xt = xl + t * x_step_bytes(B, X);
-    const float s = f16_to_f32(sz), z = f16_to_f32(sz >> 16);
+    // e4m3: the codes' unit leaves with the scale (fp16 x: at the store), so that a
+    // small scale of x does not push the sum below fp32's normal numbers
+    const float s = f16_to_f32(sz) * (X == kQ4E4M3 ? 1.f / kCodeUnit : 1.f);
+    const float z = f16_to_f32(sz >> 16);
     const float* sx = sl + t * (kStepUnits * B);
     const float* tx = tl + t * (kStepUnits * B);
     float v[B];
@@ -458,8 +461,9 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
     }
 #pragma unroll
     for (int bb = 0; bb < B; ++bb) {
-      const float f = X == kQ4F16 ? s : s * tx[bb];
-      acc[bb] = __builtin_fmaf(f, v[bb], acc[bb]);
+      // the scale of x last: s times it may be below the normal numbers
+      if constexpr (X == kQ4F16) acc[bb] = __builtin_fmaf(s, v[bb], acc[bb]);
+      else acc[bb] = __builtin_fmaf(s * v[bb], tx[bb], acc[bb]);
     }
   };
   // lane 4 bb + i < 4 B: the sum of row i of the quad, batch row bb
@@ -476,7 +480,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   auto store = [&](int quad, float r) {
     const int row = quad * 4 + r4;
     if (ul < a.batch && row < a.rows)
-      a.y[(size_t)ul * a.rows + row] = X == kQ4I8 ? r : r * (1.f / kCodeUnit);
+      a.y[(size_t)ul * a.rows + row] = X == kQ4F16 ? r * (1.f / kCodeUnit) : r;
   };
 
   float own = 0.f;  // of a quad that starts in this wave and ends in a later one

@@ -153,6 +153,21 @@ def test_subnormal_and_large_x():
     _check(d, synth.fp16_bits(r.choice([-65504.0, 65504.0], (2, cols))), 2)
 
 
+@pytest.mark.parametrize("kind", ["i8", "e4m3"])
+@pytest.mark.parametrize("factor", [1.2e-36, 1e34])
+def test_scales_of_x_at_the_ends_of_fp32(kind, factor):
+    # scales from 1.2e-38 (normal numbers) to 4e32, weights' scales about 6e-5:
+    # the results are normal numbers, so nothing before them may be less precise
+    rows, cols = 100, 4096
+    for zeros in (False, True):
+        d = synth.q4_matrix(rows, cols, 128, zeros)
+        d["scale"] = synth.fp16_bits(og.f16(d["scale"]).astype(np.float32) * np.float32(2.0 ** -8))
+        x, s = _x8(kind, 2, cols, 128, 5)
+        s = (s * np.float32(factor)).astype(np.float32)
+        assert s.min() >= np.finfo(np.float32).tiny
+        _check(d, x, 2, kind, s, 128)
+
+
 def test_zero_scales_and_row_zero_x():
     rows, cols = 9, 256
     d = synth.q4_matrix(rows, cols, 64, True)
