@@ -36,7 +36,7 @@
 // plain read of that many bytes runs at up to 6.4 TB/s, an empty launch 1.8 us):
 // 131072x4096 batch 1 45-47 us, 5.9-6.2 TB/s, bound by that read; 4096x12288
 // batch 1 7.8 us, 12288x4096 7.0 us (3.3 and 3.7 TB/s); 4096x12288 batch 4
-// 10.0-10.5 us, where each CU brings in 96 KiB of x; 4096x4096 3.8-4.3 us,
+// 10.0-10.7 us, where each CU brings in 96 KiB of x; 4096x4096 3.8-4.3 us,
 // 1024x4096 3.3 us, bound by the launch and two round trips to memory.  Without
 // its arithmetic (a timing variant of an earlier step) 131072x4096 took 42.9 us
 // instead of 45.5-46.2, 12288x4096 6.0 instead of 7.3, 4096x12288 batch 4 8.1
