@@ -445,6 +445,16 @@ def _array(t, name, types, nbytes, dev):
     _refuse(t, name, types, nbytes, dev)
 
 
+def _in_32_bits(*values):
+    """Refuses integers that the library's 32-bit arguments do not hold: they would
+    arrive as other numbers than those the size checks were made with.  Called
+    where the values, or-ed together, do not fit 31 bits; negative ones are left to
+    the library's own checks."""
+    for v in values:
+        if not -2 ** 31 <= v < 2 ** 31:
+            _check(LVQ_E_SHAPE)
+
+
 def _n_groups(cols: int, group: int) -> int:
     return -(-cols // group) if group > 0 else 1
 
@@ -454,6 +464,8 @@ def q4_gemv(codes, scale, zero, group: int, rows: int, cols: int, x, y, batch: i
     """y = W x, W 4-bit codes with a scale (and a zero, or None for 8) per group
     of columns (32, 64, 128, 256, or 0: one per row); x fp16, y fp32."""
     group, rows, cols, batch = int(group), int(rows), int(cols), int(batch)
+    if (group | rows | cols | batch) >> 31:
+        _in_32_bits(group, rows, cols, batch)
     dev, stream = _here(stream)
     meta = rows * _n_groups(cols, group) * 2
     e = _lib.q4_gemv(_array(codes, "codes", _BYTES, rows * (-(-cols // 32) * 16), dev),
@@ -471,6 +483,8 @@ def q4_gemv_q8(codes, scale, zero, group: int, rows: int, cols: int, x, x_scale,
     scales, one per x_group columns of a batch row (0: one per batch row)."""
     group, rows, cols, batch = int(group), int(rows), int(cols), int(batch)
     x_group = int(x_group)
+    if (group | rows | cols | batch | x_group) >> 31:
+        _in_32_bits(group, rows, cols, batch, x_group)
     dev, stream = _here(stream)
     xp, xt = _typed(x, "x", _EIGHT, batch * cols, dev)  # its type says how to read it
     meta = rows * _n_groups(cols, group) * 2
@@ -521,6 +535,8 @@ def rms_norm(x, residual, weight, eps: float, out, residual_out=None, scale=None
     group = int(group)
     dev, stream = _here(stream)
     xp, xt, rows, cols, stride = _rows_of(x, "x", dev)
+    if (group | rows | cols) >> 31:
+        _in_32_bits(group, rows, cols)
     n = rows * cols
     rp = rop = wp = None
     rt = wt = LVQ_F32
@@ -553,6 +569,8 @@ def silu_mul(gate, up, out, scale=None, group: int = 0, stream=None):
     up_p, ut, urows, ucols, ustride = _rows_of(up, "up", dev)
     if ut != gt or urows != rows or ucols != cols or ustride != stride:
         raise ValueError("gate and up must have the same type, shape and row stride")
+    if (group | rows | cols) >> 31:
+        _in_32_bits(group, rows, cols)
     op, ot = _typed(out, "out", _OUTS, rows * cols, dev)
     e = _lib.lvq_silu_mul(gp, up_p, gt, stride, rows, cols, op, ot,
                           _array(scale, "scale", _F32, rows * _n_groups(cols, group) * 4, dev),

@@ -1,0 +1,96 @@
+"""What the binding checks before the library sees a call, on the CPU: host
+tensors stand in for device ones (device -1) and the library's entry points are
+replaced by ones that record the call, so nothing is launched."""
+import pytest
+
+import dequant_gemv_lvq_amd as lvq
+
+torch = pytest.importorskip("torch")
+
+
+class Recorder:
+    """Every entry point returns LVQ_OK and notes its name and arguments."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return lvq.LVQ_OK
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    rec = Recorder()
+    rec.lvq_strerror = lambda code: b"refused"
+    monkeypatch.setattr(lvq, "_lib", rec)
+    monkeypatch.setattr(lvq, "_here", lambda stream: (-1, 0))
+    return rec
+
+
+def _refused(library, call, **kw):
+    with pytest.raises(lvq.LvqError) as e:
+        call(**kw)
+    assert e.value.code == lvq.LVQ_E_SHAPE and not library.calls
+
+
+def _q4(**kw):
+    a = dict(codes=torch.zeros(8, 64, dtype=torch.uint8), scale=torch.zeros(8, 4).half(), zero=None,
+             group=32, rows=8, cols=128, x=torch.zeros(2, 128).half(), y=torch.zeros(2, 8), batch=2)
+    a.update(kw)
+    return lvq.q4_gemv(**a)
+
+
+def _q8(**kw):
+    a = dict(codes=torch.zeros(8, 64, dtype=torch.uint8), scale=torch.zeros(8, 4).half(), zero=None,
+             group=32, rows=8, cols=128, x=torch.zeros(2, 128, dtype=torch.int8),
+             x_scale=torch.zeros(2, 2), x_group=64, y=torch.zeros(2, 8), batch=2)
+    a.update(kw)
+    return lvq.q4_gemv_q8(**a)
+
+
+def _norm(**kw):
+    a = dict(x=torch.zeros(8, 128), residual=torch.zeros(8, 128), weight=torch.zeros(128), eps=1e-6,
+             out=torch.zeros(8, 128, dtype=torch.int8), residual_out=torch.zeros(8, 128),
+             scale=torch.zeros(8, 4), group=32)
+    a.update(kw)
+    return lvq.rms_norm(**a)
+
+
+def _silu(**kw):
+    a = dict(gate=torch.zeros(8, 128), up=torch.zeros(8, 128),
+             out=torch.zeros(8, 128, dtype=torch.int8), scale=torch.zeros(8, 4), group=32)
+    a.update(kw)
+    return lvq.silu_mul(**a)
+
+
+@pytest.mark.parametrize("call", [_q4, _q8, _norm, _silu])
+def test_the_calls_that_are_varied_below_pass(library, call):
+    call()
+    assert len(library.calls) == 1
+
+
+@pytest.mark.parametrize("wrap", [2 ** 32, -2 ** 32])
+def test_integers_past_32_bits_are_refused(library, wrap):
+    """The library takes 32-bit integers: a number that wraps to another one would
+    pass the size checks as the one and be used as the other."""
+    for name, value in (("group", 32), ("rows", 8), ("cols", 128), ("batch", 2)):
+        for call in (_q4, _q8):
+            # one scale per row is what a group of 2^32 + 32 needs
+            _refused(library, call, **{name: value + wrap, "scale": torch.zeros(8, 1).half()})
+    _refused(library, _q8, x_group=64 + wrap, x_scale=torch.zeros(2, 1))
+    for call in (_norm, _silu):
+        _refused(library, call, group=32 + wrap, scale=torch.zeros(8, 1))
+    for value in (2 ** 31, -2 ** 31 - 1, 2 ** 63):
+        _refused(library, _q4, group=value)
+
+
+def test_more_rows_than_32_bits_are_refused(library):
+    """2^32 empty rows: as 32 bits no rows at all."""
+    many = torch.empty(2 ** 32, 0)
+    _refused(library, _norm, x=many, residual=None, residual_out=None,
+             out=torch.empty(0, dtype=torch.int8), scale=torch.empty(0), weight=None)
+    _refused(library, _silu, gate=many, up=many, out=torch.empty(0, dtype=torch.int8),
+             scale=torch.empty(0))
