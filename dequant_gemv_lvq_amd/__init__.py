@@ -415,34 +415,42 @@ def _here(stream):
     return dev, _stream(stream)
 
 
-def _refuse(t, name, types, nbytes, dev):
+def _refuse(t, name, types, nbytes, dev, pitch):
     if not isinstance(t, _Tensor):
         raise TypeError("%s must be a tensor on the GPU" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be on the GPU" % name)
     if t.get_device() != dev:
-        raise ValueError("%s is on another device than the current one" % name)
+        raise ValueError("%s is on another device than the current one" % name if t.is_cuda
+                         else "%s must be on the GPU" % name)
     if t.dtype not in types:
         raise ValueError("%s has type %s" % (name, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    raise LvqError(LVQ_E_SHAPE, "%s: %s holds %d of %d bytes" % (
-        strerror(LVQ_E_SHAPE), name, t.nbytes, nbytes))
+    raise LvqError(LVQ_E_SHAPE, "%s: %s of shape %s holds %d of %d bytes in rows of %d" % (
+        strerror(LVQ_E_SHAPE), name, tuple(t.shape), t.nbytes, nbytes, pitch))
 
 
-def _array(t, name, types, nbytes, dev):
-    """Address of a contiguous tensor of one of `types`, on device dev, of at
-    least nbytes bytes (checked, so that the kernel never reads or writes past
-    it), of an int (a raw address, not checked) or of None."""
+def _array(t, name, types, rows, pitch, dev):
+    """Address of a contiguous tensor of one of `types`, on device dev, that holds
+    at least `rows` rows of `pitch` bytes (checked, so that the kernel never reads
+    or writes past it): of such rows, or flat.  Of an int (a raw address, not
+    checked) or of None."""
     if t is None or t.__class__ is int:
         return t
     try:
-        if (t.dtype in types and t.get_device() == dev and t.nbytes >= nbytes
-                and t.is_contiguous()):
+        if (t.dtype in types and t.get_device() == dev and t.nbytes >= rows * pitch
+                and t.is_contiguous()
+                and (rows < 2 or _of_rows(t.shape, pitch, t.itemsize))):
             return t.data_ptr()
     except AttributeError:
         pass
-    _refuse(t, name, types, nbytes, dev)
+    _refuse(t, name, types, rows * pitch, dev, pitch)
+
+
+def _of_rows(shape, pitch, size):
+    """Whether a shape's last dimension is a row of `pitch` bytes.  Flat shapes pass,
+    and any where rows are empty (as any shape of a single row does: it lies the
+    same way)."""
+    return len(shape) < 2 or shape[-1] * size == pitch or not pitch
 
 
 def _in_32_bits(*values):
@@ -462,17 +470,19 @@ def _n_groups(cols: int, group: int) -> int:
 def q4_gemv(codes, scale, zero, group: int, rows: int, cols: int, x, y, batch: int = 1,
             stream=None):
     """y = W x, W 4-bit codes with a scale (and a zero, or None for 8) per group
-    of columns (32, 64, 128, 256, or 0: one per row); x fp16, y fp32."""
+    of columns (32, 64, 128, 256, or 0: one per row); x fp16, y fp32.  Every array
+    is contiguous, flat or of its rows (codes, scale, zero: of the matrix; x, y: of
+    the batch), and may hold more of them."""
     group, rows, cols, batch = int(group), int(rows), int(cols), int(batch)
     if (group | rows | cols | batch) >> 31:
         _in_32_bits(group, rows, cols, batch)
     dev, stream = _here(stream)
-    meta = rows * _n_groups(cols, group) * 2
-    e = _lib.q4_gemv(_array(codes, "codes", _BYTES, rows * (-(-cols // 32) * 16), dev),
-                     _array(scale, "scale", _F16_BITS, meta, dev),
-                     _array(zero, "zero", _F16_BITS, meta, dev), group, rows, cols,
-                     _array(x, "x", _F16_BITS, batch * cols * 2, dev),
-                     _array(y, "y", _F32, batch * rows * 4, dev), batch, stream)
+    meta = _n_groups(cols, group) * 2
+    e = _lib.q4_gemv(_array(codes, "codes", _BYTES, rows, -(-cols // 32) * 16, dev),
+                     _array(scale, "scale", _F16_BITS, rows, meta, dev),
+                     _array(zero, "zero", _F16_BITS, rows, meta, dev), group, rows, cols,
+                     _array(x, "x", _F16_BITS, batch, cols * 2, dev),
+                     _array(y, "y", _F32, batch, rows * 4, dev), batch, stream)
     if e:
         _check(e)
 
@@ -486,14 +496,13 @@ def q4_gemv_q8(codes, scale, zero, group: int, rows: int, cols: int, x, x_scale,
     if (group | rows | cols | batch | x_group) >> 31:
         _in_32_bits(group, rows, cols, batch, x_group)
     dev, stream = _here(stream)
-    xp, xt = _typed(x, "x", _EIGHT, batch * cols, dev)  # its type says how to read it
-    meta = rows * _n_groups(cols, group) * 2
-    e = _lib.q4_gemv_q8(_array(codes, "codes", _BYTES, rows * (-(-cols // 32) * 16), dev),
-                        _array(scale, "scale", _F16_BITS, meta, dev),
-                        _array(zero, "zero", _F16_BITS, meta, dev), group, rows, cols, xp, xt,
-                        _array(x_scale, "x_scale", _F32, batch * _n_groups(cols, x_group) * 4,
-                               dev),
-                        x_group, _array(y, "y", _F32, batch * rows * 4, dev), batch, stream)
+    xp, xt = _typed(x, "x", _EIGHT, batch, cols, dev)  # its type says how to read it
+    meta = _n_groups(cols, group) * 2
+    e = _lib.q4_gemv_q8(_array(codes, "codes", _BYTES, rows, -(-cols // 32) * 16, dev),
+                        _array(scale, "scale", _F16_BITS, rows, meta, dev),
+                        _array(zero, "zero", _F16_BITS, rows, meta, dev), group, rows, cols, xp, xt,
+                        _array(x_scale, "x_scale", _F32, batch, _n_groups(cols, x_group) * 4, dev),
+                        x_group, _array(y, "y", _F32, batch, rows * 4, dev), batch, stream)
     if e:
         _check(e)
 
@@ -502,7 +511,7 @@ def _rows_of(t, name, dev):
     """(address, type, rows, cols, row stride) of a 2-D tensor of floats whose
     columns are adjacent."""
     if not isinstance(t, _Tensor) or t.dtype not in _FLOATS or t.get_device() != dev:
-        _refuse(t, name, _FLOATS, 0, dev)
+        _refuse(t, name, _FLOATS, 0, dev, 0)
     shape, strides = t.shape, t.stride()
     if len(shape) != 2:
         raise ValueError("%s must have two dimensions, rows and columns" % name)
@@ -512,16 +521,18 @@ def _rows_of(t, name, dev):
     return t.data_ptr(), _TYPES[t.dtype], rows, cols, strides[0] if rows > 1 else cols
 
 
-def _typed(t, name, types, count, dev):
-    """(address, type) of a contiguous tensor of at least count values."""
+def _typed(t, name, types, rows, cols, dev):
+    """(address, type) of a contiguous tensor that holds at least `rows` rows of
+    `cols` values: of such rows, or flat."""
     try:
         kind = t.dtype
-        if (kind in types and t.get_device() == dev and t.numel() >= count
-                and t.is_contiguous()):
+        if (kind in types and t.get_device() == dev and t.numel() >= rows * cols
+                and t.is_contiguous() and (rows < 2 or _of_rows(t.shape, cols, 1))):
             return t.data_ptr(), _TYPES[kind]
     except AttributeError:
         pass
-    _refuse(t, name, types, count * getattr(t, "itemsize", 1), dev)
+    size = getattr(t, "itemsize", 1)
+    _refuse(t, name, types, rows * cols * size, dev, cols * size)
 
 
 def rms_norm(x, residual, weight, eps: float, out, residual_out=None, scale=None, group: int = 0,
@@ -529,31 +540,33 @@ def rms_norm(x, residual, weight, eps: float, out, residual_out=None, scale=None
     """out = h * rsqrt(mean(h^2) + eps) * weight over the columns of h = x +
     residual, and residual_out = h.  x is a 2-D tensor (rows may be strided) of
     fp32, fp16 or bf16; residual and residual_out (which may be the same tensor)
-    are contiguous and of one such type, weight of any; residual, weight and
-    residual_out may be None.  out: fp16, or int8 / float8_e4m3fn with scale, one
-    fp32 per `group` columns of a row (32, 64, 128, 256, or 0: one per row)."""
+    are contiguous and of one such type, weight (one row) of any; residual, weight
+    and residual_out may be None.  out: fp16, or int8 / float8_e4m3fn with scale, one
+    fp32 per `group` columns of a row (32, 64, 128, 256, or 0: one per row).
+    residual, residual_out, out and scale are flat or of x's rows."""
     group = int(group)
     dev, stream = _here(stream)
     xp, xt, rows, cols, stride = _rows_of(x, "x", dev)
     if (group | rows | cols) >> 31:
         _in_32_bits(group, rows, cols)
-    n = rows * cols
     rp = rop = wp = None
     rt = wt = LVQ_F32
     if residual is not None:
-        rp, rt = _typed(residual, "residual", _FLOATS, n, dev)
+        rp, rt = _typed(residual, "residual", _FLOATS, rows, cols, dev)
     if residual_out is residual:
         rop = rp
     elif residual_out is not None:
-        rop, rot = _typed(residual_out, "residual_out", _FLOATS, n, dev)
+        rop, rot = _typed(residual_out, "residual_out", _FLOATS, rows, cols, dev)
         if residual is not None and rot != rt:
             raise ValueError("residual and residual_out must have the same type")
         rt = rot
     if weight is not None:
-        wp, wt = _typed(weight, "weight", _FLOATS, cols, dev)
-    op, ot = _typed(out, "out", _OUTS, n, dev)
+        wp, wt = _typed(weight, "weight", _FLOATS, 1, cols, dev)
+        if cols and weight.numel() != cols:
+            _refuse(weight, "weight", _FLOATS, cols * weight.itemsize, dev, cols * weight.itemsize)
+    op, ot = _typed(out, "out", _OUTS, rows, cols, dev)
     e = _lib.lvq_rms_norm(xp, xt, stride, rp, rt, rop, wp, wt, eps, rows, cols, op, ot,
-                          _array(scale, "scale", _F32, rows * _n_groups(cols, group) * 4, dev),
+                          _array(scale, "scale", _F32, rows, _n_groups(cols, group) * 4, dev),
                           group, stream)
     if e:
         _check(e)
@@ -571,9 +584,9 @@ def silu_mul(gate, up, out, scale=None, group: int = 0, stream=None):
         raise ValueError("gate and up must have the same type, shape and row stride")
     if (group | rows | cols) >> 31:
         _in_32_bits(group, rows, cols)
-    op, ot = _typed(out, "out", _OUTS, rows * cols, dev)
+    op, ot = _typed(out, "out", _OUTS, rows, cols, dev)
     e = _lib.lvq_silu_mul(gp, up_p, gt, stride, rows, cols, op, ot,
-                          _array(scale, "scale", _F32, rows * _n_groups(cols, group) * 4, dev),
+                          _array(scale, "scale", _F32, rows, _n_groups(cols, group) * 4, dev),
                           group, stream)
     if e:
         _check(e)

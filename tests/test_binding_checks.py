@@ -36,6 +36,13 @@ def _refused(library, call, **kw):
     assert e.value.code == lvq.LVQ_E_SHAPE and not library.calls
 
 
+def _refused_shape(library, call, **kw):
+    n = len(library.calls)
+    with pytest.raises(lvq.LvqError) as e:
+        call(**kw)
+    assert e.value.code == lvq.LVQ_E_SHAPE and len(library.calls) == n
+
+
 def _q4(**kw):
     a = dict(codes=torch.zeros(8, 64, dtype=torch.uint8), scale=torch.zeros(8, 4).half(), zero=None,
              group=32, rows=8, cols=128, x=torch.zeros(2, 128).half(), y=torch.zeros(2, 8), batch=2)
@@ -94,3 +101,61 @@ def test_more_rows_than_32_bits_are_refused(library):
              out=torch.empty(0, dtype=torch.int8), scale=torch.empty(0), weight=None)
     _refused(library, _silu, gate=many, up=many, out=torch.empty(0, dtype=torch.int8),
              scale=torch.empty(0))
+
+
+def test_shapes_are_checked_and_not_only_sizes(library):
+    """A tensor of two or more dimensions has as many values in its last one as the
+    operator's rows have; a flat one is taken as it lies."""
+    f16, i8 = torch.float16, torch.int8
+    for call in (_q4, _q8):
+        _refused_shape(library, call, codes=torch.zeros(64, 8, dtype=torch.uint8))
+        _refused_shape(library, call, scale=torch.zeros(4, 8, dtype=f16))
+        _refused_shape(library, call, zero=torch.zeros(4, 8, dtype=f16))
+        _refused_shape(library, call, y=torch.zeros(8, 2))
+        call(codes=torch.zeros(8, 16, dtype=torch.int32), y=torch.zeros(16))
+        call(scale=torch.zeros(32, dtype=f16), zero=torch.zeros(8, 4, dtype=f16))
+        call(scale=torch.zeros(8, 1, dtype=f16), group=0)
+        assert len(library.calls) == 3
+        library.calls.clear()
+    _refused_shape(library, _q4, x=torch.zeros(128, 2, dtype=f16))
+    _refused_shape(library, _q8, x=torch.zeros(128, 2, dtype=i8))
+    _refused_shape(library, _q8, x_scale=torch.zeros(1, 4))
+    for name, shape in (("residual", (128, 8)), ("residual_out", (128, 8)), ("residual", (4, 256)),
+                        ("weight", (129,)), ("weight", (8, 128)), ("weight", (127,))):
+        _refused_shape(library, _norm, **{name: torch.zeros(shape)})
+    for call in (_norm, _silu):
+        _refused_shape(library, call, out=torch.zeros(128, 8, dtype=i8))
+        _refused_shape(library, call, scale=torch.zeros(4, 8))
+        call(out=torch.zeros(1024, dtype=i8), scale=torch.zeros(40))
+        call(out=torch.zeros(9, 128, dtype=i8))  # room for more rows
+        call(scale=torch.zeros(8), group=0)
+        call(out=torch.zeros(2, 4, 128, dtype=i8))
+    _norm(weight=torch.zeros(1, 128))
+    assert len(library.calls) == 9
+
+
+def test_a_single_row_may_have_any_shape(library):
+    _q4(batch=1, x=torch.zeros(128, 1).half(), y=torch.zeros(8, 1))
+    _norm(x=torch.zeros(1, 128), residual=torch.zeros(128, 1), residual_out=None,
+          out=torch.zeros(128, 1, dtype=torch.int8), scale=torch.zeros(4, 1))
+    assert len(library.calls) == 2
+
+
+def test_shapes_of_empty_operands_are_free(library):
+    _silu(gate=torch.zeros(8, 0), up=torch.zeros(8, 0), out=torch.zeros(0, 8, dtype=torch.int8),
+          scale=torch.zeros(8, 3))
+    _norm(x=torch.zeros(0, 128), residual=None, residual_out=None,
+          out=torch.zeros(0, dtype=torch.int8), scale=torch.zeros(0))
+    assert len(library.calls) == 2
+
+
+def test_short_and_foreign_tensors_are_refused(library):
+    _refused_shape(library, _q4, y=torch.zeros(15))
+    for call, name, t in ((_q4, "x", torch.zeros(2, 256).half()[:, :128]),
+                          (_q4, "y", torch.zeros(2, 8).half()),
+                          (_norm, "weight", torch.zeros(256)[::2]),
+                          (_norm, "out", torch.zeros(8, 128)),
+                          (_silu, "out", torch.zeros(128, 8, dtype=torch.int8).t())):
+        with pytest.raises(ValueError):
+            call(**{name: t})
+    assert not library.calls
