@@ -384,22 +384,28 @@ def fp16_gemv(w, rows: int, cols: int, x, y, batch: int = 1, stream=None):
 try:
     import torch as _torch
     _Tensor = _torch.Tensor
-    _TYPES = {_torch.float32: LVQ_F32, _torch.float16: LVQ_F16, _torch.bfloat16: LVQ_BF16,
-              _torch.int8: LVQ_I8, _torch.float8_e4m3fn: LVQ_E4M3}
-    # fp16 bit patterns are also accepted as 16-bit integers, codes as any bytes
-    _F16_BITS = (_torch.float16, _torch.int16, _torch.uint16)
-    _BYTES = (_torch.uint8, _torch.int8, _torch.int32, _torch.uint32)
-    _F32 = (_torch.float32,)
-    _FLOATS = (_torch.float32, _torch.float16, _torch.bfloat16)
-    _EIGHT = (_torch.int8, _torch.float8_e4m3fn)
-    _OUTS = (_torch.float16,) + _EIGHT
 except ImportError:  # the functions below that read a type from a tensor need it
     _torch = None
 
     class _Tensor:
         pass
-    _TYPES = {}
-    _F16_BITS = _BYTES = _F32 = _FLOATS = _EIGHT = _OUTS = ()
+
+
+def _types(*names):
+    """Those of torch's element types that the installed version has."""
+    return tuple(t for t in (getattr(_torch, n, None) for n in names) if t is not None)
+
+
+_TYPES = {t: code for name, code in (("float32", LVQ_F32), ("float16", LVQ_F16),
+                                     ("bfloat16", LVQ_BF16), ("int8", LVQ_I8),
+                                     ("float8_e4m3fn", LVQ_E4M3)) for t in _types(name)}
+# fp16 bit patterns are also accepted as 16-bit integers, codes as any bytes
+_F16_BITS = _types("float16", "int16", "uint16")
+_BYTES = _types("uint8", "int8", "int32", "uint32")
+_F32 = _types("float32")
+_FLOATS = _types("float32", "float16", "bfloat16")
+_EIGHT = _types("int8", "float8_e4m3fn")
+_OUTS = _types("float16") + _EIGHT
 
 
 def _here(stream):

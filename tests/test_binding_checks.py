@@ -1,11 +1,17 @@
 """What the binding checks before the library sees a call, on the CPU: host
 tensors stand in for device ones (device -1) and the library's entry points are
 replaced by ones that record the call, so nothing is launched."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 import dequant_gemv_lvq_amd as lvq
 
 torch = pytest.importorskip("torch")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 class Recorder:
@@ -159,3 +165,16 @@ def test_short_and_foreign_tensors_are_refused(library):
         with pytest.raises(ValueError):
             call(**{name: t})
     assert not library.calls
+
+
+def test_import_needs_no_type_that_torch_lacks():
+    """A torch without the newer element types still imports the package and keeps
+    the types it has."""
+    code = ("import torch\n"
+            "for n in ('uint16', 'uint32', 'float8_e4m3fn'):\n"
+            "    delattr(torch, n)\n"
+            "import dequant_gemv_lvq_amd as lvq\n"
+            "assert lvq._EIGHT == (torch.int8,) and lvq._F16_BITS == (torch.float16, torch.int16)\n"
+            "assert lvq._TYPES[torch.bfloat16] == lvq.LVQ_BF16 and None not in lvq._TYPES\n"
+            "assert lvq.layout_bytes(1, 24) > 0\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
