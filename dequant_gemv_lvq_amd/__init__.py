@@ -416,8 +416,12 @@ def _here(stream):
         dev = _torch._C._cuda_getDevice()
         if stream is None:
             return dev, _torch._C._cuda_getCurrentRawStream(dev)
-    except Exception:
-        dev = -2
+    except (AttributeError, RuntimeError):  # not in this torch, or no GPU
+        if _torch is None or not _torch.cuda.is_available():
+            return -2, None if stream is None else _stream(stream)
+        dev = _torch.cuda.current_device()
+        if stream is None:
+            stream = _torch.cuda.current_stream()
     return dev, _stream(stream)
 
 

@@ -178,3 +178,34 @@ def test_import_needs_no_type_that_torch_lacks():
             "assert lvq._TYPES[torch.bfloat16] == lvq.LVQ_BF16 and None not in lvq._TYPES\n"
             "assert lvq.layout_bytes(1, 24) > 0\n")
     subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
+
+
+class _Stream:
+    cuda_stream = 77
+
+
+def test_device_and_stream_without_torchs_private_functions(monkeypatch):
+    """Where torch's private functions are missing the public ones answer, and an
+    error of theirs is raised and not taken for another device."""
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: _Stream)
+    assert lvq._here(None) == (3, 77) and lvq._here(5) == (3, 5) and lvq._here(_Stream) == (3, 77)
+
+    def broken(*a):
+        raise RuntimeError("a HIP error")
+    monkeypatch.setattr(torch.cuda, "current_stream", broken)
+    with pytest.raises(RuntimeError, match="a HIP error"):
+        lvq._here(None)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: False)
+    assert lvq._here(None) == (-2, None) and lvq._here(5) == (-2, 5)
+
+
+def test_an_unexpected_error_of_the_private_functions_is_raised(monkeypatch):
+    def broken():
+        raise MemoryError
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", broken, raising=False)
+    with pytest.raises(MemoryError):
+        lvq._here(None)
