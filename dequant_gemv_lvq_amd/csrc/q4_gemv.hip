@@ -669,7 +669,7 @@ int q4_run(const uint8_t* codes, const uint16_t* scale, const uint16_t* zero, in
   if (gs < 0 || xs < 0) return LVQ_E_SHAPE;
   const int e = check_batch(batch);
   if (e) return e;
-  if (!y || (rows && cols && (!codes || !scale || !x || (xkind != kQ4F16 && !x_scale))))
+  if (rows && (!y || (cols && (!codes || !scale || !x || (xkind != kQ4F16 && !x_scale)))))
     return LVQ_E_NULL;
   if (!aligned16(codes) || !aligned16(scale) || !aligned16(zero) || !aligned16(x) ||
       !aligned16(x_scale) || !aligned16(y))

@@ -209,3 +209,16 @@ def test_an_unexpected_error_of_the_private_functions_is_raised(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", broken, raising=False)
     with pytest.raises(MemoryError):
         lvq._here(None)
+
+
+@pytest.mark.parametrize("entry", ["q4_gemv", "q4_gemv_q8"])
+def test_no_rows_need_no_y(entry):
+    """An empty tensor has no address: with rows == 0 the library reads and writes
+    nothing and asks for no pointer."""
+    lib = lvq.library()
+    x8 = (0, lvq.LVQ_I8, 0, 0) if entry == "q4_gemv_q8" else (0,)
+    assert getattr(lib, entry)(None, None, None, 32, 0, 64, *x8, None, 1, None) == lvq.LVQ_OK
+    assert getattr(lib, entry)(None, None, None, 32, 0, 0, *x8, None, 1, None) == lvq.LVQ_OK
+    assert getattr(lib, entry)(None, None, None, 32, 1, 0, *x8, None, 1, None) == lvq.LVQ_E_NULL
+    assert getattr(lib, entry)(None, None, None, 33, 0, 64, *x8, None, 1, None) == lvq.LVQ_E_SHAPE
+    assert getattr(lib, entry)(None, None, None, 32, 0, 64, *x8, None, 5, None) == lvq.LVQ_E_BATCH
