@@ -401,7 +401,8 @@ _TYPES = {t: code for name, code in (("float32", LVQ_F32), ("float16", LVQ_F16),
                                      ("float8_e4m3fn", LVQ_E4M3)) for t in _types(name)}
 # fp16 bit patterns are also accepted as 16-bit integers, codes as any bytes
 _F16_BITS = _types("float16", "int16", "uint16")
-_BYTES = _types("uint8", "int8", "int32", "uint32")
+_BYTES = _types("uint8", "int8")
+_WORDS = _types("int32", "uint32")
 _F32 = _types("float32")
 _FLOATS = _types("float32", "float16", "bfloat16")
 _EIGHT = _types("int8", "float8_e4m3fn")
@@ -425,7 +426,7 @@ def _here(stream):
     return dev, _stream(stream)
 
 
-def _refuse(t, name, types, nbytes, dev, pitch):
+def _refuse(t, name, types, rows, width, dev):
     if not isinstance(t, _Tensor):
         raise TypeError("%s must be a tensor on the GPU" % name)
     if t.get_device() != dev:
@@ -435,32 +436,53 @@ def _refuse(t, name, types, nbytes, dev, pitch):
         raise ValueError("%s has type %s" % (name, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    raise LvqError(LVQ_E_SHAPE, "%s: %s of shape %s holds %d of %d bytes in rows of %d" % (
-        strerror(LVQ_E_SHAPE), name, tuple(t.shape), t.nbytes, nbytes, pitch))
+    raise LvqError(LVQ_E_SHAPE, "%s: %s of shape %s for %d rows of %d values" % (
+        strerror(LVQ_E_SHAPE), name, tuple(t.shape), rows, width))
 
 
-def _array(t, name, types, rows, pitch, dev):
-    """Address of a contiguous tensor of one of `types`, on device dev, that holds
-    at least `rows` rows of `pitch` bytes (checked, so that the kernel never reads
-    or writes past it): of such rows, or flat.  Of an int (a raw address, not
-    checked) or of None."""
-    if t is None or t.__class__ is int:
-        return t
+def _array(t, name, types, rows, width, dev):
+    """Address of a contiguous tensor of one of `types` (all of one size), on device
+    dev, that holds at least `rows` rows of `width` values (checked, so that the
+    kernel never reads or writes past it): of such rows, or flat.  Of an int (a raw
+    address, not checked) or of None."""
+    if t is None:
+        return None
     try:
-        if (t.dtype in types and t.get_device() == dev and t.nbytes >= rows * pitch
-                and t.is_contiguous()
-                and (rows < 2 or _of_rows(t.shape, pitch, t.itemsize))):
+        # the usual case first, in as few of torch's calls as it takes
+        if (t.dtype in types and t.get_device() == dev and t.shape == (rows, width)
+                and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
+        if t.__class__ is int:
+            return t
+    if not _holds(t, types, rows, width, dev):
+        _refuse(t, name, types, rows, width, dev)
+    return t.data_ptr()
+
+
+def _holds(t, types, rows, width, dev):
+    """Whether _array() takes a tensor of another shape than rows by width: a flat
+    one, more rows or more dimensions with the same last one, any where there is
+    just one row (it lies the same way in any shape) or nothing in the rows."""
+    if (not isinstance(t, _Tensor) or t.dtype not in types or t.get_device() != dev
+            or not t.is_contiguous() or t.numel() < rows * width):
+        return False
+    shape = t.shape
+    return rows < 2 or len(shape) < 2 or shape[-1] == width or not width
+
+
+def _codes(t, rows, units, dev):
+    """_array() of 4-bit codes, `units` units of 16 bytes a row: as bytes or as 32-bit
+    words."""
+    try:
+        if (t.dtype in _BYTES and t.get_device() == dev and t.shape == (rows, units * 16)
+                and t.is_contiguous()):
+            return t.data_ptr()
+        if t.dtype in _WORDS:
+            return _array(t, "codes", _WORDS, rows, units * 4, dev)
+    except AttributeError:
         pass
-    _refuse(t, name, types, rows * pitch, dev, pitch)
-
-
-def _of_rows(shape, pitch, size):
-    """Whether a shape's last dimension is a row of `pitch` bytes.  Flat shapes pass,
-    and any where rows are empty (as any shape of a single row does: it lies the
-    same way)."""
-    return len(shape) < 2 or shape[-1] * size == pitch or not pitch
+    return _array(t, "codes", _BYTES, rows, units * 16, dev)
 
 
 def _in_32_bits(*values):
@@ -487,12 +509,12 @@ def q4_gemv(codes, scale, zero, group: int, rows: int, cols: int, x, y, batch: i
     if (group | rows | cols | batch) >> 31:
         _in_32_bits(group, rows, cols, batch)
     dev, stream = _here(stream)
-    meta = _n_groups(cols, group) * 2
-    e = _lib.q4_gemv(_array(codes, "codes", _BYTES, rows, -(-cols // 32) * 16, dev),
-                     _array(scale, "scale", _F16_BITS, rows, meta, dev),
-                     _array(zero, "zero", _F16_BITS, rows, meta, dev), group, rows, cols,
-                     _array(x, "x", _F16_BITS, batch, cols * 2, dev),
-                     _array(y, "y", _F32, batch, rows * 4, dev), batch, stream)
+    n = _n_groups(cols, group)
+    e = _lib.q4_gemv(_codes(codes, rows, -(-cols // 32), dev),
+                     _array(scale, "scale", _F16_BITS, rows, n, dev),
+                     _array(zero, "zero", _F16_BITS, rows, n, dev), group, rows, cols,
+                     _array(x, "x", _F16_BITS, batch, cols, dev),
+                     _array(y, "y", _F32, batch, rows, dev), batch, stream)
     if e:
         _check(e)
 
@@ -507,12 +529,12 @@ def q4_gemv_q8(codes, scale, zero, group: int, rows: int, cols: int, x, x_scale,
         _in_32_bits(group, rows, cols, batch, x_group)
     dev, stream = _here(stream)
     xp, xt = _typed(x, "x", _EIGHT, batch, cols, dev)  # its type says how to read it
-    meta = _n_groups(cols, group) * 2
-    e = _lib.q4_gemv_q8(_array(codes, "codes", _BYTES, rows, -(-cols // 32) * 16, dev),
-                        _array(scale, "scale", _F16_BITS, rows, meta, dev),
-                        _array(zero, "zero", _F16_BITS, rows, meta, dev), group, rows, cols, xp, xt,
-                        _array(x_scale, "x_scale", _F32, batch, _n_groups(cols, x_group) * 4, dev),
-                        x_group, _array(y, "y", _F32, batch, rows * 4, dev), batch, stream)
+    n = _n_groups(cols, group)
+    e = _lib.q4_gemv_q8(_codes(codes, rows, -(-cols // 32), dev),
+                        _array(scale, "scale", _F16_BITS, rows, n, dev),
+                        _array(zero, "zero", _F16_BITS, rows, n, dev), group, rows, cols, xp, xt,
+                        _array(x_scale, "x_scale", _F32, batch, _n_groups(cols, x_group), dev),
+                        x_group, _array(y, "y", _F32, batch, rows, dev), batch, stream)
     if e:
         _check(e)
 
@@ -521,7 +543,7 @@ def _rows_of(t, name, dev):
     """(address, type, rows, cols, row stride) of a 2-D tensor of floats whose
     columns are adjacent."""
     if not isinstance(t, _Tensor) or t.dtype not in _FLOATS or t.get_device() != dev:
-        _refuse(t, name, _FLOATS, 0, dev, 0)
+        _refuse(t, name, _FLOATS, 0, 0, dev)
     shape, strides = t.shape, t.stride()
     if len(shape) != 2:
         raise ValueError("%s must have two dimensions, rows and columns" % name)
@@ -531,18 +553,31 @@ def _rows_of(t, name, dev):
     return t.data_ptr(), _TYPES[t.dtype], rows, cols, strides[0] if rows > 1 else cols
 
 
-def _typed(t, name, types, rows, cols, dev):
-    """(address, type) of a contiguous tensor that holds at least `rows` rows of
-    `cols` values: of such rows, or flat."""
+def _typed(t, name, types, rows, width, dev):
+    """(address, type) of a tensor that _array() takes."""
     try:
         kind = t.dtype
-        if (kind in types and t.get_device() == dev and t.numel() >= rows * cols
-                and t.is_contiguous() and (rows < 2 or _of_rows(t.shape, cols, 1))):
+        if (kind in types and t.get_device() == dev and t.shape == (rows, width)
+                and t.is_contiguous()):
             return t.data_ptr(), _TYPES[kind]
     except AttributeError:
         pass
-    size = getattr(t, "itemsize", 1)
-    _refuse(t, name, types, rows * cols * size, dev, cols * size)
+    if not _holds(t, types, rows, width, dev):
+        _refuse(t, name, types, rows, width, dev)
+    return t.data_ptr(), _TYPES[t.dtype]
+
+
+def _row(t, name, types, width, dev):
+    """(address, type) of a tensor that is one row of `width` values, no longer."""
+    try:
+        if (t.dtype in types and t.get_device() == dev and t.shape == (width,)
+                and t.is_contiguous()):
+            return t.data_ptr(), _TYPES[t.dtype]
+    except AttributeError:
+        pass
+    if not _holds(t, types, 1, width, dev) or (width and t.numel() != width):
+        _refuse(t, name, types, 1, width, dev)
+    return t.data_ptr(), _TYPES[t.dtype]
 
 
 def rms_norm(x, residual, weight, eps: float, out, residual_out=None, scale=None, group: int = 0,
@@ -571,12 +606,10 @@ def rms_norm(x, residual, weight, eps: float, out, residual_out=None, scale=None
             raise ValueError("residual and residual_out must have the same type")
         rt = rot
     if weight is not None:
-        wp, wt = _typed(weight, "weight", _FLOATS, 1, cols, dev)
-        if cols and weight.numel() != cols:
-            _refuse(weight, "weight", _FLOATS, cols * weight.itemsize, dev, cols * weight.itemsize)
+        wp, wt = _row(weight, "weight", _FLOATS, cols, dev)
     op, ot = _typed(out, "out", _OUTS, rows, cols, dev)
     e = _lib.lvq_rms_norm(xp, xt, stride, rp, rt, rop, wp, wt, eps, rows, cols, op, ot,
-                          _array(scale, "scale", _F32, rows, _n_groups(cols, group) * 4, dev),
+                          _array(scale, "scale", _F32, rows, _n_groups(cols, group), dev),
                           group, stream)
     if e:
         _check(e)
@@ -596,7 +629,7 @@ def silu_mul(gate, up, out, scale=None, group: int = 0, stream=None):
         _in_32_bits(group, rows, cols)
     op, ot = _typed(out, "out", _OUTS, rows, cols, dev)
     e = _lib.lvq_silu_mul(gp, up_p, gt, stride, rows, cols, op, ot,
-                          _array(scale, "scale", _F32, rows, _n_groups(cols, group) * 4, dev),
+                          _array(scale, "scale", _F32, rows, _n_groups(cols, group), dev),
                           group, stream)
     if e:
         _check(e)
