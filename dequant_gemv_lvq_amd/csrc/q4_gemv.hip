@@ -12,17 +12,26 @@
 // four batch sums of its own row and unit, so scale and zero are applied in the
 // lane that loaded them, in fp32, once per unit.
 //
-// No conversion of the codes to floats: a 4-bit value in bits 4..7 of an fp16 is
-// a subnormal, the value times 2^-20.  Per 8 codes three shifts and four masks
-// give two operands (columns 0, 4, 2, 6 and 1, 5, 3, 7 of the eight; x is stored
-// in LDS in that order).  The position matters: the matrix core aligns a
-// product by the exponents as stored, and a subnormal's leading zeros push its
-// bits off the lower end of the sum.  With the values in bits 0..3 (five
-// operations per 8 codes instead of seven) the error against 64 bits was 4e-6 to
-// 9e-6 of the result's norm, in bits 4..7 it is 0.9e-7 to 4e-7, in bits 6..9 (eight
-// operations) 0.7e-7 to 1e-7; the middle one is below what an fp32 product of
-// unpacked weights has.  The sum starts from minus zero times the unit's sum of x.  For int8 x two masks and a shift give the codes as
-// bytes and the sums are exact 32-bit integers.
+// No conversion of the codes to floats: a 4-bit value inside the ten mantissa bits
+// of an fp16 is a subnormal, the value times a power of two.  Shifts and masks give
+// two operands per 8 codes (columns 0, 4, 2, 6 and 1, 5, 3, 7 of the eight; x is
+// stored in LDS in that order).  The position matters: the matrix core aligns a
+// product by the exponents as stored, as if the code were as large as the top of
+// the ten bits, so what a code lies below it is lost at the lower end of the sum.
+//   fp16 x   bits 6..9 (eight operations per 8 codes): the sum q x0 + q x1 keeps
+//            every x1 down to 2^-20 x0, as fp32 does for a 4-bit q.  In bits 4..7
+//            (seven operations) it kept them to 2^-18, and the error against 64
+//            bits rose above an fp32 product's where codes lie close to their zero
+//            and x has outliers: norms of 0.9e-6 to 1.8e-6 of the result's at 4096
+//            columns, 1.2e-7 to 3.4e-7 now; an fp32 product of unpacked weights has
+//            4.6e-7 to 5.6e-7.  It takes 0 to 2 % of the time of the shapes below.
+//   e4m3 x   bits 4..7: x itself spans 2^-17 of its largest value at most, so
+//            nothing is lost (0.4e-7 to 0.9e-7, whatever the codes).
+//   int8 x   two masks and a shift give the codes as bytes, and the sums are exact
+//            32-bit integers.
+// The sum starts from minus zero times the unit's sum of x: where x has one sign and
+// the codes lie close to a zero far from 0 the two cancel, as the order of the sum
+// in fp32 has it (13..15 about zero 14, x > 0: 1.4e-6).
 //
 // The weights are the bytes (4.1 to 5 bits each): 4 flops per byte at batch 1.
 // Each wave streams 1 KiB of codes per step (4 rows x 256 contiguous bytes) in
@@ -108,7 +117,9 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef float float2_t __attribute__((ext_vector_type(2)));
 
-constexpr float kCodeUnit = 0x1p-20f;  // what a code's lowest bit is worth as an fp16 subnormal
+// The bit of an fp16 subnormal where a code starts, and what that bit is worth.
+constexpr int code_bit(int X) { return X == kQ4F16 ? 6 : 4; }
+constexpr float code_unit(int X) { return X == kQ4F16 ? 0x1p-18f : 0x1p-20f; }
 constexpr int kQ4Waves = 16;   // waves per workgroup at most
 constexpr int kStepUnits = 16; // units of 32 columns per step
 constexpr int kChunk = 4;      // steps a wave loads at a time
@@ -225,7 +236,7 @@ __device__ __forceinline__ void put_x8(uint8_t* xs, float* sums, float* scaled,
   sum = dpp_add<0x4E, 0xF>(dpp_add<0xB1, 0xF>(sum));  // the quad's four words
   if (w == 0) {
     const int u = t * kStepUnits + ul, at = u * B + bb;
-    sum *= (Z ? -1.f : -8.f) * (X == kQ4I8 ? 1.f : kCodeUnit);
+    sum *= (Z ? -1.f : -8.f) * (X == kQ4I8 ? 1.f : code_unit(X));
     if constexpr (X == kQ4I8 && !Z) sum = __builtin_bit_cast(float, (int)sum);  // a whole number
     sums[at] = sum;
     if constexpr (X != kQ4F16) scaled[at] = s;
@@ -417,7 +428,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
     const uint8_t* xt = xl + t * x_step_bytes(B, X);
     // e4m3: the codes' unit leaves with the scale (fp16 x: at the store), so that a
     // small scale of x does not push the sum below fp32's normal numbers
-    const float s = f16_to_f32(sz) * (X == kQ4E4M3 ? 1.f / kCodeUnit : 1.f);
+    const float s = f16_to_f32(sz) * (X == kQ4E4M3 ? 1.f / code_unit(X) : 1.f);
     const float z = f16_to_f32(sz >> 16);
     const float* sx = sl + t * (kStepUnits * B);
     const float* tx = tl + t * (kStepUnits * B);
@@ -448,13 +459,15 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
       for (int k = 0; k < 4; ++k) {
         const u32x4_t x = *(const u32x4_t*)(xt + k * slab_bytes(B));
         const uint32_t w = q[k];
-        constexpr uint32_t m = 0x00F000F0u;
+        constexpr int b = code_bit(X);
+        constexpr uint32_t m = 0x000F000Fu << b;
         c = __builtin_amdgcn_mfma_f32_4x4x4f16(
             __builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}),
-            __builtin_bit_cast(half4_t, u32x2_t{(w << 4) & m, (w >> 4) & m}), c, 0, 0, 0);
+            __builtin_bit_cast(half4_t, u32x2_t{(w << b) & m, (w >> (8 - b)) & m}), c, 0, 0, 0);
         c = __builtin_amdgcn_mfma_f32_4x4x4f16(
             __builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}),
-            __builtin_bit_cast(half4_t, u32x2_t{w & m, (w >> 8) & m}), c, 0, 0, 0);
+            __builtin_bit_cast(half4_t, u32x2_t{(w << (b - 4)) & m, (w >> (12 - b)) & m}), c, 0, 0,
+            0);
       }
 #pragma unroll
       for (int bb = 0; bb < B; ++bb) v[bb] = c[bb];
@@ -480,7 +493,7 @@ __global__ void __launch_bounds__(kQ4Waves * kWave) q4_gemv_kernel(Q4Args a) {
   auto store = [&](int quad, float r) {
     const int row = quad * 4 + r4;
     if (ul < a.batch && row < a.rows)
-      a.y[(size_t)ul * a.rows + row] = X == kQ4F16 ? r * (1.f / kCodeUnit) : r;
+      a.y[(size_t)ul * a.rows + row] = X == kQ4F16 ? r * (1.f / code_unit(X)) : r;
   };
 
   float own = 0.f;  // of a quad that starts in this wave and ends in a later one

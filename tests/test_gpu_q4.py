@@ -5,6 +5,7 @@ import pytest
 
 import synth
 from oracle import gemv as og
+from oracle import norm as on
 from oracle import q4 as oq
 
 pytestmark = pytest.mark.gpu
@@ -308,3 +309,76 @@ def test_precision_is_that_of_fp32(kind, zeros):
     r = float(np.linalg.norm(y - y64) / np.linalg.norm(y64))
     print("precision %s %s: %.3g" % (kind, zeros, r), flush=True)
     assert r <= 2.0 ** -20
+
+
+def _two_codes(a, b, x_a, x_b, kind="f16"):
+    """Rows of q = 1..15 at columns a and b and 0 elsewhere, zero 0 and scale 1;
+    batch rows of x_a[i] and x_b[i] there.  Returns (y, q)."""
+    q = np.arange(1, 16)
+    codes = np.zeros((15, 16), dtype=np.uint8)
+    for c in (a, b):
+        codes[:, c // 2] |= (q << (4 * (c % 2))).astype(np.uint8)
+    d = {"codes": codes, "scale": synth.fp16_bits(np.ones((15, 1))),
+         "zero": synth.fp16_bits(np.zeros((15, 1))), "rows": 15, "cols": 32, "group": 0}
+    x = np.zeros((len(x_a), 32))
+    x[:, a], x[:, b] = x_a, x_b
+    if kind == "f16":
+        return _run(d, synth.fp16_bits(x), len(x_a)), q
+    x8 = torch.from_numpy(x).to(E4M3).view(torch.uint8).numpy()
+    return _run(d, x8, len(x_a), kind, np.ones((len(x_a), 1), dtype=np.float32)), q
+
+
+@pytest.mark.parametrize("a,b", [(0, 4), (0, 2), (1, 5), (4, 0), (0, 1), (3, 31), (31, 3)])
+def test_a_product_keeps_what_fp32_keeps_beside_a_larger_one(a, b):
+    """q 2^10 + q 2^(10-k) with a 4-bit q has k + 4 bits at most: up to k = 20 it is
+    an fp32 number, so nothing of the smaller product may be lost, whatever the code."""
+    k = np.array([17, 18, 19, 20])
+    y, q = _two_codes(a, b, np.full(4, 2.0 ** 10), 2.0 ** (10 - k))
+    assert np.array_equal(y, (2.0 ** 10 + 2.0 ** (10.0 - k))[:, None] * q)
+
+
+def test_e4m3_x_keeps_every_value_beside_the_largest():
+    """The smallest e4m3 value, 2^-9, beside 2^8: 17 + 4 bits."""
+    y, q = _two_codes(0, 4, [2.0 ** 8] * 2, [2.0 ** -9, 3 * 2.0 ** -9], "e4m3")
+    assert np.array_equal(y, (2.0 ** 8 + np.array([1, 3]) * 2.0 ** -9)[:, None] * q)
+
+
+CODES = [("8, sigma 1", lambda r, s: np.rint(8 + r.standard_normal(s)).clip(0, 15), None),
+         ("7..9", lambda r, s: r.integers(7, 10, s), None),
+         ("7..9, zero 8", lambda r, s: r.integers(7, 10, s), 8.0),
+         ("0..1, zero 0", lambda r, s: r.integers(0, 2, s), 0.0),
+         ("0..3, zero 1.5", lambda r, s: r.integers(0, 4, s), 1.5),
+         ("13..15, zero 14", lambda r, s: r.integers(13, 16, s), 14.0)]
+
+
+@pytest.mark.parametrize("kind", ["f16", "i8", "e4m3"])
+@pytest.mark.parametrize("name,codes,zero", CODES, ids=[c[0] for c in CODES])
+def test_precision_with_codes_close_to_their_zero(name, codes, zero, kind):
+    """The error's norm against the result's where the result is small beside its
+    terms: codes of one to three steps about the zero, x with outliers.  A unit's sum
+    starts at zero times the sum of x, at most 14 / 0.8 = 17 times the unit's result,
+    and falls to it over ten roundings (u = 2^-24 at most, about 0.4 u as a root mean
+    square; the fall's mean square is a third of its start's): sqrt(10 / 3) 17 0.4 u
+    = 12.4 u = 2^-20.4.  2^-20 is allowed."""
+    rows, cols = 1024, 4096
+    r = np.random.default_rng(8)
+    q = codes(r, (rows, cols)).astype(np.uint8)
+    d = synth.q4_matrix(rows, cols, 128, zero is not None, key=(12,))
+    d["codes"] = q[:, 0::2] | q[:, 1::2] << 4
+    if zero is not None:
+        d["zero"] = synth.fp16_bits(np.full(d["zero"].shape, zero))
+    w, _ = oq.weights(d["codes"], d["scale"], d["zero"], rows, cols, 128)
+    v = synth.hidden(4, cols, key=(12,))
+    if kind == "f16":
+        x, s = synth.fp16_bits(v), None
+        xf = og.f16(x)
+    else:
+        s = (np.abs(v).max(axis=1, keepdims=True) / on.LARGEST[kind]).astype(np.float32)
+        x = (np.rint(v / s).astype(np.int8) if kind == "i8" else
+             torch.from_numpy(v / s).to(E4M3).view(torch.uint8).numpy())
+        xf = oq.activations(x, kind, s, cols, 0)
+    y64 = xf @ w.T
+    y = _run(d, x, 4, kind, s, 0)
+    e = float(np.linalg.norm(y - y64) / np.linalg.norm(y64))
+    print("precision %s %s: %.3g" % (kind, name, e), flush=True)
+    assert e <= 2.0 ** -20
