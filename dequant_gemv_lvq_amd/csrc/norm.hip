@@ -506,9 +506,13 @@ __device__ __forceinline__ void silu_chunk(const Chunk<T>& gc, const Chunk<T>& u
 #pragma unroll
   for (int i = 0; i < kChunk; ++i) {
     // e^-g as 2^(-g log2 e); both of the hardware's approximations (2^v and
-    // 1/v) are within an ulp, the product of the exponent off by |g| 2^-24
+    // 1/v) are within an ulp, the product of the exponent off by up to 2 |g| 2^-24 of
+    // the power, which an 11-bit output hides.  The hardware's 1/v is 0 where it
+    // would be subnormal (g below -87.3), so a quarter of 1 + e^-g is inverted and a
+    // quarter of g multiplied: right down to where e^-g leaves fp32 (g below
+    // -88.72, then 0).
     const float e = __builtin_amdgcn_exp2f(g[i] * -1.44269504f);
-    o[i] = g[i] * __builtin_amdgcn_rcpf(1.f + e) * u[i];
+    o[i] = g[i] * 0.25f * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0.25f, 0.25f)) * u[i];
   }
 }
 

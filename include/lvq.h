@@ -441,7 +441,9 @@ int lvq_rms_norm(const void* x, int x_type, int64_t x_stride, const void* residu
                  int out_group, void* stream);
 
 /* Gated activation between the gate/up projections and the down projection:
- *   out = gate / (1 + exp(-gate)) * up        (fp32, rounded once)
+ *   out = gate / (1 + exp(-gate)) * up        (fp32, rounded once; exp(-gate) is
+ *         off by up to 2^-23 |gate| of it, and out is 0 for gates below -88.72,
+ *         where it leaves the fp32 range)
  *   gate, up   fp32, fp16 or bf16 (in_type) rows of cols values, in_stride
  *              values apart (gate and up may be the halves of one matrix's
  *              output, in_stride = 2 * cols); in_stride >= cols

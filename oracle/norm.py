@@ -10,8 +10,9 @@ Bounds count roundings, u = 2^-24 relative for a nearest rounding to fp32.
          products 2 u, division and eps 2 u.
   silu   2^(-g log2 e): the exponent is off by |g| log2(e) (u + u), that is a
          relative 2 |g| u of the power; the power and the reciprocal a step
-         each (2 u), the addition and two products u.  Below g = -80 the power
-         leaves the fp32 range: the result is off by at most |g u| e^-80.
+         each (2 u), the addition and two products u.  Below g = -88.72 the power
+         leaves the fp32 range (2^128 = e^88.7228) and the result may be 0.  Products
+         below the normal numbers are off by half their spacing, 2^-150, each.
 """
 import numpy as np
 
@@ -35,7 +36,8 @@ def silu_mul(gate, up) -> tuple:
     """(out, rel, absolute): f64 result and the bounds of its fp32 error."""
     with np.errstate(over="ignore"):
         out = gate / (1 + np.exp(-gate)) * up
-    return out, (2 * np.abs(gate) + 2 + 2 + 3) * U, np.abs(gate * up) * np.exp(-80.0)
+    least = np.where(gate < -88.72, np.abs(out), 0.0) + (np.abs(up) + 1) * 2.0 ** -149
+    return out, (2 * np.abs(gate) + 2 + 2 + 3) * U, least
 
 
 def half_step(v, kind: str) -> np.ndarray:

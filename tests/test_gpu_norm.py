@@ -226,6 +226,22 @@ def test_silu_mul_zero_and_extreme_gates():
     assert o[6] == float("inf") and o[7].isnan()
 
 
+@pytest.mark.parametrize("kind,group", [("f16", 0), ("e4m3", 32), ("i8", 0)])
+@pytest.mark.parametrize("cols", [512, 3000])
+def test_silu_mul_gates_down_to_the_end_of_fp32(cols, kind, group):
+    """Gates of -80 to -90 times an up that brings the result back into range: the
+    stated fp32 formula is a normal number down to -88.72 (below that 0, which 8-bit
+    groups, with a scale of their own largest value, are not asked for here)."""
+    g = torch.linspace(-90 if kind == "f16" else -88.7, -80, 3 * cols).view(3, cols)
+    u = torch.full((3, cols), 1e36) * (1 + torch.arange(cols) % 7)
+    want, rel, least = on.silu_mul(g.double().numpy(), u.double().numpy())
+    assert (least[g.numpy() > -88.71] < 1e-8).all()
+    od, sd, n = _out(3, cols, kind, group)
+    lvq.silu_mul(g.to(DEV), u.to(DEV), od, scale=sd, group=group)
+    torch.cuda.synchronize()
+    _check_out(od, sd, n, 3, cols, kind, group, want, rel, least)
+
+
 def test_binding_refusals():
     x = torch.zeros(4, 64, device=DEV)
     out = torch.zeros(4, 64, dtype=torch.float16, device=DEV)

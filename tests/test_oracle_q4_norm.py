@@ -68,6 +68,13 @@ def test_silu_mul_matches_torch():
     assert (rel < 1e-5).all() and (least < 1e-30).all()
 
 
+def test_silu_slack_begins_where_the_power_leaves_fp32():
+    assert np.isfinite(np.float32(np.exp(88.72))) and np.exp(88.7229) >= 2.0 ** 128
+    g = np.array([-100.0, -88.75, -88.71, -80.0, 0.0, 90.0])
+    out, _, least = on.silu_mul(g, np.full(6, 1e36))
+    assert (least[:2] >= np.abs(out[:2])).all() and (least[2:] < 1e-8).all()
+
+
 def test_half_step_is_half_the_distance_of_neighbours():
     for kind, dt in (("f32", np.float32), ("f16", np.float16)):
         v = np.array([1.0, 1.5, 2.0, 1000.0, 3e-6, 6.1e-5], dtype=dt)
