@@ -431,10 +431,15 @@ int q4_gemv_q8(const uint8_t* codes, const uint16_t* scale, const uint16_t* zero
  *                group whose a is below 2^-100 gets scale 0 and zero codes, one
  *                that holds a NaN or an infinity zero codes and a scale that is
  *                not finite.  NULL and out_group 0 for fp16.
- * The statistics and the results before the rounding are fp32.  rows is any
- * number >= 0, cols <= 32768.  x needs the alignment of its type only (it may
- * be a slice of a wider buffer); every other pointer 16 bytes.  No output may overlap an input
- * or another output, residual_out == residual excepted (LVQ_E_SHAPE). */
+ * The statistics and the results before the rounding are fp32, so a row with
+ * values above about 1.8e19 has an infinite mean square and zeros as results.  The
+ * order of a row's sum of squares depends on cols, rows and the device: a row may
+ * differ in the last bits of its fp32 results between calls of few and of many
+ * rows, and is the same from run to run.  rows is any number >= 0, cols <= 32768;
+ * with rows or cols 0 nothing is written, neither out_scale.  x needs the alignment
+ * of its type only (it may be a slice of a wider buffer); every other pointer 16
+ * bytes.  No output may overlap an input or another output, residual_out ==
+ * residual excepted (LVQ_E_SHAPE). */
 int lvq_rms_norm(const void* x, int x_type, int64_t x_stride, const void* residual,
                  int residual_type, void* residual_out, const void* weight, int weight_type,
                  float eps, int rows, int cols, void* out, int out_type, float* out_scale,

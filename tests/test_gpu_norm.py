@@ -242,6 +242,37 @@ def test_silu_mul_gates_down_to_the_end_of_fp32(cols, kind, group):
     _check_out(od, sd, n, 3, cols, kind, group, want, rel, least)
 
 
+@pytest.mark.parametrize("kind", ["i8", "e4m3"])
+@pytest.mark.parametrize("rows,cols", [(3, 0), (0, 64), (0, 0)])
+def test_rows_or_columns_of_zero_write_nothing(rows, cols, kind):
+    """Not the scales either: with no columns a row has no largest value."""
+    x = torch.ones(rows, cols, device=DEV)
+    for group in (0, 32):
+        out = torch.full((64,), 1, dtype=torch.uint8, device=DEV).to(OUTS[kind])
+        scale = torch.full((16,), 7.0, device=DEV)
+        stream = torch.full((64,), 5.0, device=DEV)
+        lvq.rms_norm(x, stream, None, EPS, out, residual_out=stream, scale=scale, group=group)
+        lvq.silu_mul(x, x, out, scale=scale, group=group)
+        torch.cuda.synchronize()
+        assert (out.float() == 1).all() and (scale == 7).all() and (stream == 5).all()
+
+
+def test_a_row_repeats_its_bits_and_keeps_its_bounds_for_any_number_of_rows():
+    """The number of rows may move a row's last bits; its place among them, and a
+    second call, may not."""
+    cols = 4096
+    x = torch.from_numpy(synth.hidden(1, cols)).float().to(DEV)
+    h, want, rel = on.rms_norm(x.double().cpu().numpy(), None, None, EPS)
+    tol = on.half_step(want * (1 + 1e-5), "f16") + rel * np.abs(want)
+    for rows in (1, 64, 1024):
+        xs = x.expand(rows, cols).contiguous()
+        a, b = (torch.empty(rows, cols, dtype=torch.float16, device=DEV) for _ in range(2))
+        lvq.rms_norm(xs, None, None, EPS, a)
+        lvq.rms_norm(xs, None, None, EPS, b)
+        assert torch.equal(a, b) and torch.equal(a, a[:1].expand(rows, cols))
+        assert (np.abs(a[0].double().cpu().numpy() - want[0]) <= tol[0]).all()
+
+
 def test_binding_refusals():
     x = torch.zeros(4, 64, device=DEV)
     out = torch.zeros(4, 64, dtype=torch.float16, device=DEV)
