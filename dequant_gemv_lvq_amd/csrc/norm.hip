@@ -18,7 +18,7 @@
 //
 // Measured (GPU time per call in a graph, one MI355X; a large copy reaches 5.2
 // TB/s, an empty launch 1.8-2.0 us): rms_norm 8192x4096 bf16 onto bf16, e4m3 out
-// 44.6 us (5.3 TB/s), 8192x4096 fp16 49.1 us (5.5 TB/s), 32768x128 5.0 us, one row
+// 44.6 us (5.3 TB/s), 8192x4096 fp16 48.4 us (5.5 TB/s), 32768x128 5.0 us, one row
 // of 4096 2.9 us; silu_mul 2048x12288 fp16 27.8 us (5.4 TB/s), to int8 with one
 // scale per row 26.2 us, one row of 12288 fp32 2.7 us (group scales; 3.8 with one
 // scale, where one workgroup does the row).
@@ -439,8 +439,8 @@ __global__ void __launch_bounds__(LANES ? 256 : kRowThreads) rms_norm_kernel(Nor
 // 32 or 64 lanes; above, a workgroup with one chunk per thread for few rows (the
 // shortest way through one row), two for many (fewer waves meet at a row's
 // barriers and each has more loads in flight: 2048x8192 int8 25.5 us with 512
-// threads and two chunks, 36.9 with 1024 and one, 29.5 with 256 and four;
-// 8192x4096 44.5 against 45.9), four where 1024 threads need them.
+// threads and two chunks, 36.7 with 1024 and one, 29.1 with 256 and four;
+// 8192x4096 44.6 with two, 45.0 with one), four where 1024 threads need them.
 struct RowShape {
   int nv, threads, lanes;
 };
@@ -453,9 +453,12 @@ RowShape row_shape(int rows, int cols, int group) {
   return {nv, ((chunks + nv - 1) / nv + kWave - 1) / kWave * kWave, 0};
 }
 
-// As many workgroups as the chip holds at once (lanes), or four times that, so
-// that those which end early are followed by others (32768x128: 8.4 us against
-// 11.9; 8192x4096: 51.0 against 45.9).
+// As many workgroups as the chip holds at once where lanes share a row, four times
+// that where a workgroup does, so that those which end early are followed by others
+// (8192x4096: 44.6 us with four times, 47.2 with once).  With lanes the smaller grid
+// reads the weights less often: 70000x64 fp16 6.5 us with once, 7.7 with four times;
+// far longer inputs lose by it, 131072x512 fp16 49.0 against 47.5, 1000000x64 to int8
+// 131 against 104.
 int row_grid(int rows, const RowShape& s) {
   const int per = s.lanes ? s.threads / s.lanes : 1;
   const long long wgs = ((long long)rows + per - 1) / per;

@@ -588,12 +588,12 @@ int launch_q4_ring(const Q4Call& c, hipStream_t st) {
   // a chunk being about 80 cycles of its load unit (five loads of 16, whether or
   // not a load cut off returns anything) and 1200 cycles of one wave's time, which
   // other waves overlap: 4096x12288 takes 12 waves of two full chunks instead of
-  // 16 of four steps and two (batch 4: 10.1 us against 11.1), 4096x4096 takes 8 of
-  // one instead of 16 of half a chunk (3.9 us against 6.1).  And enough to bring
+  // 16 of four steps and two (batch 4: 9.8 us against 10.7), 4096x4096 takes 8 of
+  // one instead of 16 of half a chunk (4.2 us against 4.6).  And enough to bring
   // in the x of four batch rows, whatever the batch: the waves decide where a
   // row's steps are divided, and a row's bits are the same in every batch.  (With
   // the lower bound of batch 1 for all, 1024x12288 batch 4 takes 7.1 us instead
-  // of 6.4; with this one, 1024x16384 batch 1 takes 4.9 instead of 4.6.)
+  // of 6.5; with this one, 1024x16384 batch 1 takes 4.9 instead of 4.6.)
   const int cus = device_cus();
   const int quads = (int)(((long long)c.rows + 3) / 4);
   Q4Args a;
@@ -650,8 +650,10 @@ int launch_q4_batch(const Q4Call& c, hipStream_t st) {
   return c.zero ? launch_q4_groups<B, X, true>(c, st) : launch_q4_groups<B, X, false>(c, st);
 }
 
-// Three batch rows run as four (the fourth zeros) where their x fits in LDS,
-// else as two and one.  Every other x of batch * cols <= 65536 fits.
+// Three batch rows run as four (the fourth zeros) where their x fits in LDS (up to
+// 18,432 columns, 17,408 of e4m3, any of int8), else as two and one, which reads the
+// weights twice: 4096x21840 24.6 us, of which the two rows take 13.1 and the one 11.9
+// (4096x16384 batch 3 11.9).  Every other x of batch * cols <= 65536 fits.
 template <int X>
 int launch_q4(Q4Call c, hipStream_t st) {
   const size_t most = device_lds_bytes();
