@@ -18,7 +18,7 @@
 //
 // Measured (GPU time per call in a graph, one MI355X; a large copy reaches 5.2
 // TB/s, an empty launch 1.8-2.0 us): rms_norm 8192x4096 bf16 onto bf16, e4m3 out
-// 44.6 us (5.3 TB/s), 8192x4096 fp16 48.4 us (5.5 TB/s), 32768x128 5.0 us, one row
+// 44.6 us (5.3 TB/s), 8192x4096 fp16 48.4-49.3 us (5.4-5.5 TB/s), 32768x128 5.0 us, one row
 // of 4096 2.9 us; silu_mul 2048x12288 fp16 27.8 us (5.4 TB/s), to int8 with one
 // scale per row 26.2 us, one row of 12288 fp32 2.7 us (group scales; 3.8 with one
 // scale, where one workgroup does the row).

@@ -39,19 +39,21 @@
 // in LDS.  Loads are counted: one of 64 lanes takes a CU's load unit 16 cycles
 // whatever it returns, so the scales and zeros of four steps come with one load
 // each (16 groups x 4 rows, or 16 x 2 bytes a row) and reach their lanes through
-// ds_bpermute, and no load is made for nothing.
+// ds_bpermute.  A chunk ends with its quad, so the last one of a quad costs four
+// loads of codes whatever steps it holds: rows of up to 1024 columns run below the
+// memory's rate for that (70003x96 10.4 us).
 //
 // Measured (GPU time per call in a graph over rotating matrices, one MI355X; a
 // plain read of that many bytes runs at up to 6.4 TB/s, an empty launch 1.8 us):
-// 131072x4096 batch 1 45-47 us, 5.9-6.2 TB/s, bound by that read; 4096x12288
-// batch 1 7.8 us, 12288x4096 7.0 us (3.3 and 3.7 TB/s); 4096x12288 batch 4
-// 10.0-10.7 us, where each CU brings in 96 KiB of x; 4096x4096 3.8-4.3 us,
-// 1024x4096 3.3 us, bound by the launch and two round trips to memory.  Without
-// its arithmetic (a timing variant of an earlier step) 131072x4096 took 42.9 us
-// instead of 45.5-46.2, 12288x4096 6.0 instead of 7.3, 4096x12288 batch 4 8.1
-// instead of 10.2.  A full chunk's block holds 38-40 vector instructions per
-// step at batch 1, 28 of them unpack the codes and 8 are matrix products, and 5
-// LDS reads.
+// 131072x4096 batch 1 45-47 us, 5.9-6.1 TB/s, bound by that read; 4096x12288
+// batch 1 7.4-7.9 us, 12288x4096 7.1-7.4 us (3.3-3.5 and 3.5-3.7 TB/s); 4096x12288
+// batch 4 9.7-10.7 us, where each CU brings in 96 KiB of x; 4096x4096 3.8-4.4 us,
+// 1024x4096 3.3 us, bound by the launch and two round trips to memory.  With the
+// codes taken as they are, not unpacked (a timing variant), 131072x4096 took 43.6 us
+// instead of 45.3, 12288x4096 6.3 instead of 7.1, 4096x12288 batch 4 9.0 instead of
+// 9.8; without the loads of x the last took 9.2, without ordering and summing x 9.8.
+// A full chunk's block holds 43-44 vector instructions per step at batch 1, 32 of
+// them unpack the codes and 8 are matrix products, and 6 LDS reads.
 
 #include <type_traits>
 
