@@ -432,7 +432,8 @@ int q4_gemv_q8(const uint8_t* codes, const uint16_t* scale, const uint16_t* zero
  *                that holds a NaN or an infinity zero codes and a scale that is
  *                not finite.  NULL and out_group 0 for fp16.
  * The statistics and the results before the rounding are fp32, so a row with
- * values above about 1.8e19 has an infinite mean square and zeros as results.  The
+ * values above about 1.8e19 has an infinite mean square and zeros as results, and
+ * one whose values are all below about 1e-19 needs an eps above 0.  The
  * order of a row's sum of squares depends on cols, rows and the device: a row may
  * differ in the last bits of its fp32 results between calls of few and of many
  * rows, and is the same from run to run.  rows is any number >= 0, cols <= 32768;
