@@ -20,6 +20,7 @@ STREAM_SINK_WORDS = 4096
 STREAM_GEOM_SINK_WORDS = 65536
 MAX_FUSED = 4
 MAX_BATCH = 4
+MAX_QUERIES = 16
 
 LVQ_F32 = 0
 LVQ_F16 = 1
@@ -94,6 +95,12 @@ def _load():
         "lvq_rms_norm": (i, [vp, i, i64, vp, i, vp, vp, i, ctypes.c_float, i, i, vp, i, vp, i,
                              vp]),
         "lvq_silu_mul": (i, [vp, vp, i, i64, i, i, vp, i, vp, i, vp]),
+        "lvq_kv_page_bytes": (sz, [i, i, i, i]),
+        "lvq_kv_append": (i, [vp, vp, i64, vp, i64, i, vp, vp, i, vp, vp, i, i, i, vp, i64, i, vp,
+                              i, vp]),
+        "lvq_kv_read": (i, [vp, vp, vp, i, vp, vp, i, vp]),
+        "lvq_attend_workspace": (sz, [vp, i, i]),
+        "lvq_attend": (i, [vp, vp, i, i64, i, i, vp, ctypes.c_float, i, vp, i, vp, sz, vp]),
         "lvq_rotate": (i, [vp, vp, vp, i, i, vp, i, vp]),
         "lvq_gemv_rotated": (i, [vp, i, i, vp, vp, i, vp, vp, i, vp]),
         "lvq_stream_read": (i, [vp, sz, vp, vp]),
@@ -116,7 +123,8 @@ EXPORTED = ("lvq_strerror", "lvq_last_error_index", "lvq_class_table", "lvq_layo
             "lvq_rank", "lvq_gemv", "lvq_gemv_gain",
             "lvq_unfold", "lvq_gemv_fused", "lvq_gemv_noweights", "lvq_decode",
             "bpdq_gemv", "trellis_gemv", "fp16_gemv", "q4_gemv", "q4_gemv_q8",
-            "lvq_rms_norm", "lvq_silu_mul", "lvq_rotate", "lvq_gemv_rotated",
+            "lvq_rms_norm", "lvq_silu_mul", "lvq_kv_page_bytes", "lvq_kv_append", "lvq_kv_read",
+            "lvq_attend_workspace", "lvq_attend", "lvq_rotate", "lvq_gemv_rotated",
             "lvq_stream_read", "lvq_stream_read_geom", "lvq_gemv_launch_info")
 
 
@@ -404,6 +412,7 @@ _F16_BITS = _types("float16", "int16", "uint16")
 _BYTES = _types("uint8", "int8")
 _WORDS = _types("int32", "uint32")
 _F32 = _types("float32")
+_INT32 = getattr(_torch, "int32", None)
 _FLOATS = _types("float32", "float16", "bfloat16")
 _EIGHT = _types("int8", "float8_e4m3fn")
 _OUTS = _types("float16") + _EIGHT
@@ -548,7 +557,7 @@ def _rows_of(t, name, dev):
     if len(shape) != 2:
         raise ValueError("%s must have two dimensions, rows and columns" % name)
     rows, cols = shape
-    if strides[1] != 1 and cols > 1:
+    if strides[1] != 1 and cols > 1 and rows:
         raise ValueError("%s must have adjacent columns" % name)
     return t.data_ptr(), _TYPES[t.dtype], rows, cols, strides[0] if rows > 1 else cols
 
@@ -631,6 +640,193 @@ def silu_mul(gate, up, out, scale=None, group: int = 0, stream=None):
     e = _lib.lvq_silu_mul(gp, up_p, gt, stride, rows, cols, op, ot,
                           _array(scale, "scale", _F32, rows, _n_groups(cols, group), dev),
                           group, stream)
+    if e:
+        _check(e)
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("table", ctypes.c_void_p), ("pages", ctypes.c_int),
+                ("seqs", ctypes.c_int), ("max_pages", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("dim", ctypes.c_int), ("page", ctypes.c_int), ("group", ctypes.c_int)]
+
+
+class KvCache:
+    """A key/value cache in 4 bits as kv_append(), kv_read() and attend() take it: the
+    pool of pages and the table of pages per sequence, both the caller's tensors."""
+
+    __slots__ = ("pool", "table", "_struct", "_ref")
+
+    def _here(self, dev):
+        """Address of the description; its tensors are looked at anew in every call."""
+        s, pool, table = self._struct, self.pool, self.table
+        if pool.get_device() != dev:
+            _refuse(pool, "pool", _types("uint8"), s.pages, 0, dev)
+        if table.get_device() != dev:
+            _refuse(table, "table", _types("int32"), s.seqs, s.max_pages, dev)
+        s.pool, s.table = pool.data_ptr(), table.data_ptr()
+        return self._ref
+
+
+def kv_page_bytes(kv_heads: int, dim: int, page: int, group: int = 0) -> int:
+    """Bytes of a page of `page` tokens."""
+    kv_heads, dim, page, group = int(kv_heads), int(dim), int(page), int(group)
+    _in_32_bits(kv_heads, dim, page, group)
+    n = int(_lib.lvq_kv_page_bytes(kv_heads, dim, page, group))
+    if n == 0:
+        _check(LVQ_E_SHAPE)
+    return n
+
+
+def kv_cache(pool, table, kv_heads: int, dim: int, page: int, group: int = 0) -> KvCache:
+    """Describes a cache: pool uint8 [pages][kv_page_bytes(...)], table int32
+    [seqs][max_pages], both contiguous and on the GPU."""
+    size = kv_page_bytes(kv_heads, dim, page, group)
+    for t, name, kind in ((pool, "pool", "uint8"), (table, "table", "int32")):
+        if not isinstance(t, _Tensor):
+            raise TypeError("%s must be a tensor on the GPU" % name)
+        if t.dtype not in _types(kind):
+            raise ValueError("%s has type %s" % (name, t.dtype))
+        if len(t.shape) != 2 or not t.is_contiguous():
+            raise ValueError("%s must be contiguous, of two dimensions" % name)
+    if pool.shape[1] != size:
+        raise LvqError(LVQ_E_SHAPE, "%s: pages of %d bytes, not of %d" % (
+            strerror(LVQ_E_SHAPE), pool.shape[1], size))
+    _in_32_bits(pool.shape[0], table.shape[0], table.shape[1])
+    c = KvCache()
+    c.pool, c.table = pool, table
+    c._struct = _CacheStruct(0, 0, pool.shape[0], table.shape[0], table.shape[1], int(kv_heads),
+                             int(dim), int(page), int(group))
+    c._ref = ctypes.addressof(c._struct)
+    return c
+
+
+def _index(t, name, n, dev):
+    """Address of a contiguous int32 tensor of n values, one for each token or sequence."""
+    try:
+        if (t.dtype is _INT32 and t.get_device() == dev and t.shape == (n,)
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not _holds(t, _types("int32"), 1, n, dev) or t.numel() != n:
+        _refuse(t, name, _types("int32"), 1, n, dev)
+    return t.data_ptr()
+
+
+def kv_append(cache: KvCache, k, v, pos, seq=None, cos=None, sin=None, interleaved: bool = False,
+              q=None, q_out=None, stream=None):
+    """Stores tokens in the cache, their keys rotated, and rotates their queries.  k, v: 2-D
+    tensors of one type (fp32, fp16 or bf16), a row of kv_heads * dim values per token (rows may
+    be strided, for instance the parts of one product's output); pos and seq int32, one per
+    token (seq None: token i is of sequence i).  cos, sin: fp32 [positions][rot / 2], the
+    first rot channels of every head turned in pairs (j, j + rot/2), or (2 j, 2 j + 1) if
+    interleaved; None for no rotation.  q (of k's type, heads * dim values per token) and q_out
+    (fp16, bf16 or fp32, contiguous) go together or are None."""
+    dev, stream = _here(stream)
+    s = cache._struct
+    ref = cache._here(dev)
+    kp, kt, tokens, kcols, kstride = _rows_of(k, "k", dev)
+    vp, vt, vtokens, vcols, vstride = _rows_of(v, "v", dev)
+    if tokens >> 31:
+        _in_32_bits(tokens)
+    cols = s.kv_heads * s.dim
+    if kt != vt or tokens != vtokens or kcols != cols or vcols != cols:
+        raise ValueError("k and v must have the same type and %d values per token" % cols)
+    cp = sp = qp = qop = None
+    rot = positions = heads = qstride = 0
+    qot = LVQ_F16
+    if cos is not None or sin is not None:
+        if cos is None or sin is None or len(cos.shape) != 2:
+            raise ValueError("cos and sin go together, of two dimensions")
+        positions, half = cos.shape
+        rot = 2 * half
+        if positions >> 31 or rot >> 31:
+            _in_32_bits(positions, rot)
+        cp = _same(cos, "cos", _F32, positions, half, dev)
+        sp = _same(sin, "sin", _F32, positions, half, dev)
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out go together")
+        qp, qt, qtokens, qcols, qstride = _rows_of(q, "q", dev)
+        heads = qcols // s.dim
+        if qt != kt or qtokens != tokens or heads * s.dim != qcols:
+            raise ValueError("q must have k's type and number of tokens, and whole heads")
+        qop, qot = _typed(q_out, "q_out", _FLOATS, tokens, qcols, dev)
+    e = _lib.lvq_kv_append(ref, kp, kstride, vp, vstride, kt,
+                           None if seq is None else _index(seq, "seq", tokens, dev),
+                           _index(pos, "pos", tokens, dev), tokens, cp, sp, rot, positions,
+                           1 if interleaved else 0, qp, qstride, heads, qop, qot, stream)
+    if e:
+        _check(e)
+
+
+def _same(t, name, types, rows, width, dev):
+    """Address of a contiguous tensor of exactly this shape."""
+    if isinstance(t, _Tensor) and t.shape == (rows, width):
+        return _array(t, name, types, rows, width, dev)
+    _refuse(t, name, types, rows, width, dev)
+
+
+def kv_read(cache: KvCache, pos, k_out, v_out, seq=None, stream=None):
+    """Reads tokens back: k_out, v_out (fp32, fp16 or bf16, one type; either may be None) get a
+    row of kv_heads * dim values per entry of pos."""
+    dev, stream = _here(stream)
+    s = cache._struct
+    ref = cache._here(dev)
+    tokens = pos.numel() if isinstance(pos, _Tensor) else 0
+    if tokens >> 31:
+        _in_32_bits(tokens)
+    cols = s.kv_heads * s.dim
+    kp = vp = None
+    kt = vt = LVQ_F16
+    if k_out is not None:
+        kp, kt = _typed(k_out, "k_out", _FLOATS, tokens, cols, dev)
+        vt = kt
+    if v_out is not None:
+        vp, vt = _typed(v_out, "v_out", _FLOATS, tokens, cols, dev)
+    if kp is not None and kt != vt:
+        raise ValueError("k_out and v_out must have the same type")
+    e = _lib.lvq_kv_read(ref, None if seq is None else _index(seq, "seq", tokens, dev),
+                         _index(pos, "pos", tokens, dev), tokens, kp, vp, vt, stream)
+    if e:
+        _check(e)
+
+
+def attend_workspace_bytes(cache: KvCache, heads: int, queries: int = 1) -> int:
+    """Bytes of workspace that attend() needs for any lengths and window."""
+    heads, queries = int(heads), int(queries)
+    _in_32_bits(heads, queries)
+    s = cache._struct
+    if heads < 1 or heads % s.kv_heads or not 1 <= queries <= MAX_QUERIES:
+        _check(LVQ_E_SHAPE)
+    s.pool, s.table = cache.pool.data_ptr(), cache.table.data_ptr()
+    return int(_lib.lvq_attend_workspace(cache._ref, heads, queries))
+
+
+def attend(cache: KvCache, q, lens, out, workspace, queries: int = 1, window: int = 0, scale=None,
+           stream=None):
+    """Causal attention of the last `queries` tokens of every sequence over the cache.  q:
+    2-D, fp16 or bf16, seqs * queries rows (sequence by sequence; they may be strided) of
+    heads * dim values; lens int32, tokens of each sequence, these queries' included; out
+    fp32, fp16 or bf16, contiguous; workspace: a uint8 tensor of attend_workspace_bytes().
+    window: how many tokens back a query sees (0: all); scale: dim ** -0.5 if None."""
+    queries, window = int(queries), int(window)
+    if (queries | window) >> 31:
+        _in_32_bits(queries, window)
+    dev, stream = _here(stream)
+    s = cache._struct
+    ref = cache._here(dev)
+    qp, qt, rows, cols, qstride = _rows_of(q, "q", dev)
+    if rows != s.seqs * queries or cols % s.dim or qt == LVQ_F32:
+        raise ValueError("q must be fp16 or bf16, %d rows of whole heads" % (s.seqs * queries))
+    op, ot = _typed(out, "out", _FLOATS, rows, cols, dev)
+    wp, n = None, 0
+    if workspace is not None:
+        n = workspace.numel()
+        wp = _array(workspace, "workspace", _BYTES, 1, n, dev)
+    e = _lib.lvq_attend(ref, qp, qt, qstride, cols // s.dim, queries,
+                        _index(lens, "lens", s.seqs, dev),
+                        s.dim ** -0.5 if scale is None else scale, window, op, ot, wp, n, stream)
     if e:
         _check(e)
 

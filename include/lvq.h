@@ -17,7 +17,8 @@
  * Next to them stand the other operators of a decoder block: 4-bit weights with
  * group scales for the projections that do not stand two bits (fp16 or 8-bit x),
  * the root-mean-square norm of a residual stream and the gated activation, with
- * fp16 or 8-bit outputs that the 4-bit arm reads.
+ * fp16 or 8-bit outputs that the 4-bit arm reads; the key/value cache in 4 bits and
+ * the attention over it.
  *
  * Conventions shared by every function.
  *   - Return value: LVQ_OK (0) or a negative LVQ_E_* code.  No exception or
@@ -459,6 +460,98 @@ int lvq_rms_norm(const void* x, int x_type, int64_t x_stride, const void* residu
 int lvq_silu_mul(const void* gate, const void* up, int in_type, int64_t in_stride, int rows,
                  int cols, void* out, int out_type, float* out_scale, int out_group,
                  void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Key/value cache in 4 bits, in pages, and the attention that reads it: the other half
+ * of a decoder layer, between the q/k/v projections and the output projection.
+ *
+ * The cache is described by a struct that is read during the call only; the buffers it
+ * points at are the caller's.  Position p of sequence s lies in page table[s][p / page],
+ * at p % page.  A page holds its tokens head by head, each head's in blocks of 16 tokens;
+ * with g = dim / group groups of channels (1 for group 0), a block is
+ *   uint8 [16][dim/2]  keys, token by token: channel 32 a + 8 b + i (b < 4, i < 8) is bits
+ *                      4 f..4 f + 3, f = i / 2 + 4 (i % 2), of the 32-bit word a of
+ *                      quarter b of the token's dim / 2 bytes
+ *   uint8 [dim/2][16]  values: channels 32 a + p (low half) and 32 a + 16 + p (high half)
+ *                      of token t are byte [16 a + p][t]
+ *   fp16 [g][16][2]    scale and low end of the keys of each group and token
+ *   fp16 [g][16][2]    of the values
+ * The value of a code c is scale * c + low.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  void* pool;           /* device, [pages] pages of lvq_kv_page_bytes bytes */
+  const int32_t* table; /* device, [seqs][max_pages] page numbers */
+  int pages, seqs, max_pages; /* >= 0; max_pages * page < 2^31 */
+  int kv_heads;         /* 1..1024 */
+  int dim;              /* channels of a head: 64, 128 or 256 */
+  int page;             /* tokens of a page: 16, 32, 64, 128, 256, 512 or 1024 */
+  int group;            /* channels per scale: 32, 64, 128 or 256, at most dim; 0 for dim */
+} lvq_kv_cache;
+
+/* Bytes of a page, 0 for sizes that no cache has. */
+size_t lvq_kv_page_bytes(int kv_heads, int dim, int page, int group);
+
+/* Stores `tokens` tokens and rotates their queries.  Token i belongs to position pos[i] of
+ * sequence seq[i] (seq NULL: of sequence i, one token of each).  The first rot channels of
+ * every head of k and q are turned, in pairs (j, j + rot/2), j < rot/2, or with interleaved
+ * 1 (2 j, 2 j + 1), by the angle whose cosine and sine are cos[pos][j] and sin[pos][j]:
+ *   a' = a cos - b sin,  b' = b cos + a sin
+ * (fp32, each product rounded before the sum).  Then keys and values are rounded to 4 bits,
+ * per token, head and group of channels:
+ *   scale = fp16((max - min) * fp32(1/15)),  low = fp16(min),
+ *   code = (v - low) * (1 / scale) rounded to the nearest (ties to even), within 0..15,
+ *   0 where the scale is 0
+ * A group that holds an infinity or a NaN is stored as NaN (its low end); magnitudes past
+ * fp16's range make its scale or low end infinite.
+ *   k, v       fp32, fp16 or bf16 (type), [tokens] rows of kv_heads * dim values, k_stride
+ *              and v_stride values from one row's start to the next's (< 2^31)
+ *   seq, pos   device, int32 [tokens]
+ *   cos, sin   device, fp32 [positions][rot/2]; rot a multiple of 16, at most dim, 0 for
+ *              no rotation (then NULL will do)
+ *   q, q_out   heads (0..1024; 0 for none) heads of dim channels per token: rows of `type`,
+ *              q_stride apart, and fp16, bf16 or fp32 (q_out_type) [tokens][heads * dim]
+ * A token whose sequence, position (negative, past the table of pages, or past `positions`
+ * where there is a rotation) or page is out of range is left out: nothing of it is stored
+ * and its row of q_out stays as it is.  No two tokens of a call may have the same place
+ * (what it then holds is unspecified).  Nothing else in the pool changes.  k, v and q need the
+ * alignment of their type, seq and pos of theirs, every other pointer 16 bytes.  The pool and
+ * q_out may overlap no input and not each other (LVQ_E_SHAPE). */
+int lvq_kv_append(const lvq_kv_cache* cache, const void* k, int64_t k_stride, const void* v,
+                  int64_t v_stride, int type, const int32_t* seq, const int32_t* pos, int tokens,
+                  const float* cos, const float* sin, int rot, int positions, int interleaved,
+                  const void* q, int64_t q_stride, int heads, void* q_out, int q_out_type,
+                  void* stream);
+
+/* Reads `tokens` tokens back: k_out, v_out (either may be NULL) [tokens][kv_heads * dim] of
+ * out_type (fp32, fp16 or bf16), the value of each code computed in fp32 and rounded once.
+ * seq and pos as in lvq_kv_append; a token out of range reads as zeros. */
+int lvq_kv_read(const lvq_kv_cache* cache, const int32_t* seq, const int32_t* pos, int tokens,
+                void* k_out, void* v_out, int out_type, void* stream);
+
+/* Causal attention of the last `queries` tokens of every sequence over the cache:
+ *   out[s][i][h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q[s][i][h] . k_t)
+ * over the positions t <= lens[s] - queries + i of sequence s (with window > 0 only the last
+ * `window` of them), k and v those of key/value head h / (heads / kv_heads).
+ *   q          fp16 or bf16 (q_type), rows of heads * dim values, q_stride apart, row
+ *              s * queries + i for query i of sequence s
+ *   heads      a multiple of kv_heads, at most 1024; queries 1..LVQ_MAX_QUERIES
+ *   lens       device, int32 [seqs]: tokens of each sequence, the queries' own included
+ *              (a length past the table counts as the table's end, a negative one as 0)
+ *   scale      above 0, finite
+ *   out        fp32, fp16 or bf16 (out_type) [seqs * queries][heads * dim]
+ *   workspace  device, lvq_attend_workspace bytes, its content of no account before and
+ *              after; calls that may run at the same time need one each
+ * A query that sees nothing (a length of 0, or fewer tokens than queries before it) gets
+ * zeros.  Tokens on pages outside the pool are not seen.  What a query does not see has no
+ * effect on it, whatever it holds; a NaN or an infinity that it sees gives NaN.  Sums and
+ * weights are fp32, the weights times the values' scales in two fp16 (22 bits).  The result
+ * is the same from run to run; how a sequence is split, and so the order of its sums,
+ * depends on its length, the cache's sizes and the device.  cache->seqs <= 65535. */
+#define LVQ_MAX_QUERIES 16
+size_t lvq_attend_workspace(const lvq_kv_cache* cache, int heads, int queries);
+int lvq_attend(const lvq_kv_cache* cache, const void* q, int q_type, int64_t q_stride, int heads,
+               int queries, const int32_t* lens, float scale, int window, void* out, int out_type,
+               void* workspace, size_t workspace_bytes, void* stream);
 
 /* Activation rotation before a GEMV whose weights are stored in a rotated
  * basis.  arXiv 2609.02652 (the incoherence-rotated basis; the paragraph on
