@@ -21,6 +21,8 @@ STREAM_GEOM_SINK_WORDS = 65536
 MAX_FUSED = 4
 MAX_BATCH = 4
 MAX_QUERIES = 16
+MAX_MOE_TOKENS = 16
+MAX_MOE_TOP = 16
 
 LVQ_F32 = 0
 LVQ_F16 = 1
@@ -92,6 +94,9 @@ def _load():
         "fp16_gemv": (i, [vp, i, i, vp, vp, i, vp]),
         "q4_gemv": (i, [vp, vp, vp, i, i, i, vp, vp, i, vp]),
         "q4_gemv_q8": (i, [vp, vp, vp, i, i, i, vp, i, vp, i, vp, i, vp]),
+        "q4_moe_workspace": (sz, [i, i, i, i, i]),
+        "q4_moe": (i, [vp, i, i, vp, i, i, i, i, vp, vp, vp, i, vp, vp, vp, i, i, vp, vp, vp, vp,
+                       sz, vp]),
         "lvq_rms_norm": (i, [vp, i, i64, vp, i, vp, vp, i, ctypes.c_float, i, i, vp, i, vp, i,
                              vp]),
         "lvq_silu_mul": (i, [vp, vp, i, i64, i, i, vp, i, vp, i, vp]),
@@ -123,7 +128,7 @@ EXPORTED = ("lvq_strerror", "lvq_last_error_index", "lvq_class_table", "lvq_layo
             "lvq_rank", "lvq_gemv", "lvq_gemv_gain",
             "lvq_unfold", "lvq_gemv_fused", "lvq_gemv_noweights", "lvq_decode",
             "bpdq_gemv", "trellis_gemv", "fp16_gemv", "q4_gemv", "q4_gemv_q8",
-            "lvq_rms_norm", "lvq_silu_mul", "lvq_kv_page_bytes", "lvq_kv_append", "lvq_kv_read",
+            "q4_moe_workspace", "q4_moe", "lvq_rms_norm", "lvq_silu_mul", "lvq_kv_page_bytes", "lvq_kv_append", "lvq_kv_read",
             "lvq_attend_workspace", "lvq_attend", "lvq_rotate", "lvq_gemv_rotated",
             "lvq_stream_read", "lvq_stream_read_geom", "lvq_gemv_launch_info")
 
@@ -548,6 +553,62 @@ def q4_gemv_q8(codes, scale, zero, group: int, rows: int, cols: int, x, x_scale,
         _check(e)
 
 
+def q4_moe_workspace_bytes(tokens: int, hidden: int, inner: int, experts: int, top: int) -> int:
+    """Bytes of workspace that q4_moe() needs."""
+    sizes = [int(v) for v in (tokens, hidden, inner, experts, top)]
+    _in_32_bits(*sizes)
+    n = int(_lib.q4_moe_workspace(*sizes))
+    if n == 0:
+        _check(LVQ_E_SHAPE)
+    return n
+
+
+def q4_moe(x, router, gate_up, down, inner: int, top: int, y, workspace, renormalize: bool = True,
+           ids=None, weights=None, stream=None):
+    """Mixture-of-experts layer of up to 16 tokens.  x fp16 [tokens][hidden]; router fp32,
+    fp16 or bf16 [experts][hidden]; gate_up and down: (codes, scale, zero or None, group) of
+    the experts' matrices [2 inner][hidden] (the gate's rows first) and [hidden][inner] as
+    q4_gemv() takes them, one behind the other; y fp32 [tokens][hidden]; workspace: a uint8
+    tensor of q4_moe_workspace_bytes().  The weights of the chosen experts are a softmax over
+    all of them, or with renormalize over the `top` chosen.  ids (int32) and weights (fp32),
+    [tokens][top], are filled if given."""
+    inner, top = int(inner), int(top)
+    dev, stream = _here(stream)
+    if not (isinstance(x, _Tensor) and isinstance(router, _Tensor)):
+        _refuse(x if not isinstance(x, _Tensor) else router, "x and router", (), 0, 0, dev)
+    if len(x.shape) != 2 or len(router.shape) != 2:
+        raise ValueError("x and router must have two dimensions, rows and columns")
+    (tokens, hidden), experts = x.shape, router.shape[0]
+    gc, gs, gz, gg = gate_up
+    dc, ds, dz, dg = down
+    gg, dg = int(gg), int(dg)
+    _in_32_bits(tokens, hidden, inner, experts, top, gg, dg, 2 * experts * max(inner, hidden))
+    rp, rt = _typed(router, "router", _FLOATS, experts, hidden, dev)
+    n_gu, n_down = _n_groups(hidden, gg), _n_groups(inner, dg)
+    rows_gu, rows_down = experts * 2 * inner, experts * hidden
+    e = _lib.q4_moe(_array(x, "x", _F16_BITS, tokens, hidden, dev), tokens, hidden, rp, rt, experts,
+                    top, 1 if renormalize else 0, _codes(gc, rows_gu, -(-hidden // 32), dev),
+                    _array(gs, "scale", _F16_BITS, rows_gu, n_gu, dev),
+                    _array(gz, "zero", _F16_BITS, rows_gu, n_gu, dev), gg,
+                    _codes(dc, rows_down, -(-inner // 32), dev),
+                    _array(ds, "scale", _F16_BITS, rows_down, n_down, dev),
+                    _array(dz, "zero", _F16_BITS, rows_down, n_down, dev), dg, inner,
+                    _array(y, "y", _F32, tokens, hidden, dev),
+                    _array(ids, "ids", _types("int32"), tokens, top, dev),
+                    _array(weights, "weights", _F32, tokens, top, dev),
+                    *_space(workspace, dev), stream)
+    if e:
+        _check(e)
+
+
+def _space(t, dev):
+    """(address, bytes) of a workspace, a contiguous tensor of bytes."""
+    if not isinstance(t, _Tensor):
+        _refuse(t, "workspace", _BYTES, 0, 0, dev)
+    n = t.numel()
+    return _array(t, "workspace", _BYTES, 1, n, dev), n
+
+
 def _rows_of(t, name, dev):
     """(address, type, rows, cols, row stride) of a 2-D tensor of floats whose
     columns are adjacent."""
@@ -820,10 +881,7 @@ def attend(cache: KvCache, q, lens, out, workspace, queries: int = 1, window: in
     if rows != s.seqs * queries or cols % s.dim or qt == LVQ_F32:
         raise ValueError("q must be fp16 or bf16, %d rows of whole heads" % (s.seqs * queries))
     op, ot = _typed(out, "out", _FLOATS, rows, cols, dev)
-    wp, n = None, 0
-    if workspace is not None:
-        n = workspace.numel()
-        wp = _array(workspace, "workspace", _BYTES, 1, n, dev)
+    wp, n = (None, 0) if workspace is None else _space(workspace, dev)
     e = _lib.lvq_attend(ref, qp, qt, qstride, cols // s.dim, queries,
                         _index(lens, "lens", s.seqs, dev),
                         s.dim ** -0.5 if scale is None else scale, window, op, ot, wp, n, stream)

@@ -1,0 +1,741 @@
+// A mixture-of-experts layer in 4-bit weights for a few tokens (q4_moe).
+//
+//   l = R x, the `top` largest l are chosen, w = softmax(l) of the chosen
+//   y = sum_e w_e D_e (silu(G_e x) * (U_e x))
+//
+// Three launches, each needing all of the one before: the router's logits (a workgroup per
+// expert), the choice and the chosen experts' gate and up products with the activation,
+// the down products with the weighted sum.  The choice is a few hundred operations, so
+// every workgroup of the second launch makes it for itself.
+//
+// The products are those of the 4-bit matvec: 4x4x4 matrix products in 16 blocks, lane l
+// holding row l % 4 of a quad of rows and unit l / 4 of a step of 16 units of 32 columns; the
+// codes are fp16 subnormals (bits 6..9 of the mantissa), scale and zero are applied in the
+// lane in fp32.  Up to four tokens of an expert share a pass over its weights (a job).  x
+// sits in LDS.  The activations between the products are kept as two fp16, the rounded
+// value and the rest (22 bits), which the down product multiplies one after the other.
+
+#include "q4_dev.h"
+
+namespace lvq {
+
+constexpr float kMoeUnit = 0x1p-18f;   // of a code inside an fp16
+constexpr int kGateWaves = 16, kDownWaves = 8;
+constexpr int kMaxPairs = LVQ_MAX_MOE_TOKENS * LVQ_MAX_MOE_TOP;
+constexpr int kMaxExperts = 512;
+
+// ---------------------------------------------------------------- router
+
+struct RouterArgs {
+  const uint16_t* x;
+  const void* router;
+  float* logits;
+  int tokens, hidden, experts;
+  int type;
+};
+
+__device__ __forceinline__ float router_value(const void* p, int type, size_t i) {
+  if (type == LVQ_F32) return ((const float*)p)[i];
+  const uint32_t b = ((const uint16_t*)p)[i];
+  return type == LVQ_F16 ? f16_to_f32(b) : __builtin_bit_cast(float, b << 16);
+}
+
+// A workgroup: one expert, four tokens.
+__global__ void __launch_bounds__(256) moe_router_kernel(RouterArgs a) {
+  __shared__ float red[4][4];
+  const int e = blockIdx.x, t0 = blockIdx.y * 4;
+  const int n = a.tokens - t0 < 4 ? a.tokens - t0 : 4;
+  const size_t row = (size_t)e * a.hidden;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int c = threadIdx.x * 8; c < a.hidden; c += 256 * 8) {
+    float w[8];
+    const bool whole = c + 8 <= a.hidden;
+    if (whole && a.type == LVQ_F32) {
+      __builtin_memcpy(w, (const float*)a.router + row + c, 32);
+    } else if (whole) {
+      uint32_t r[4];
+      __builtin_memcpy(r, (const uint16_t*)a.router + row + c, 16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t b = (r[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+        w[i] = a.type == LVQ_F16 ? f16_to_f32(b) : __builtin_bit_cast(float, b << 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = c + i < a.hidden ? router_value(a.router, a.type, row + c + i) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= n) break;
+      const uint16_t* xr = a.x + (size_t)(t0 + k) * a.hidden + c;
+      uint32_t r[4] = {0, 0, 0, 0};
+      if (whole) {
+        __builtin_memcpy(r, xr, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i < a.hidden) r[i >> 1] |= (uint32_t)xr[i] << (16 * (i & 1));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (whole || c + i < a.hidden)
+          acc[k] = __builtin_fmaf(w[i], f16_to_f32((r[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), acc[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float s = wave_sum_lane63(acc[k]);
+    if ((threadIdx.x & 63) == 63) red[threadIdx.x >> 6][k] = s;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < n) {
+    const int k = threadIdx.x;
+    a.logits[(size_t)(t0 + k) * a.experts + e] = (red[0][k] + red[1][k]) + (red[2][k] + red[3][k]);
+  }
+}
+
+// ---------------------------------------------------------------- the choice
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_umax(uint32_t v) {
+  const uint32_t m = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+  return v > m ? v : m;
+}
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  v = dpp_umax<0xB1>(v);
+  v = dpp_umax<0x4E>(v);
+  v = dpp_umax<0x141>(v);
+  v = dpp_umax<0x140>(v);
+  auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = p[0] > p[1] ? p[0] : p[1];
+  auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return q[0] > q[1] ? q[0] : q[1];
+}
+
+// The top of a token's logits, by a wave: expert j goes to lane j's *id and *weight.
+// Values are compared as integers of the same order; equal ones go by their index.  A NaN
+// is below everything, and makes the token's weights NaN.
+__device__ __forceinline__ void choose(const float* logits, int experts, int top, bool renormalize,
+                                       int lane, int* id, float* weight) {
+  constexpr int S = kMaxExperts / kWave;
+  float v[S];
+  uint32_t key[S];
+  bool nan = false;
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const int e = s * kWave + lane;
+    v[s] = e < experts ? logits[e] + 0.f : -__builtin_inff();  // + 0: no negative zero
+    const uint32_t b = __builtin_bit_cast(uint32_t, v[s]);
+    key[s] = e >= experts ? 0u : v[s] != v[s] ? 1u : (b >> 31) ? ~b : b | 0x80000000u;
+    nan |= v[s] != v[s];
+  }
+  nan = __any(nan);
+  float best = 0.f, total = 0.f, mine = -__builtin_inff();
+  int chosen = 0;
+  for (int j = 0; j < top; ++j) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int s = 1; s < S; ++s) m = m > key[s] ? m : key[s];
+    m = wave_umax(m);
+    int e = 0;
+#pragma unroll
+    for (int s = S - 1; s >= 0; --s) {
+      const uint64_t who = __ballot(key[s] == m);
+      if (who) e = s * kWave + __builtin_ctzll(who);
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      if (s * kWave + lane == e) key[s] = 0u;
+    const float val = __builtin_bit_cast(float, (m >> 31) ? m & 0x7FFFFFFFu : ~m);
+    if (j == 0) {
+      best = val;
+      if (!renormalize) {
+        float sum = 0.f;
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+          if (s * kWave < experts) sum += expf(v[s] - best);
+        total = wave_sum(sum);
+      }
+    }
+    if (lane == j) chosen = e, mine = val;
+  }
+  const float p = lane < top ? expf(mine - best) : 0.f;
+  if (renormalize) total = wave_sum(p);
+  *id = chosen;
+  *weight = nan ? __builtin_nanf("") : p / total;
+}
+
+// The pairs (token, chosen expert) by expert, and the jobs: up to four tokens of one expert.
+struct Jobs {
+  uint16_t expert[kMaxPairs], first[kMaxPairs], count[kMaxPairs];
+  uint16_t pair[kMaxPairs];   // sorted by expert, then by token
+  uint16_t flags[kMaxPairs];
+  uint16_t ids[kMaxPairs];    // of each pair
+  int n;
+};
+
+// ids[] is filled; every thread of the workgroup calls.
+__device__ __forceinline__ void make_jobs(Jobs& j, int pairs, int threads) {
+  __syncthreads();
+  for (int p = threadIdx.x; p < pairs; p += threads) {
+    const int e = j.ids[p];
+    int before = 0, start = 0, same = 0;
+    for (int q = 0; q < pairs; ++q) {
+      const int o = j.ids[q];
+      start += o < e;
+      same += o == e;
+      before += o == e && q < p;
+    }
+    j.pair[start + before] = (uint16_t)p;
+    // a job starts at every fourth token of an expert; how many it holds
+    const int left = same - before;
+    j.flags[start + before] = (uint16_t)(before % 4 ? 0 : left < 4 ? left : 4);
+  }
+  __syncthreads();
+  if (threadIdx.x < kWave) {
+    int n = 0;
+    for (int p0 = 0; p0 < pairs; p0 += kWave) {
+      const int p = p0 + threadIdx.x;
+      const int c = p < pairs ? j.flags[p] : 0;
+      const uint64_t who = __ballot(c != 0);
+      if (c) {
+        const int at = n + __builtin_popcountll(who & ((1ull << threadIdx.x) - 1));
+        j.expert[at] = j.ids[j.pair[p]];
+        j.first[at] = (uint16_t)p, j.count[at] = (uint16_t)c;
+      }
+      n += __builtin_popcountll(who);
+    }
+    if (threadIdx.x == 0) j.n = n;
+  }
+  __syncthreads();
+}
+
+// ---------------------------------------------------------------- gate and up
+
+struct GateArgs {
+  const uint8_t* codes;
+  const uint16_t* scale;
+  const uint16_t* zero;
+  const uint16_t* x;
+  const float* logits;
+  int32_t* ids;      // workspace, then the caller's (may be NULL)
+  float* weights;
+  int32_t* ids_out;
+  float* weights_out;
+  uint16_t* act;     // [pairs][pitch] rounded values, then as many rests
+  int hidden, inner, wgs;
+  uint16_t tokens, experts, top;
+  uint8_t gshift, renormalize;
+};
+static_assert(sizeof(GateArgs) < 128, "launches of 128 bytes and more are slower");
+
+// LDS of x: a token's row of steps, each four words of 16 units; 32 bytes more than they
+// are long, so that four tokens' pieces lie in different banks.
+__host__ __device__ inline int x_row_bytes(int steps) { return steps * 1024 + 32; }
+inline size_t gate_lds_bytes(int tokens, int steps) {
+  return (size_t)tokens * (x_row_bytes(steps) + steps * 64);
+}
+
+// Four steps of codes of a gate and an up quad; scales (low) and zeros of their groups.
+template <int NS>
+struct GateChunk {
+  u32x4_t w[2][4];
+  uint16_t s[2][NS], z[2][NS];
+};
+
+template <int NS, bool Z>
+__global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ Jobs jobs;
+  const int nunits = (a.hidden + 31) / 32, steps = (nunits + 15) / 16;
+  const int groups = ((nunits - 1) >> a.gshift) + 1;
+  const int row_x = x_row_bytes(steps);
+  uint8_t* xs = smem;
+  float* sums = (float*)(smem + a.tokens * row_x);
+  const int lane = threadIdx.x & (kWave - 1), ul = lane >> 2, r4 = lane & 3;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // 1. x into LDS, and minus the sums of its units, as the products start from them
+  for (int i = wv; i < a.tokens * steps; i += kGateWaves) {
+    const int t = i / steps, st = i - t * steps, c = (st * 64 + lane) * 8;
+    const uint16_t* row = a.x + (size_t)t * a.hidden;
+    u32x4_t v = {0, 0, 0, 0};
+    if (c + 8 <= a.hidden) {
+      __builtin_memcpy(&v, row + c, 16);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < a.hidden) v[k >> 1] |= (uint32_t)row[c + k] << (16 * (k & 1));
+    }
+    *(u32x4_t*)(xs + t * row_x + st * 1024 + r4 * 256 + ul * 16) = pair_order(v);
+    constexpr uint32_t kOnes = 0x3C003C00u;
+    float s = dot2(v.x, kOnes, dot2(v.y, kOnes, dot2(v.z, kOnes, dot2(v.w, kOnes, 0.f))));
+    s = dpp_add<0x4E, 0xF>(dpp_add<0xB1, 0xF>(s));
+    if (r4 == 0) sums[(t * steps + st) * 16 + ul] = s * ((Z ? -1.f : -8.f) * kMoeUnit);
+  }
+
+  // 2. the choice
+  for (int t = wv; t < a.tokens; t += kGateWaves) {
+    int id;
+    float w;
+    choose(a.logits + (size_t)t * a.experts, a.experts, a.top, a.renormalize, lane, &id, &w);
+    if (lane < a.top) {
+      const int p = t * a.top + lane;
+      jobs.ids[p] = (uint16_t)id;
+      if (blockIdx.x == 0) {
+        a.ids[p] = id, a.weights[p] = w;
+        if (a.ids_out) a.ids_out[p] = id;
+        if (a.weights_out) a.weights_out[p] = w;
+      }
+    }
+  }
+  make_jobs(jobs, a.tokens * a.top, kGateWaves * kWave);
+
+  // 3. items: a job and four rows of the activation, whole rows of the weights
+  const int pitch = ((a.inner + 31) / 32) * 32, quads = pitch / 4;
+  const int row_bytes = nunits * 16, chunks = (steps + 3) / 4;
+  const int items = jobs.n * quads, stride = a.wgs * kGateWaves;
+  const size_t lo = (size_t)a.tokens * a.top * pitch;
+  struct Cursor {
+    int item, chunk;
+  };
+  Cursor ld = {(int)blockIdx.x * kGateWaves + wv, 0}, at = ld;
+  auto advance = [&](Cursor& c) {
+    if (++c.chunk == chunks) c.chunk = 0, c.item += stride;
+  };
+  const int lane_off = r4 * row_bytes + ul * 16;
+  GateChunk<NS> ring[2];
+  auto load = [&](GateChunk<NS>& k) {
+    if (ld.item >= items) return;
+    const int job = ld.item / quads, quad = ld.item - job * quads, t0 = ld.chunk * 4;
+    const size_t e = jobs.expert[job];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = quad * 4 + (h ? a.inner : 0), left = 2 * a.inner - row;
+      const int rows = left < 0 ? 0 : left < 4 ? left : 4;
+      const size_t first = e * 2 * a.inner + (rows ? row : 0);
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        const int t = t0 + n * (4 / NS);
+        const int g = ((t * 16) >> a.gshift) + ul;
+        const int off = ((r4 * groups + g) * 2) | ((groups - 1 - g) & (int)0x80000000);
+        const uint32_t bytes = t < steps ? (uint32_t)(rows * groups) * 2 : 0;
+        k.s[h][n] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.scale + first * groups, bytes),
+                                                         off, 0, 0);
+        if constexpr (Z)
+          k.z[h][n] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.zero + first * groups, bytes),
+                                                           off, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = quad * 4 + (h ? a.inner : 0), left = 2 * a.inner - row;
+      const int rows = left < 0 ? 0 : left < 4 ? left : 4;
+      const size_t first = e * 2 * a.inner + (rows ? row : 0);
+      const uint8_t* base = a.codes + first * row_bytes + t0 * 256;
+      const uint32_t bytes = rows ? rows * row_bytes - t0 * 256 : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        k.w[h][i] = __builtin_bit_cast(
+            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(q4_rsrc(base, t0 + i < steps ? bytes : 0),
+                                                           lane_off, i * 256, 2));
+    }
+    advance(ld);
+  };
+  float acc[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) acc[h][b] = 0.f;
+  const int from = (((ul >> a.gshift) << 2) | r4) << 2, from_step = (16 >> a.gshift) << 4;
+  auto consume = [&](const GateChunk<NS>& k) {
+    if (at.item >= items) return;
+    const int job = at.item / quads, quad = at.item - job * quads, t0 = at.chunk * 4;
+    const int first = jobs.first[job], nb = jobs.count[job];
+    auto token = [&](int b) { return (int)jobs.pair[first + (b < nb ? b : 0)] / a.top; };
+    const uint8_t* xl = xs + token(r4) * row_x + ul * 16 + t0 * 1024;
+    const float* sl[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) sl[b] = sums + (token(b) * steps + t0) * 16 + ul;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (t0 + i >= steps) break;
+      constexpr int SPL = 4 / NS;
+      uint32_t sz[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sz[h] = (uint32_t)k.s[h][i / SPL] | (Z ? (uint32_t)k.z[h][i / SPL] << 16 : 0x48000000u);
+        if constexpr (NS < 4)
+          sz[h] = (uint32_t)__builtin_amdgcn_ds_bpermute(from + (i % SPL) * from_step, (int)sz[h]);
+      }
+      float sx[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) sx[b] = sl[b][i * 16];
+      float4_t c[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) c[h][b] = Z ? f16_to_f32(sz[h] >> 16) * sx[b] : sx[b];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const u32x4_t x = *(const u32x4_t*)(xl + i * 1024 + w * 256);
+        constexpr uint32_t m = 0x03C003C0u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t q = k.w[h][i][w];
+          c[h] = __builtin_amdgcn_mfma_f32_4x4x4f16(
+              __builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}),
+              __builtin_bit_cast(half4_t, u32x2_t{(q << 6) & m, (q >> 2) & m}), c[h], 0, 0, 0);
+          c[h] = __builtin_amdgcn_mfma_f32_4x4x4f16(
+              __builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}),
+              __builtin_bit_cast(half4_t, u32x2_t{(q << 2) & m, (q >> 6) & m}), c[h], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float s = f16_to_f32(sz[h]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) acc[h][b] = __builtin_fmaf(s, c[h][b], acc[h][b]);
+      }
+    }
+    advance(at);
+    if (at.chunk) return;
+    // the rows' end: sums over the units, the activation in lane 4 b + i of token b, row i
+    float g = 0.f, u = 0.f;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (b < nb) {
+        const float gb = sum_blocks(acc[0][b]), ub = sum_blocks(acc[1][b]);
+        g = ul == b ? gb : g, u = ul == b ? ub : u;
+      }
+      acc[0][b] = acc[1][b] = 0.f;
+    }
+    if (ul < nb) {
+      g *= 1.f / kMoeUnit, u *= 1.f / kMoeUnit;
+      // a quarter of 1 + e^-g is inverted: the hardware's 1/v is 0 where it would be subnormal
+      const float e = __builtin_amdgcn_exp2f(g * -1.44269504f);
+      float v = g * 0.25f * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0.25f, 0.25f)) * u;
+      const int row = quad * 4 + r4;
+      if (row >= a.inner) v = 0.f;
+      const _Float16 hi = (_Float16)v, rest = (_Float16)(v - (float)hi);
+      // in the order of the operands' pairs: bits of the column within eight reversed
+      const int col = (row & ~7) | (row & 1) << 2 | (row & 2) | (row >> 2 & 1);
+      const size_t to = (size_t)jobs.pair[first + ul] * pitch + col;
+      a.act[to] = __builtin_bit_cast(uint16_t, hi);
+      a.act[lo + to] = __builtin_bit_cast(uint16_t, rest);
+    }
+  };
+  load(ring[0]);
+  load(ring[1]);
+  while (at.item < items) {
+    consume(ring[0]);
+    load(ring[0]);
+    consume(ring[1]);
+    load(ring[1]);
+  }
+}
+
+// ---------------------------------------------------------------- down
+
+struct DownArgs {
+  const uint8_t* codes;
+  const uint16_t* scale;
+  const uint16_t* zero;
+  const uint16_t* act;
+  const int32_t* ids;
+  const float* weights;
+  float* y;
+  int hidden, inner;
+  uint16_t tokens, top;
+  uint8_t gshift;
+};
+static_assert(sizeof(DownArgs) < 128, "launches of 128 bytes and more are slower");
+
+// A workgroup: NQ quads of rows, all jobs; their steps are dealt to the waves in equal parts.
+template <int NQ, bool Z>
+__global__ void __launch_bounds__(kDownWaves* kWave) moe_down_kernel(DownArgs a) {
+  constexpr int R = 4 * NQ;
+  __shared__ Jobs jobs;
+  __shared__ float wts[kMaxPairs];
+  __shared__ float part[kDownWaves][LVQ_MAX_MOE_TOKENS * R];
+  const int lane = threadIdx.x & (kWave - 1), ul = lane >> 2, r4 = lane & 3;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int pairs = a.tokens * a.top;
+  for (int p = threadIdx.x; p < pairs; p += kDownWaves * kWave) {
+    jobs.ids[p] = (uint16_t)a.ids[p];
+    wts[p] = a.weights[p];
+  }
+  for (int i = lane; i < a.tokens * R; i += kWave) part[wv][i] = 0.f;
+  make_jobs(jobs, pairs, kDownWaves * kWave);
+
+  const int nunits = (a.inner + 31) / 32, steps = (nunits + 15) / 16;
+  const int groups = ((nunits - 1) >> a.gshift) + 1;
+  const int pitch = nunits * 32, row_bytes = nunits * 16;
+  const int all = jobs.n * steps, per = (all + kDownWaves - 1) / kDownWaves;
+  const int f0 = wv * per < all ? wv * per : all, f1 = f0 + per < all ? f0 + per : all;
+  const int row0 = blockIdx.x * R;
+  const uint32_t act_bytes = (uint32_t)pairs * pitch * 2;
+
+  struct Step {
+    u32x4_t x[2][4];
+    u32x4_t w[NQ];
+    uint16_t s[NQ], z[NQ];
+  };
+  struct Cursor {
+    int f, job, t;
+  };
+  auto start = [&](int f) { return Cursor{f, f / steps, f - f / steps * steps}; };
+  auto next = [&](Cursor& c) {
+    ++c.f;
+    if (++c.t == steps) c.t = 0, ++c.job;
+  };
+  Cursor ld = start(f0), at = ld;
+  auto load = [&](Step& k) {
+    if (ld.f >= f1) return;
+    const int first = jobs.first[ld.job], nb = jobs.count[ld.job];
+    const size_t e = jobs.expert[ld.job];
+    const int u = ld.t * 16 + ul;
+    const int pair = jobs.pair[first + (r4 < nb ? r4 : 0)];
+    const bool none = r4 >= nb || u >= nunits;
+    const uint32_t xo = none ? 0x80000000u : (uint32_t)pair * (pitch * 2) + u * 64;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const int row = row0 + 4 * q, left = a.hidden - row;
+      const int rows = left < 0 ? 0 : left < 4 ? left : 4;
+      const size_t fr = e * a.hidden + (rows ? row : 0);
+      const int g = u >> a.gshift;
+      const int off = ((r4 * groups + g) * 2) | ((groups - 1 - g) & (int)0x80000000);
+      const uint32_t sb = (uint32_t)(rows * groups) * 2;
+      k.s[q] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.scale + fr * groups, sb), off, 0, 0);
+      if constexpr (Z)
+        k.z[q] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.zero + fr * groups, sb), off, 0, 0);
+      const uint32_t bytes = rows ? rows * row_bytes - ld.t * 256 : 0;
+      k.w[q] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                       q4_rsrc(a.codes + fr * row_bytes + ld.t * 256, bytes),
+                       r4 * row_bytes + ul * 16, 0, 2));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        k.x[h][w] = __builtin_bit_cast(
+            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                         q4_rsrc((const uint8_t*)a.act + (size_t)h * act_bytes, act_bytes), (int)xo,
+                         w * 16, 0));
+    next(ld);
+  };
+  float acc[NQ][4];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) acc[q][b] = 0.f;
+  auto consume = [&](const Step& k) {
+    if (at.f >= f1) return;
+    constexpr uint32_t kOne = 0x00400040u, m = 0x03C003C0u;
+    const half4_t ones = __builtin_bit_cast(half4_t, u32x2_t{kOne, kOne});
+    float4_t sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const u32x4_t x = k.x[h][w];
+        sum = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}),
+                                                 ones, sum, 0, 0, 0);
+        sum = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}),
+                                                 ones, sum, 0, 0, 0);
+      }
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const float z = Z ? -f16_to_f32(k.z[q]) : -8.f;
+      float4_t c;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) c[b] = z * sum[b];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t v = k.w[q][w];
+        const half4_t lo = __builtin_bit_cast(half4_t, u32x2_t{(v << 6) & m, (v >> 2) & m});
+        const half4_t hi = __builtin_bit_cast(half4_t, u32x2_t{(v << 2) & m, (v >> 6) & m});
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const u32x4_t x = k.x[h][w];
+          c = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}), lo,
+                                                 c, 0, 0, 0);
+          c = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}), hi,
+                                                 c, 0, 0, 0);
+        }
+      }
+      const float s = f16_to_f32(k.s[q]);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) acc[q][b] = __builtin_fmaf(s, c[b], acc[q][b]);
+    }
+    const int job = at.job;
+    next(at);
+    if (at.f < f1 && at.t) return;
+    const int first = jobs.first[job], nb = jobs.count[job];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      float v = 0.f;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (b < nb) {
+          const float s = sum_blocks(acc[q][b]);
+          v = ul == b ? s : v;
+        }
+        acc[q][b] = 0.f;
+      }
+      if (ul < nb) {
+        const int p = jobs.pair[first + ul];
+        float* to = &part[wv][p / a.top * R + 4 * q + r4];
+        *to = __builtin_fmaf(wts[p], v * (1.f / kMoeUnit), *to);
+      }
+    }
+  };
+  Step ring[2];
+  load(ring[0]);
+  load(ring[1]);
+  while (at.f < f1) {
+    consume(ring[0]);
+    load(ring[0]);
+    consume(ring[1]);
+    load(ring[1]);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.tokens * R; i += kDownWaves * kWave) {
+    const int t = i / R, r = row0 + i - t * R;
+    float v = part[0][i];
+#pragma unroll
+    for (int w = 1; w < kDownWaves; ++w) v += part[w][i];
+    if (r < a.hidden) a.y[(size_t)t * a.hidden + r] = v;
+  }
+}
+
+// ---------------------------------------------------------------- launch
+
+struct MoeSpace {
+  size_t logits, ids, weights, act, all;
+};
+inline MoeSpace moe_space(int tokens, int inner, int experts, int top) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  MoeSpace s;
+  const size_t pairs = (size_t)tokens * top;
+  s.logits = 0;
+  s.ids = up((size_t)tokens * experts * 4);
+  s.weights = s.ids + up(pairs * 4);
+  s.act = s.weights + up(pairs * 4);
+  s.all = s.act + up(pairs * ((inner + 31) / 32 * 32) * 4);
+  return s;
+}
+
+inline bool moe_sizes_ok(int tokens, int hidden, int inner, int experts, int top) {
+  return tokens >= 0 && tokens <= LVQ_MAX_MOE_TOKENS && hidden >= 1 && inner >= 1 &&
+         hidden <= 65536 && inner <= 65536 && (long long)tokens * hidden <= 65536 &&
+         experts >= 1 && experts <= kMaxExperts && top >= 1 && top <= LVQ_MAX_MOE_TOP &&
+         top <= experts;
+}
+
+template <int NS, bool Z>
+int launch_gate(const GateArgs& a, size_t lds, hipStream_t st) {
+  hipLaunchKernelGGL((moe_gate_kernel<NS, Z>), dim3(a.wgs), dim3(kGateWaves * kWave), lds, st, a);
+  return launch_status();
+}
+template <bool Z>
+int launch_gate(const GateArgs& a, size_t lds, hipStream_t st) {
+  return a.gshift == 0   ? launch_gate<4, Z>(a, lds, st)
+         : a.gshift == 1 ? launch_gate<2, Z>(a, lds, st)
+                         : launch_gate<1, Z>(a, lds, st);
+}
+
+template <int NQ>
+int launch_down(const DownArgs& a, hipStream_t st) {
+  const dim3 grid((a.hidden + 4 * NQ - 1) / (4 * NQ)), block(kDownWaves * kWave);
+  if (a.zero) hipLaunchKernelGGL((moe_down_kernel<NQ, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((moe_down_kernel<NQ, false>), grid, block, 0, st, a);
+  return launch_status();
+}
+
+struct MoeRange {
+  const void* p;
+  size_t n;
+};
+
+}  // namespace lvq
+
+using namespace lvq;
+
+extern "C" size_t q4_moe_workspace(int tokens, int hidden, int inner, int experts, int top) {
+  return moe_sizes_ok(tokens, hidden, inner, experts, top)
+             ? moe_space(tokens, inner, experts, top).all : 0;
+}
+
+extern "C" int q4_moe(const uint16_t* x, int tokens, int hidden, const void* router,
+                      int router_type, int experts, int top, int renormalize,
+                      const uint8_t* gu_codes, const uint16_t* gu_scale, const uint16_t* gu_zero,
+                      int gu_group, const uint8_t* down_codes, const uint16_t* down_scale,
+                      const uint16_t* down_zero, int down_group, int inner, float* y,
+                      int32_t* ids_out, float* weights_out, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  const int gs = group_shift(gu_group), ds = group_shift(down_group);
+  if (!moe_sizes_ok(tokens, hidden, inner, experts, top) || gs < 0 || ds < 0 ||
+      (router_type != LVQ_F32 && router_type != LVQ_F16 && router_type != LVQ_BF16) ||
+      renormalize < 0 || renormalize > 1)
+    return LVQ_E_SHAPE;
+  if (tokens == 0) return LVQ_OK;
+  if (!x || !router || !gu_codes || !gu_scale || !down_codes || !down_scale || !y || !workspace)
+    return LVQ_E_NULL;
+  const void* all[] = {x, router, gu_codes, gu_scale, gu_zero, down_codes, down_scale, down_zero, y,
+                       ids_out, weights_out, workspace};
+  for (const void* p : all)
+    if (!aligned16(p)) return LVQ_E_ALIGN;
+  const MoeSpace sp = moe_space(tokens, inner, experts, top);
+  if (workspace_bytes < sp.all) return LVQ_E_SHAPE;
+  const size_t pairs = (size_t)tokens * top;
+  const size_t gu_rows = (size_t)experts * 2 * inner, down_rows = (size_t)experts * hidden;
+  const size_t gu_meta = gu_rows * group_count(hidden, gu_group) * 2;
+  const size_t down_meta = down_rows * group_count(inner, down_group) * 2;
+  const MoeRange in[8] = {{x, (size_t)tokens * hidden * 2},
+                          {router, (size_t)experts * hidden * (router_type == LVQ_F32 ? 4 : 2)},
+                          {gu_codes, gu_rows * units_of(hidden) * 16},
+                          {gu_scale, gu_meta},
+                          {gu_zero, gu_meta},
+                          {down_codes, down_rows * units_of(inner) * 16},
+                          {down_scale, down_meta},
+                          {down_zero, down_meta}};
+  const MoeRange made[4] = {{y, (size_t)tokens * hidden * 4},
+                            {ids_out, pairs * 4},
+                            {weights_out, pairs * 4},
+                            {workspace, sp.all}};
+  for (int i = 0; i < 4; ++i) {
+    for (const MoeRange& r : in)
+      if (ranges_overlap(made[i].p, made[i].n, r.p, r.n)) return LVQ_E_SHAPE;
+    for (int j = i + 1; j < 4; ++j)
+      if (ranges_overlap(made[i].p, made[i].n, made[j].p, made[j].n)) return LVQ_E_SHAPE;
+  }
+  const int steps = steps_of(hidden);
+  const size_t lds = gate_lds_bytes(tokens, steps);
+  if (lds + sizeof(Jobs) > device_lds_bytes()) return LVQ_E_SHAPE;
+  uint8_t* w = (uint8_t*)workspace;
+  hipStream_t st = (hipStream_t)stream;
+  RouterArgs r = {x, router, (float*)(w + sp.logits), tokens, hidden, experts, router_type};
+  clear_hip_error();
+  hipLaunchKernelGGL(moe_router_kernel, dim3(experts, (tokens + 3) / 4), dim3(256), 0, st, r);
+  int e = launch_status();
+  if (e) return e;
+  GateArgs g;
+  g.codes = gu_codes, g.scale = gu_scale, g.zero = gu_zero, g.x = x;
+  g.logits = r.logits, g.ids = (int32_t*)(w + sp.ids), g.weights = (float*)(w + sp.weights);
+  g.ids_out = ids_out, g.weights_out = weights_out, g.act = (uint16_t*)(w + sp.act);
+  g.hidden = hidden, g.inner = inner;
+  g.tokens = (uint16_t)tokens, g.experts = (uint16_t)experts, g.top = (uint16_t)top;
+  g.gshift = (uint8_t)gs, g.renormalize = (uint8_t)renormalize;
+  // at most a job per pair
+  const long long items = (long long)pairs * units_of(inner) * 8;
+  const long long wgs = (items + kGateWaves - 1) / kGateWaves;
+  g.wgs = wgs < device_cus() ? (int)wgs : device_cus();
+  e = gu_zero ? launch_gate<true>(g, lds, st) : launch_gate<false>(g, lds, st);
+  if (e) return e;
+  DownArgs d = {down_codes, down_scale, down_zero, g.act, g.ids, g.weights, y, hidden, inner,
+                (uint16_t)tokens, (uint16_t)top, (uint8_t)ds};
+  return hidden >= 16 * device_cus() ? launch_down<4>(d, st) : launch_down<2>(d, st);
+}

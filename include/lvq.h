@@ -18,7 +18,7 @@
  * group scales for the projections that do not stand two bits (fp16 or 8-bit x),
  * the root-mean-square norm of a residual stream and the gated activation, with
  * fp16 or 8-bit outputs that the 4-bit arm reads; the key/value cache in 4 bits and
- * the attention over it.
+ * the attention over it; a mixture-of-experts layer in the 4-bit weights.
  *
  * Conventions shared by every function.
  *   - Return value: LVQ_OK (0) or a negative LVQ_E_* code.  No exception or
@@ -411,6 +411,40 @@ int q4_gemv(const uint8_t* codes, const uint16_t* scale, const uint16_t* zero, i
 int q4_gemv_q8(const uint8_t* codes, const uint16_t* scale, const uint16_t* zero, int group,
                int rows, int cols, const void* x, int x_type, const float* x_scale, int x_group,
                float* y, int batch, void* stream);
+
+/* Mixture-of-experts layer of a few tokens in 4-bit weights:
+ *   l = router x;  the `top` largest l are chosen, equal ones by the lower index
+ *   w = exp(l) / sum exp(l), the sum over all experts, or with renormalize 1 over the chosen
+ *   y = sum over the chosen e of w_e down_e (silu(gate_e x) * (up_e x))
+ *   x            fp16 [tokens][hidden], tokens 0..LVQ_MAX_MOE_TOKENS, tokens * hidden <= 65536
+ *   router       fp32, fp16 or bf16 (router_type) [experts][hidden], experts 1..512
+ *   top          1..LVQ_MAX_MOE_TOP, at most experts
+ *   gu_*         codes, scale, zero (or NULL) and group of [experts][2 inner][hidden] matrices
+ *                as q4_gemv reads them, an expert's behind the other's; rows 0..inner - 1 are
+ *                the gate's, the others up's
+ *   down_*       the same of [experts][hidden][inner] matrices
+ *   hidden, inner  1..65536, any numbers
+ *   y            fp32 [tokens][hidden]
+ *   ids_out, weights_out  int32 and fp32 [tokens][top], largest first; either may be NULL
+ *   workspace    device, q4_moe_workspace bytes, its content of no account before and after;
+ *                calls that may run at the same time need one each
+ * Logits, sums and weights are fp32; an activation is kept as two fp16, the rounded value
+ * and the rest (22 bits), so one past 65504 is infinite, as in lvq_silu_mul's fp16 output, and
+ * one below 2^-14 is off by 2^-25.  A NaN among a token's logits makes its weights NaN.  An
+ * infinity in x gives NaN in its token.  Tokens do not affect each other's values, and the
+ * result is the same from run to run; the order of its sums depends on the sizes, the
+ * device and, for the sum over the experts, on which are chosen by the tokens together.
+ * LVQ_E_SHAPE for any other size, a short workspace, or an output over an input or another
+ * output; all pointers 16-byte aligned. */
+#define LVQ_MAX_MOE_TOKENS 16
+#define LVQ_MAX_MOE_TOP 16
+size_t q4_moe_workspace(int tokens, int hidden, int inner, int experts, int top);
+int q4_moe(const uint16_t* x, int tokens, int hidden, const void* router, int router_type,
+           int experts, int top, int renormalize, const uint8_t* gu_codes,
+           const uint16_t* gu_scale, const uint16_t* gu_zero, int gu_group,
+           const uint8_t* down_codes, const uint16_t* down_scale, const uint16_t* down_zero,
+           int down_group, int inner, float* y, int32_t* ids_out, float* weights_out,
+           void* workspace, size_t workspace_bytes, void* stream);
 
 /* Root-mean-square norm of a residual stream, between two projections:
  *   h = x + residual                       (fp32; h = x when residual is NULL)

@@ -22,6 +22,7 @@ layout  the expected logical planes of a Leech block and an independent
 rotate  the activation rotation (H kron Q)(S x) with its error bound.
 q4      f64 weights of the 4-bit format, values of 8-bit activations.
 kv      the pages of the 4-bit key/value cache and attention over them, with its bound.
+moe     the mixture-of-experts layer with its bound.
 norm    the root-mean-square norm, the gated activation and the 8-bit rounding
         with group scales, each with its error bound.
 index   the 47-bit rank / unrank of the m <= 12 ball, the 48-bit word and

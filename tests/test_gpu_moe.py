@@ -1,0 +1,219 @@
+"""The mixture-of-experts layer on the GPU against the f64 oracle (bounds: oracle/moe.py)."""
+import numpy as np
+import pytest
+
+from oracle import moe as om
+from oracle import q4 as oq
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import dequant_gemv_lvq_amd as lvq  # noqa: E402
+from gpu_util import DEV  # noqa: E402
+
+FLOATS = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+class Weights:
+    """Matrices [experts][rows][cols] in 4 bits, random bytes in the rows' padding too."""
+
+    def __init__(self, r, experts, rows, cols, group, zeros):
+        self.rows, self.cols, self.group = rows, cols, group
+        n = -(-cols // group) if group else 1
+        self.codes = r.integers(0, 256, (experts, rows, -(-cols // 32) * 16)).astype(np.uint8)
+        scale = 0.25 * cols ** -0.5 * r.uniform(0.5, 1.5, (experts, rows, n))
+        self.scale = scale.astype(np.float16)
+        self.zero = r.integers(0, 16, (experts, rows, n)).astype(np.float16) if zeros else None
+
+    def dev(self):
+        up = lambda a: None if a is None else torch.from_numpy(a).to(DEV)  # noqa: E731
+        return up(self.codes), up(self.scale), up(self.zero), self.group
+
+    def expert(self, e):
+        z = None if self.zero is None else self.zero[e].view(np.uint16)
+        return oq.weights(self.codes[e], self.scale[e].view(np.uint16), z, self.rows, self.cols,
+                          self.group)
+
+
+class Layer:
+    def __init__(self, hidden, inner, experts, top, group=128, zeros=True, renormalize=True,
+                 router="f16", seed=0):
+        r = np.random.default_rng(seed)
+        self.hidden, self.inner, self.experts, self.top = hidden, inner, experts, top
+        self.renormalize = renormalize
+        self.router = torch.from_numpy(2 * hidden ** -0.5 * r.standard_normal((experts, hidden))).to(
+            FLOATS[router])
+        self.gu = Weights(r, experts, 2 * inner, hidden, group, zeros)
+        self.down = Weights(r, experts, hidden, inner, group, zeros)
+        self.args = (self.router.to(DEV), self.gu.dev(), self.down.dev(), inner, top)
+
+    def x(self, tokens, seed=1):
+        r = np.random.default_rng(seed)
+        v = r.standard_normal((tokens, self.hidden))
+        v[:, r.random(self.hidden) < 0.01] *= 10
+        return torch.from_numpy(v).half().to(DEV)
+
+    def space(self, tokens):
+        n = lvq.q4_moe_workspace_bytes(tokens, self.hidden, self.inner, self.experts, self.top)
+        return torch.full((n + 64,), 0xFF, dtype=torch.uint8, device=DEV)
+
+    def run(self, x, stream=None):
+        tokens = x.shape[0]
+        y = torch.full((tokens * self.hidden + 32,), float("nan"), device=DEV)
+        ids = torch.full((tokens * self.top + 32,), -9, dtype=torch.int32, device=DEV)
+        w = torch.full((tokens * self.top + 32,), float("nan"), device=DEV)
+        space = self.space(tokens)
+        lvq.q4_moe(x, *self.args, y[:tokens * self.hidden], space[:-64],
+                   renormalize=self.renormalize, ids=ids[:tokens * self.top],
+                   weights=w[:tokens * self.top], stream=stream)
+        torch.cuda.synchronize()
+        assert (space[-64:] == 0xFF).all() and y[tokens * self.hidden:].isnan().all()
+        assert (ids[tokens * self.top:] == -9).all() and w[tokens * self.top:].isnan().all()
+        return (y[:-32].view(tokens, -1), ids[:-32].view(tokens, -1), w[:-32].view(tokens, -1))
+
+    def check(self, x):
+        y, ids, w = self.run(x)
+        xh, rh = x.double().cpu().numpy(), self.router.double().numpy()
+        want_ids, want_w, dw, gap = om.choose(xh, rh, self.top, self.renormalize)
+        assert gap > 1, "the inputs leave the choice open"
+        assert np.array_equal(ids.cpu().numpy(), want_ids)
+        assert (np.abs(w.double().cpu().numpy() - want_w) <= dw).all()
+        want, tol = om.layer(xh, want_ids, want_w, dw, self.gu.expert, self.down.expert)
+        err = np.abs(y.double().cpu().numpy() - want)
+        ratio = float((err / tol).max())
+        rel = float(np.linalg.norm(err) / np.linalg.norm(want))
+        print("moe %d tokens %dx%d, %d of %d: err/tol %.3g, norm %.3g" % (
+            x.shape[0], self.hidden, self.inner, self.top, self.experts, ratio, rel), flush=True)
+        assert ratio <= 1
+        return y
+
+
+SHAPES = [  # hidden, inner, experts, top, group: one value, tiles cut short, several steps
+    (1, 1, 1, 1, 0), (31, 33, 3, 2, 32), (32, 32, 4, 4, 32), (100, 70, 5, 1, 64), (512, 64, 8, 2, 128),
+    (513, 513, 3, 3, 256), (1001, 331, 13, 3, 32), (1536, 1000, 6, 2, 0), (2048, 768, 64, 8, 128),
+    (4096, 1024, 9, 2, 64), (128, 2500, 4, 2, 128), (256, 96, 512, 16, 32), (200, 40, 65, 5, 0)]
+
+
+@pytest.mark.parametrize("hidden,inner,experts,top,group", SHAPES)
+@pytest.mark.parametrize("zeros", [False, True])
+def test_layer(hidden, inner, experts, top, group, zeros):
+    m = Layer(hidden, inner, experts, top, group, zeros, renormalize=zeros)
+    for tokens in (1, 2, 3, 7, 16):
+        # the inputs whose choice is clear (a token of one value leaves most open)
+        for seed in range(20):
+            x = m.x(tokens, seed)
+            if om.choose(x.double().cpu().numpy(), m.router.double().numpy(), top, True)[3] > 1:
+                break
+        m.check(x)
+
+
+@pytest.mark.parametrize("router", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_router_types(router, renormalize):
+    m = Layer(1000, 96, 37, 4, 64, False, renormalize, router, seed=3)
+    m.check(m.x(5))
+
+
+def test_largest_x():
+    m = Layer(4096, 64, 4, 2, 128, True)
+    m.check(m.x(16))
+    m = Layer(65536, 32, 2, 1, 0, True)
+    m.check(m.x(1))
+    m = Layer(64, 65536, 2, 2, 128, False)
+    m.check(m.x(2))
+
+
+def test_all_tokens_through_one_expert():
+    """One expert far above the others for every token: jobs of four tokens, the last short."""
+    m = Layer(256, 80, 6, 2, 32, True)
+    x = m.x(15)
+    m.router[3] = x.double().mean(0).cpu()
+    base = x.double().cpu().numpy()
+    m.router[3] = torch.from_numpy(np.sign(base[0]) * 0.5).half()
+    same = torch.from_numpy(np.abs(base) * np.sign(base[0])).half().to(DEV)
+    m.args = (m.router.to(DEV),) + m.args[1:]
+    m.check(same)
+    assert (m.run(same)[1][:, 0] == 3).all()
+
+
+@pytest.mark.parametrize("top", [1, 2, 5])
+def test_ties_go_to_the_lowest_index(top):
+    m = Layer(64, 32, 200, top, 32, False)
+    m.router[:] = m.router[7]
+    m.router[100:] = -m.router[7]
+    m.args = (m.router.to(DEV),) + m.args[1:]
+    x = m.x(4)
+    _, ids, w = m.run(x)
+    up = (x.double().cpu() @ m.router[7].double()) > 0
+    for t in range(4):
+        first = 0 if up[t] else 100
+        assert ids[t].tolist() == list(range(first, first + top))
+        assert torch.equal(w[t], w[t, :1].expand(top))
+    m.router[:] = 0  # zeros of both signs
+    x = -x.abs()
+    m.args = (m.router.to(DEV),) + m.args[1:]
+    assert m.run(x)[1].tolist() == [list(range(top))] * 4
+
+
+def test_a_token_does_not_change_the_others():
+    m = Layer(300, 100, 8, 2, 64, True)
+    x = m.x(6)
+    y, ids, w = m.run(x)
+    for bad in (float("nan"), float("inf")):
+        z = x.clone()
+        z[2, 5] = bad
+        y2, ids2, w2 = m.run(z)
+        keep = [0, 1, 3, 4, 5]
+        assert y2[2].isnan().all()
+        assert torch.equal(ids2[keep], ids[keep]) and torch.equal(w2[keep], w[keep])
+        # its experts are others, so the order of the sum may be too
+        assert (y2[keep] - y[keep]).abs().max() <= 1e-5 * y[keep].abs().max()
+
+
+def test_scales_that_are_not_finite():
+    """A scale of a row of one expert's down matrix: that channel, in the tokens that chose it."""
+    m = Layer(300, 100, 8, 2, 64, False)
+    x = m.x(6)
+    y, ids, _ = m.run(x)
+    e = int(ids[1, 0])
+    m.down.scale[e, 17, 1] = np.inf
+    m.args = m.args[:2] + (m.down.dev(),) + m.args[3:]
+    y2 = m.run(x)[0]
+    hit = (ids == e).any(1)
+    assert not y2[hit, 17].isfinite().any()
+    y2[hit, 17] = y[hit, 17]
+    assert torch.equal(y2, y)
+
+
+def test_determinism_streams_and_graphs():
+    """Two captured layers over one workspace, replayed in turn with eager work and new inputs."""
+    layers = [Layer(512, 200, 16, 3, 32, True, seed=s) for s in (5, 6)]
+    tokens = 3
+    xs = [m.x(tokens) for m in layers]
+    space = torch.empty(max(m.space(tokens).numel() for m in layers), dtype=torch.uint8, device=DEV)
+    ys = [torch.empty(tokens, 512, device=DEV) for _ in layers]
+    a = layers[0].run(xs[0])
+    for _ in range(3):
+        assert all(torch.equal(p, q) for p, q in zip(layers[0].run(xs[0]), a))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        lvq.q4_moe(xs[0], *layers[0].args, ys[0], space)
+    s.synchronize()
+    assert torch.equal(ys[0], a[0])
+    graphs = []
+    for m, x, y in zip(layers, xs, ys):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            lvq.q4_moe(x, *m.args, y, space)
+        graphs.append(g)
+    for i in range(5):
+        for m, x in zip(layers, xs):
+            x.copy_(m.x(tokens, 10 + i))
+        for g in graphs:
+            g.replay()
+        for m, x, y in zip(layers, xs, ys):
+            assert torch.equal(y, m.run(x)[0])
