@@ -14,12 +14,15 @@
 // each pair, and the pages hold the codes in the order in which these pairs are
 // operands.  p s is split into two fp16, the rounded value and the rest.
 //
-// A wave takes 64 tokens at a time, four blocks of 16.  Keys: four 16x16 products (rows
-// by tokens) of dim / 32 steps; lane 16 b + t then holds token t of block b and four
-// rows (with 4 or 8 rows the 16 of the product repeat them, and every lane keeps what is
-// its own).  The weights p pass through LDS to become operands again: product of the
-// values' channels by rows.  Workgroups of four waves split a sequence further, and a
-// second launch joins their parts (flash decoding).
+// A wave takes 64 tokens at a time, four blocks of 16.  Keys: four products of 16 tokens by
+// 16 rows in dim / 32 steps.  Row 4 b + i of product j is token 4 j + i of block b, so that
+// lane 16 b + r leaves them with the 16 tokens of block b for row r: exactly the operand
+// that the product of the values' channels by rows needs, whose steps run over those tokens.
+// Weights never leave their lane.  With 4 or 8 rows the 16 columns repeat them; a
+// lane then keeps one or two of its four products' tokens, and its other weights are zeros
+// (the columns are summed at the end), so no exponential is computed twice.  Scales
+// pass through LDS, to the lanes that need the scales of their tokens.  Workgroups split
+// a sequence further, and a second launch joins their parts (flash decoding).
 
 #include "kv_cache.h"
 
@@ -33,7 +36,6 @@ constexpr int kAttWaves = 4;
 constexpr int kAttTokens = 64;  // of a wave at a time
 constexpr uint32_t kCodeMask = 0x03C003C0u;
 constexpr float kCodeUnit = 0x1p18f;
-constexpr int kPStride = 144;   // bytes of a row of weights in LDS: 64 fp16 and 16 to spread banks
 
 struct AttArgs {
   KvPages c;
@@ -88,27 +90,38 @@ __device__ __forceinline__ float dpp_max_f(float v) {
                       float, __builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, false)));
 }
 
-// Over the lanes that hold the same rows: the 16 of a quarter, and the quarters
-// RT / 4 apart.
+// Over the lanes of one row: the 16 / RT of a quarter that share it, and the quarters.
 template <int RT>
-__device__ __forceinline__ float rows_max(float v) {
-  v = dpp_max_f<0xB1>(v);
-  v = dpp_max_f<0x4E>(v);
-  v = dpp_max_f<0x141>(v);
-  v = dpp_max_f<0x140>(v);
-  if constexpr (RT <= 4) v = fmaxf(v, __shfl_xor(v, 16, kWave));
-  if constexpr (RT <= 8) v = fmaxf(v, __shfl_xor(v, 32, kWave));
+__device__ __forceinline__ float row_max(float v) {
+  if constexpr (RT <= 8) v = dpp_max_f<0x128>(v);  // row_ror:8
+  if constexpr (RT <= 4) v = dpp_max_f<0x124>(v);  // row_ror:4
+  if constexpr (RT <= 1) {
+    v = dpp_max_f<0x4E>(v);
+    v = dpp_max_f<0xB1>(v);
+  }
+  uint32_t u = __builtin_bit_cast(uint32_t, v);
+  auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  v = fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
+  u = __builtin_bit_cast(uint32_t, v);
+  auto q = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)q[0]),
+               __builtin_bit_cast(float, (uint32_t)q[1]));
+}
+// Over the columns of a row, then (row_sum) the quarters; every step adds the same two
+// values on both sides.
+template <int RT>
+__device__ __forceinline__ float column_sum(float v) {
+  if constexpr (RT <= 8) v = dpp_add<0x128, 0xF>(v);
+  if constexpr (RT <= 4) v = dpp_add<0x124, 0xF>(v);
   return v;
 }
-template <int RT>
-__device__ __forceinline__ float rows_sum(float v) {
-  v = dpp_add<0xB1, 0xF>(v);
-  v = dpp_add<0x4E, 0xF>(v);
-  v = dpp_add<0x141, 0xF>(v);
-  v = dpp_add<0x140, 0xF>(v);
-  if constexpr (RT <= 4) v += __shfl_xor(v, 16, kWave);
-  if constexpr (RT <= 8) v += __shfl_xor(v, 32, kWave);
-  return v;
+__device__ __forceinline__ float quarter_sum(float v) {
+  uint32_t u = __builtin_bit_cast(uint32_t, v);
+  auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  v = __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
+  u = __builtin_bit_cast(uint32_t, v);
+  auto q = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, (uint32_t)q[0]) + __builtin_bit_cast(float, (uint32_t)q[1]);
 }
 
 // Orders a wave's LDS accesses (its LDS instructions execute in order).
@@ -140,21 +153,25 @@ __device__ __forceinline__ void att_store4(void* out, int type, size_t at, f32x4
   __builtin_memcpy((uint16_t*)out + at, b, 8);
 }
 
-// LDS: while the tokens are read, each wave's weights (2 RT rows); then, in the same
-// place, each wave's part of the result [RT][DIM], maxima, sums and low ends.
-constexpr int att_p_bytes(int RT) { return 2 * RT * kPStride; }
+// LDS of a wave: the scales and low ends of 64 tokens; then, in the same place, its part of
+// the result [RT][DIM], maxima, sums and low ends.
 constexpr int att_part_bytes(int RT, int dim) { return RT * dim * 4; }
 constexpr int att_wave_bytes(int RT, int dim, int groups) {
-  const int small = (2 + groups) * RT * 4;
-  const int a = att_p_bytes(RT), b = att_part_bytes(RT, dim) + small;
-  return (a > b ? a : b);
+  const int a = 2 * groups * kAttTokens * 4;
+  const int b = att_part_bytes(RT, dim) + (2 + groups) * RT * 4;
+  return a > b ? a : b;
+}
+
+// Waves of a SIMD that the registers are to leave room for.
+constexpr int att_waves(int dim, int groups) {
+  return dim == 64 || (dim == 128 && groups == 1) ? 3 : dim == 128 || groups <= 2 ? 2 : 1;
 }
 
 template <int DIM, int RT, int NG>
-__global__ void __launch_bounds__(kAttWaves* kWave) attend_kernel(AttArgs a) {
+__global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_kernel(AttArgs a) {
   constexpr int KS = DIM / 32;       // steps of 32 channels
   constexpr int GS = KS / NG;        // of a group
-  constexpr int NT = RT / 4;         // tokens of a lane
+  constexpr int NT = RT / 4;         // products (of four tokens a lane) that a lane keeps
   __shared__ __attribute__((aligned(16))) uint8_t smem[kAttWaves][att_wave_bytes(RT, DIM, NG)];
   const int lane = threadIdx.x & (kWave - 1), t16 = lane & 15, quarter = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -167,23 +184,82 @@ __global__ void __launch_bounds__(kAttWaves* kWave) attend_kernel(AttArgs a) {
   const int b0 = sp.first + part * sp.each;
   const int b1 = b0 + sp.each < sp.last ? b0 + sp.each : sp.last;
 
-  // q: operand row t16 (repeated every RT rows), channels 32 s + 8 quarter .. + 7 of step s
+  uint8_t* const lds = smem[wv];
+  const int64_t page_size = kv_page_size(a.c);
+  constexpr int kBlock = kv_block_bytes(DIM, NG);
+  const int blocks_mask = (1 << (a.c.page_shift - 4)) - 1;
+  const int32_t* table = a.c.table + (int64_t)seq * a.c.max_pages;
+  const uint8_t* pool = a.c.pool + (int64_t)head * (blocks_mask + 1) * kBlock;
+
+  // the page of block `blk` of 64 tokens, and where the block lies (a page outside the
+  // pool: the first page, read and not used)
+  auto page_of = [&](int b, int blk) {
+    const int at = (b * kAttTokens + 16 * blk) >> a.c.page_shift;
+    return at < a.c.max_pages ? table[at] : -1;
+  };
+  auto outside = [&](int page) { return page < 0 || page >= a.c.pages; };
+  auto block_at = [&](int b, int blk, int page) {
+    return pool + (outside(page) ? 0 : page) * page_size +
+           ((4 * b + blk) & blocks_mask) * (int64_t)kBlock;
+  };
+  // a lane reads the keys of block t16 / 4, tokens 4 j + t16 % 4, and the values and
+  // the scales of block `quarter`
+  const int kblk = t16 >> 2;
+  struct Tokens {
+    uint32_t k[4][KS];
+    u32x4 v[KS];
+    uint32_t ks[NG], vs[NG];
+  };
+  Tokens x;
+  auto load_k = [&](const uint8_t* key, const uint8_t* own) {
+    const uint8_t* p = key + (t16 & 3) * (DIM / 2) + quarter * (DIM / 8);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) __builtin_memcpy(x.k[j], p + j * 2 * DIM, KS * 4);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) x.ks[g] = *(const uint32_t*)(own + 16 * DIM + 64 * g + 4 * t16);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+      x.vs[g] = *(const uint32_t*)(own + 16 * DIM + 64 * (NG + g) + 4 * t16);
+  };
+  auto load_v = [&](const uint8_t* own) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) __builtin_memcpy(&x.v[s], own + 8 * DIM + (16 * s + t16) * 16, 16);
+  };
+
+  int b = b0 + wv;
+  const uint8_t* own;
+  int page = -1, page_n = -1, key_page_n = -1;
+  if (b < b1) {
+    const int key_page = page_of(b, kblk);
+    page = page_of(b, quarter);
+    if (b + kAttWaves < b1) {
+      key_page_n = page_of(b + kAttWaves, kblk);
+      page_n = page_of(b + kAttWaves, quarter);
+    }
+    own = block_at(b, quarter, page);
+    load_k(block_at(b, kblk, key_page), own);
+    load_v(own);
+  }
+
+  // q: operand column t16 (row t16 % RT), channels 32 s + 8 quarter .. + 7 of step s
   half8_t qa[KS];
-  float qs[NG][4], unit[4];  // of this lane's four rows: sums of q over a group, logit's unit
-  int see_first[4], see_last[4];
+  float qs[NG], unit = a.scale * kCodeUnit;  // sums of the row's q over a group, a logit's unit
+  const int r = row0 + (t16 & (RT - 1));
+  int see_first = 0, see_last = sp.len - 1;  // rows past the last: not stored
   {
-    const int r = row0 + (t16 & (RT - 1));
     const bool real = r < rows;
     const int query = real ? r / per : 0, h = head * per + (real ? r - query * per : 0);
+    if (real) {
+      see_last = sp.len - a.queries + query;
+      see_first = a.window > 0 ? see_last - a.window + 1 : 0;
+    }
     const uint16_t* row = (const uint16_t*)a.q +
                           ((int64_t)seq * a.queries + query) * a.q_stride + (int64_t)h * DIM;
     uint4 raw[KS];
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
-      __builtin_memcpy(&raw[s], row + 32 * s + 8 * quarter, 16);
-    float sum[NG], mine = a.scale * kCodeUnit;
+    for (int s = 0; s < KS; ++s) __builtin_memcpy(&raw[s], row + 32 * s + 8 * quarter, 16);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) sum[g] = 0.f;
+    for (int g = 0; g < NG; ++g) qs[g] = 0.f;
     if (a.q_type == LVQ_F16) {
 #pragma unroll
       for (int s = 0; s < KS; ++s) qa[s] = __builtin_bit_cast(half8_t, raw[s]);
@@ -197,9 +273,9 @@ __global__ void __launch_bounds__(kAttWaves* kWave) attend_kernel(AttArgs a) {
         const uint32_t w[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t b = (i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
-          v[s][i] = __builtin_bit_cast(float, b);
-          const uint32_t m = b & 0x7F800000u;
+          const uint32_t bits = (i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+          v[s][i] = __builtin_bit_cast(float, bits);
+          const uint32_t m = bits & 0x7F800000u;
           top = top > m ? top : m;
         }
       }
@@ -211,7 +287,7 @@ __global__ void __launch_bounds__(kAttWaves* kWave) attend_kernel(AttArgs a) {
       top = top == 0x7F800000u || top == 0 ? 0x3F800000u : top;
       top = top < 0x01000000u ? 0x01000000u : top > 0x7E000000u ? 0x7E000000u : top;
       const float down = __builtin_bit_cast(float, 0x7F000000u - top);
-      mine *= __builtin_bit_cast(float, top);
+      unit *= __builtin_bit_cast(float, top);
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -220,101 +296,59 @@ __global__ void __launch_bounds__(kAttWaves* kWave) attend_kernel(AttArgs a) {
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[s / GS] += (float)qa[s][i];
+      for (int i = 0; i < 8; ++i) qs[s / GS] += (float)qa[s][i];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      sum[g] += __shfl_xor(sum[g], 16, kWave);
-      sum[g] += __shfl_xor(sum[g], 32, kWave);
-    }
-    // from lanes by operand row to lanes by result row
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int from = 4 * (quarter & (NT - 1)) + i;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) qs[g][i] = __shfl(sum[g], from, kWave) * (1.f / kCodeUnit);
-      unit[i] = __shfl(mine, from, kWave);
-      const int rr = row0 + from, qq = rr / per;
-      see_last[i] = sp.len - a.queries + qq;
-      see_first[i] = a.window > 0 ? see_last[i] - a.window + 1 : 0;
-      if (rr >= rows) see_last[i] = sp.len - 1, see_first[i] = 0;  // not stored
-    }
+    for (int g = 0; g < NG; ++g) qs[g] = quarter_sum(qs[g]) * (1.f / kCodeUnit);
   }
-  // tokens that every row sees
-  int all_first, all_last;
-  // and the first that any row sees
-  const int any_first = a.window > 0 ? sp.len - a.queries - a.window + 1 : 0;
+  // tokens that every row sees, and the first that any does
+  int all_first = 0, any_first = 0, all_last;
   {
     const int q0 = row0 / per, q1 = (row0 + RT < rows ? row0 + RT - 1 : rows - 1) / per;
     all_last = sp.len - a.queries + q0;
-    all_first = a.window > 0 ? sp.len - a.queries + q1 - a.window + 1 : 0;
-  }
-
-  uint8_t* const lds = smem[wv];
-  const int64_t page_size = kv_page_size(a.c);
-  constexpr int kBlock = kv_block_bytes(DIM, NG);
-  const int blocks_mask = (1 << (a.c.page_shift - 4)) - 1;
-  const int32_t* table = a.c.table + (int64_t)seq * a.c.max_pages;
-  const uint8_t* pool = a.c.pool + (int64_t)head * (blocks_mask + 1) * kBlock;
-
-  // the page of this lane's block (quarter) of 64 tokens
-  auto page_of = [&](int b) {
-    const int at = (b * kAttTokens + 16 * quarter) >> a.c.page_shift;
-    return at < a.c.max_pages ? table[at] : -1;
-  };
-  struct Tokens {
-    uint32_t k[4][KS];
-    u32x4 v[KS];
-    uint32_t ks[NG], vs[NG];
-  };
-  Tokens x;
-  auto block_at = [&](int b, int page) {
-    const bool bad = page < 0 || page >= a.c.pages;
-    return pool + (bad ? 0 : page) * page_size +
-           ((4 * b + quarter) & blocks_mask) * (int64_t)kBlock;
-  };
-  auto load_k = [&](const uint8_t* at) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)(uintptr_t)at, 16 * j);
-      const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)((uintptr_t)at >> 32), 16 * j);
-      const uint8_t* p = (const uint8_t*)((uint64_t)hi << 32 | lo) + (t16 * 4 + quarter) * KS * 4;
-      __builtin_memcpy(x.k[j], p, KS * 4);
+    if (a.window > 0) {
+      all_first = sp.len - a.queries + q1 - a.window + 1;
+      any_first = sp.len - a.queries - a.window + 1;
     }
+  }
+  // the products that a lane keeps: its n-th is number product(n)
+  const int col = RT == 4 ? t16 >> 2 : RT == 8 ? t16 >> 3 : 0;
+  auto product = [&](int n) { return RT == 4 ? col : RT == 8 ? 2 * n + col : n; };
+  uint32_t keep[4];  // operand masks: all ones where the lane keeps product j
 #pragma unroll
-    for (int g = 0; g < NG; ++g) x.ks[g] = *(const uint32_t*)(at + 16 * DIM + 64 * g + 4 * t16);
-  };
-  auto load_v = [&](const uint8_t* at) {
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-      x.vs[g] = *(const uint32_t*)(at + 16 * DIM + 64 * (NG + g) + 4 * t16);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) __builtin_memcpy(&x.v[s], at + 8 * DIM + (16 * s + t16) * 16, 16);
-  };
+  for (int j = 0; j < 4; ++j)
+    keep[j] = RT == 4 ? (col == j ? ~0u : 0u) : RT == 8 ? (col == (j & 1) ? ~0u : 0u) : ~0u;
 
-  float m[4], l[4], low[NG][4];
+  float m = -__builtin_inff(), l = 0.f, low[NG];
   f32x4_t acc[KS][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m[i] = -__builtin_inff(), l[i] = 0.f;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) low[g][i] = 0.f;
-  }
+  for (int g = 0; g < NG; ++g) low[g] = 0.f;
 #pragma unroll
   for (int s = 0; s < KS; ++s) acc[s][0] = acc[s][1] = f32x4_t{0, 0, 0, 0};
-  // the weights' unit: 2^6 over a power of two at or above the largest scale so far
+  // the weights' unit: 2^6 over a power of two above the largest scale so far
   float smax = 0.f, pu = 1.f;
 
-  int b = b0 + wv;
-  int page = b < b1 ? page_of(b) : -1;
-  int page_next = b + kAttWaves < b1 ? page_of(b + kAttWaves) : -1;
-  const uint8_t* at = block_at(b, page);
-  if (b < b1) {
-    load_k(at);
-    load_v(at);
-  }
   for (; b < b1; b += kAttWaves) {
+    const int t0 = b * kAttTokens;
+    const bool bad = outside(page);
+    const bool edge = t0 < all_first || t0 + kAttTokens - 1 > all_last || __any(bad);
+    // ---- scales into LDS; the largest of the values' (of tokens that some row sees)
+    float top = 0.f;
+    {
+      const int tok = t0 + lane;
+      const bool none = edge && (bad || tok >= sp.len || tok < any_first);
+      lds_order();
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        *(uint32_t*)(lds + (g * kAttTokens + lane) * 4) = x.ks[g];
+        *(uint32_t*)(lds + ((NG + g) * kAttTokens + lane) * 4) = x.vs[g];
+        const float s = fabsf(att_f16(x.vs[g]));
+        top = s < __builtin_inff() ? fmaxf(top, s) : top;
+      }
+      top = none ? 0.f : top;
+      lds_order();
+    }
     // ---- logits
-    float x0[NT][4];
+    float lg[NT][4];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       f32x4_t d[4];
@@ -325,225 +359,171 @@ __global__ void __launch_bounds__(kAttWaves* kWave) attend_kernel(AttArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t w = x.k[j][s];
-          d[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-              qa[s], codes8(w << 6, w << 2, w >> 2, w >> 6), d[j], 0, 0, 0);
+          d[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8(w << 6, w << 2, w >> 2, w >> 6),
+                                                        qa[s], d[j], 0, 0, 0);
         }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         f32x4_t e;
-        uint32_t sl;
-        if constexpr (RT == 4) {
-          e = quarter & 2 ? (quarter & 1 ? d[3] : d[2]) : (quarter & 1 ? d[1] : d[0]);
-          sl = x.ks[g];
-        } else if constexpr (RT == 8) {
-          e = quarter & 2 ? d[2 * n + 1] : d[2 * n];
-          sl = __shfl(x.ks[g], 16 * (2 * n + (quarter >> 1)) + t16, kWave);
-        } else {
-          e = d[n];
-          sl = __shfl(x.ks[g], 16 * n + t16, kWave);
-        }
-        const float s = att_f16(sl), lo = att_f16(sl >> 16);
+        if constexpr (RT == 4) e = col & 2 ? (col & 1 ? d[3] : d[2]) : (col & 1 ? d[1] : d[0]);
+        else if constexpr (RT == 8) e = col ? d[2 * n + 1] : d[2 * n];
+        else e = d[n];
+        const u32x4 sl =
+            *(const u32x4*)(lds + (g * kAttTokens + 16 * quarter + 4 * product(n)) * 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float r = __builtin_fmaf(s, e[i], lo * qs[g][i]);
-          x0[n][i] = g ? x0[n][i] + r : r;
+          const float c = __builtin_fmaf(att_f16(sl[i]), e[i], g ? lg[n][i] : 0.f);
+          lg[n][i] = __builtin_fmaf(att_f16(sl[i] >> 16), qs[g], c);
         }
       }
+      if constexpr (NG > 1) __builtin_amdgcn_sched_barrier(0);
     }
-    uint32_t vs[NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) vs[g] = x.vs[g];
-    // ---- what a row does not see
-    const int t0 = b * kAttTokens;
-    const bool bad = page < 0 || page >= a.c.pages;
-    if (t0 < all_first || t0 + kAttTokens - 1 > all_last || __any(bad)) {
-      // a value that is not finite: NaN in the rows that see it, and nothing in the others
-      bool wild = false;
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-        wild |= (vs[g] & 0x7C00u) == 0x7C00u || (vs[g] & 0x7C000000u) == 0x7C000000u;
-      const int mine = t0 + 16 * quarter + t16;
-      const bool none = bad || mine >= sp.len || mine < any_first;
-      const int flags = (none ? 1 : 0) | (wild ? 2 : 0);
-      if (none || wild)
-#pragma unroll
-        for (int g = 0; g < NG; ++g) vs[g] = 0;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int blk = RT == 4 ? quarter : RT == 8 ? 2 * n + (quarter >> 1) : n;
-        const int tok = t0 + 16 * blk + t16;
-        const int f = RT == 4 ? flags : __shfl(flags, 16 * blk + t16, kWave);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (f & 2) x0[n][i] = __builtin_nanf("");
-          if ((f & 1) || tok < see_first[i] || tok > see_last[i]) x0[n][i] = -__builtin_inff();
-        }
-      }
-    }
-    // ---- the next tokens' keys
-    const int bn = b + kAttWaves;
-    const int page_n = page_next;
-    const uint8_t* at_n = block_at(bn, page_n);
+    // ---- the next tokens' keys and scales
+    const int bn = b + kAttWaves, page_b = page_n;
+    const uint8_t* own_n = block_at(bn, quarter, page_n);
     if (bn < b1) {
-      page_next = bn + kAttWaves < b1 ? page_of(bn + kAttWaves) : -1;
-      load_k(at_n);
+      const uint8_t* key_n = block_at(bn, kblk, key_page_n);
+      if (bn + kAttWaves < b1) {
+        key_page_n = page_of(bn + kAttWaves, kblk);
+        page_n = page_of(bn + kAttWaves, quarter);
+      }
+      load_k(key_n, own_n);
     }
-    // ---- maxima: left behind by up to 2^8, so that they seldom change
-    float top = 0.f;
-    bool grown = false;
+    // ---- what the row does not see
+    bool unseen[NT][4];
+    if (edge) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) top = fmaxf(top, fabsf(att_f16(vs[g])));
-    grown = top > smax;
-    float xm[4];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      xm[i] = x0[0][i];
-#pragma unroll
-      for (int n = 1; n < NT; ++n) xm[i] = fmaxf(xm[i], x0[n][i]);
-      grown |= xm[i] * unit[i] > m[i] + 8.f;
+        for (int i = 0; i < 4; ++i) {
+          const int tok = t0 + 16 * quarter + 4 * product(n) + i;
+          unseen[n][i] = bad || tok < see_first || tok > see_last;
+          if (unseen[n][i]) lg[n][i] = -__builtin_inff();
+        }
     }
-    if (__any(grown)) {
-      float old_pu = pu;
-      top = fmaxf(top, smax);
-      top = rows_max<4>(top);
-      smax = top;
-      if (top > 0.f && top < __builtin_inff()) {
-        // 2^6 over the power of two above it
-        const uint32_t e = __builtin_bit_cast(uint32_t, top) & 0x7F800000u;
-        pu = __builtin_bit_cast(float, 0x7F800000u + 0x02000000u - e);
-      }
-      float f[4];
+    // ---- maximum: left behind by up to 2^8, so that it seldom changes
+    float big = lg[0][0];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float nm = fmaxf(m[i], rows_max<RT>(xm[i]) * unit[i]);
-        f[i] = m[i] == nm ? 1.f : __builtin_amdgcn_exp2f(m[i] - nm);  // 0 from minus infinity
-        m[i] = nm;
-        l[i] *= f[i];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int g = 0; g < NG; ++g) low[g][i] *= f[i];
-        f[i] *= pu / old_pu;
+      for (int i = 0; i < 4; ++i) big = fmaxf(big, lg[n][i]);
+    if (__any(top > smax || big * unit > m + 8.f)) {
+      const float old_pu = pu;
+      smax = row_max<1>(fmaxf(top, smax));
+      if (smax > 0.f) {
+        const uint32_t e = __builtin_bit_cast(uint32_t, smax) & 0x7F800000u;
+        pu = __builtin_bit_cast(float, 0x81800000u - e);
       }
-      // from lanes by four rows to lanes by one: row t16 is f[t16 % 4] of quarter t16 / 4
-      float mine = 0.f;
+      const float nm = fmaxf(m, row_max<RT>(big) * unit);
+      float f = m == nm ? 1.f : __builtin_amdgcn_exp2f(m - nm);  // 0 from minus infinity
+      m = nm;
+      l *= f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float o = __shfl(f[i], 16 * ((t16 & (RT - 1)) >> 2), kWave);
-        mine = (t16 & 3) == i ? o : mine;
-      }
+      for (int g = 0; g < NG; ++g) low[g] *= f;
+      f *= pu / old_pu;
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) acc[s][h] *= mine;
+        for (int h = 0; h < 2; ++h) acc[s][h] *= f;
     }
     // ---- weights
     float p[NT][4];
+    const float mi = m == -__builtin_inff() ? 0.f : m;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float mi = m[i] == -__builtin_inff() ? 0.f : m[i];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        p[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x0[n][i], unit[i], -mi));
-        l[i] += p[n][i];
+      for (int i = 0; i < 4; ++i) {
+        p[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(lg[n][i], unit, -mi));
+        l += p[n][i];
       }
-    }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      lds_order();
+      // p s, the rounded value and the rest, in the order of the values' pairs: tokens 0 and
+      // 2, 1 and 3 of four
+      uint32_t hi[NT][2], rest[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int blk = RT == 4 ? quarter : RT == 8 ? 2 * n + (quarter >> 1) : n;
-        const uint32_t sl = RT == 4 ? vs[g] : __shfl(vs[g], 16 * blk + t16, kWave);
-        const float s = att_f16(sl) * pu, lo = att_f16(sl >> 16);
-        // the values' pairs hold tokens 0 and 2, 1 and 3 of four
-        const int tok = 16 * blk + ((t16 & 12) | (t16 & 1) << 1 | (t16 & 2) >> 1);
+        u32x4 sl =
+            *(const u32x4*)(lds + ((NG + g) * kAttTokens + 16 * quarter + 4 * product(n)) * 4);
+        _Float16 h[4], t[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          low[g][i] = __builtin_fmaf(p[n][i], lo, low[g][i]);
-          const float w = p[n][i] * s;
-          const _Float16 hi = (_Float16)w, rest = (_Float16)(w - (float)hi);
-          const int row = 4 * (quarter & (NT - 1)) + i;
-          *(_Float16*)(lds + row * kPStride + 2 * tok) = hi;
-          *(_Float16*)(lds + (RT + row) * kPStride + 2 * tok) = rest;
+          if (edge && unseen[n][i]) sl[i] = 0;  // whatever it holds
+          low[g] = __builtin_fmaf(p[n][i], att_f16(sl[i] >> 16), low[g]);
+          const float w = p[n][i] * pu, s = att_f16(sl[i]);
+          h[i] = (_Float16)(w * s);
+          t[i] = (_Float16)__builtin_fmaf(w, s, -(float)h[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          hi[n][k] = (uint32_t)__builtin_bit_cast(uint16_t, h[k]) |
+                     (uint32_t)__builtin_bit_cast(uint16_t, h[k + 2]) << 16;
+          rest[n][k] = (uint32_t)__builtin_bit_cast(uint16_t, t[k]) |
+                       (uint32_t)__builtin_bit_cast(uint16_t, t[k + 2]) << 16;
         }
       }
-      lds_order();
-      // operand column t16: row t16 of the rounded weights, then of the rests
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int col = RT == 4 ? t16 & 7 : t16;
-        const half8_t w0 = *(const half8_t*)(lds + col * kPStride + 32 * quarter + 16 * k);
-        half8_t w1;
-        if constexpr (RT == 16)
-          w1 = *(const half8_t*)(lds + (RT + col) * kPStride + 32 * quarter + 16 * k);
+        // products 2 k and 2 k + 1
+        const int n0 = RT == 4 ? 0 : RT == 8 ? k : 2 * k, n1 = RT == 16 ? n0 + 1 : n0;
+        const uint32_t k0 = keep[2 * k], k1 = keep[2 * k + 1];
+        const half8_t w0 = __builtin_bit_cast(
+            half8_t, u32x4{hi[n0][0] & k0, hi[n0][1] & k0, hi[n1][0] & k1, hi[n1][1] & k1});
+        const half8_t w1 = __builtin_bit_cast(
+            half8_t, u32x4{rest[n0][0] & k0, rest[n0][1] & k0, rest[n1][0] & k1, rest[n1][1] & k1});
 #pragma unroll
         for (int s = g * GS; s < (g + 1) * GS; ++s) {
           const uint32_t c0 = x.v[s][2 * k], c1 = x.v[s][2 * k + 1];
-          const half8_t lo = codes8(c0 << 6, c0 >> 2, c1 << 6, c1 >> 2);
-          const half8_t hi = codes8(c0 << 2, c0 >> 6, c1 << 2, c1 >> 6);
-          acc[s][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, w0, acc[s][0], 0, 0, 0);
-          acc[s][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, w0, acc[s][1], 0, 0, 0);
-          if constexpr (RT == 16) {
-            acc[s][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, w1, acc[s][0], 0, 0, 0);
-            acc[s][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, w1, acc[s][1], 0, 0, 0);
-          }
+          const half8_t vl = codes8(c0 << 6, c0 >> 2, c1 << 6, c1 >> 2);
+          const half8_t vh = codes8(c0 << 2, c0 >> 6, c1 << 2, c1 >> 6);
+          acc[s][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vl, w0, acc[s][0], 0, 0, 0);
+          acc[s][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vh, w0, acc[s][1], 0, 0, 0);
+          acc[s][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vl, w1, acc[s][0], 0, 0, 0);
+          acc[s][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vh, w1, acc[s][1], 0, 0, 0);
         }
       }
+      if constexpr (NG > 1) __builtin_amdgcn_sched_barrier(0);
     }
-    if (bn < b1) load_v(at_n);
-    page = page_n;
+    if (bn < b1) load_v(own_n);
+    page = page_b;
   }
 
-  // ---- this wave's part: maxima, sums and low ends by row, then the result
+  // ---- this wave's part: maxima, sums and the result by row
   lds_order();
   float* const part_o = (float*)lds;
   float* const part_m = (float*)(lds + att_part_bytes(RT, DIM));
   float* const part_l = part_m + RT;
-  float* const part_low = part_l + RT;
+  const float sum = quarter_sum(column_sum<RT>(l)), back = kCodeUnit / pu;
+  if (lane < RT) part_m[lane] = m, part_l[lane] = sum;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 4 * (quarter & (NT - 1)) + i;
-    const float sum = rows_sum<RT>(l[i]);
-    if (t16 == 0 && quarter < NT) part_m[row] = m[i], part_l[row] = sum;
+  for (int g = 0; g < NG; ++g) {
+    const float lo = quarter_sum(column_sum<RT>(low[g]));
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const float v = rows_sum<RT>(low[g][i]);
-      if (t16 == 0 && quarter < NT) part_low[g * RT + row] = v;
-    }
+    for (int s = g * GS; s < (g + 1) * GS; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f32x4_t v = acc[s][h];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(column_sum<RT>(v[i]), back, lo);
+        if (t16 < RT) *(f32x4_t*)(part_o + t16 * DIM + 32 * s + 16 * h + 4 * quarter) = v;
+      }
   }
-  lds_order();
-  const float back = kCodeUnit / pu;
-#pragma unroll
-  for (int s = 0; s < KS; ++s)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      f32x4_t v = acc[s][h];
-      if constexpr (RT < 16) {  // the rests' columns are RT further
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += __shfl(v[i], (lane + RT) & 63, kWave);
-      }
-      if (t16 < RT) {
-        const float lo = part_low[(s / GS) * RT + t16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(v[i], back, lo);
-        *(f32x4_t*)(part_o + t16 * DIM + 32 * s + 16 * h + 4 * quarter) = v;
-      }
-    }
   __syncthreads();
 
   // ---- the workgroup's: four channels of a row per thread
   for (int at4 = threadIdx.x; at4 < RT * (DIM / 4); at4 += kAttWaves * kWave) {
     const int r = at4 / (DIM / 4), c = (at4 - r * (DIM / 4)) * 4;
     if (row0 + r >= rows) break;
-    float big = -__builtin_inff();
+    float most = -__builtin_inff();
 #pragma unroll
     for (int w = 0; w < kAttWaves; ++w)
-      big = fmaxf(big, ((float*)(smem[w] + att_part_bytes(RT, DIM)))[r]);
+      most = fmaxf(most, ((float*)(smem[w] + att_part_bytes(RT, DIM)))[r]);
     float sum = 0.f;
     f32x4_t v = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kAttWaves; ++w) {
       const float* ml = (float*)(smem[w] + att_part_bytes(RT, DIM));
-      const float f = ml[r] == big ? 1.f : __builtin_amdgcn_exp2f(ml[r] - big);
+      const float f = ml[r] == most ? 1.f : __builtin_amdgcn_exp2f(ml[r] - most);
       sum = __builtin_fmaf(ml[RT + r], f, sum);
       v += *(const f32x4_t*)((float*)smem[w] + r * DIM + c) * f;
     }
@@ -558,7 +538,7 @@ __global__ void __launch_bounds__(kAttWaves* kWave) attend_kernel(AttArgs a) {
       __builtin_memcpy(a.parts + at * DIM + c, &v, 16);
       if (c == 0) {
         float* ml = a.parts + (size_t)a.c.seqs * a.c.kv_heads * n * DIM + 2 * at;
-        ml[0] = big, ml[1] = sum;
+        ml[0] = most, ml[1] = sum;
       }
     }
   }
