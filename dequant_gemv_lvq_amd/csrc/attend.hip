@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
   // pool: the first page, read and not used)
   auto page_of = [&](int b, int blk) {
     const int at = (b * kAttTokens + 16 * blk) >> a.c.page_shift;
-    return at < a.c.max_pages ? table[at] : -1;
+    return table[at < a.c.max_pages ? at : a.c.max_pages - 1];
   };
   auto outside = [&](int page) { return page < 0 || page >= a.c.pages; };
   auto block_at = [&](int b, int blk, int page) {
@@ -229,13 +229,14 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
   int b = b0 + wv;
   const uint8_t* own;
   int page = -1, page_n = -1, key_page_n = -1;
+  // the loads of the loop are one sequence without branches, so that each wait counts
+  // just the loads behind the one it is for: at the end the last block again
+  int bn = b + kAttWaves < b1 ? b + kAttWaves : b;
   if (b < b1) {
     const int key_page = page_of(b, kblk);
     page = page_of(b, quarter);
-    if (b + kAttWaves < b1) {
-      key_page_n = page_of(b + kAttWaves, kblk);
-      page_n = page_of(b + kAttWaves, quarter);
-    }
+    key_page_n = page_of(bn, kblk);
+    page_n = page_of(bn, quarter);
     own = block_at(b, quarter, page);
     load_k(block_at(b, kblk, key_page), own);
     load_v(own);
@@ -379,16 +380,13 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
       if constexpr (NG > 1) __builtin_amdgcn_sched_barrier(0);
     }
     // ---- the next tokens' keys and scales
-    const int bn = b + kAttWaves, page_b = page_n;
+    const int page_b = page_n;
     const uint8_t* own_n = block_at(bn, quarter, page_n);
-    if (bn < b1) {
-      const uint8_t* key_n = block_at(bn, kblk, key_page_n);
-      if (bn + kAttWaves < b1) {
-        key_page_n = page_of(bn + kAttWaves, kblk);
-        page_n = page_of(bn + kAttWaves, quarter);
-      }
-      load_k(key_n, own_n);
-    }
+    const uint8_t* key_n = block_at(bn, kblk, key_page_n);
+    bn = bn + kAttWaves < b1 ? bn + kAttWaves : bn;
+    key_page_n = page_of(bn, kblk);
+    page_n = page_of(bn, quarter);
+    load_k(key_n, own_n);
     // ---- what the row does not see
     bool unseen[NT][4];
     if (edge) {
@@ -484,7 +482,7 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
       }
       if constexpr (NG > 1) __builtin_amdgcn_sched_barrier(0);
     }
-    if (bn < b1) load_v(own_n);
+    load_v(own_n);
     page = page_b;
   }
 
