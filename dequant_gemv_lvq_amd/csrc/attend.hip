@@ -335,17 +335,32 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
     // ---- scales into LDS; the largest of the values' (of tokens that some row sees)
     float top = 0.f;
     {
-      const int tok = t0 + lane;
-      const bool none = edge && (bad || tok >= sp.len || tok < any_first);
+      uint32_t ks[NG], vs[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) ks[g] = x.ks[g], vs[g] = x.vs[g];
+      if (edge) {
+        // what no row sees is 0, whatever it holds; a value that is not finite becomes a
+        // NaN of the logit, for the rows that see it, and nothing for the others
+        const int tok = t0 + lane;
+        const bool none = bad || tok >= sp.len || tok < any_first;
+        bool wild = false;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          wild |= (vs[g] & 0x7C00u) == 0x7C00u || (vs[g] & 0x7C000000u) == 0x7C000000u;
+        if (none || wild) {
+          ks[0] = wild ? 0x7E00u : ks[0];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) vs[g] = 0;
+        }
+      }
       lds_order();
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        *(uint32_t*)(lds + (g * kAttTokens + lane) * 4) = x.ks[g];
-        *(uint32_t*)(lds + ((NG + g) * kAttTokens + lane) * 4) = x.vs[g];
-        const float s = fabsf(att_f16(x.vs[g]));
+        *(uint32_t*)(lds + (g * kAttTokens + lane) * 4) = ks[g];
+        *(uint32_t*)(lds + ((NG + g) * kAttTokens + lane) * 4) = vs[g];
+        const float s = fabsf(att_f16(vs[g]));
         top = s < __builtin_inff() ? fmaxf(top, s) : top;
       }
-      top = none ? 0.f : top;
       lds_order();
     }
     // ---- logits
@@ -388,15 +403,13 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
     page_n = page_of(bn, quarter);
     load_k(key_n, own_n);
     // ---- what the row does not see
-    bool unseen[NT][4];
     if (edge) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int tok = t0 + 16 * quarter + 4 * product(n) + i;
-          unseen[n][i] = bad || tok < see_first || tok > see_last;
-          if (unseen[n][i]) lg[n][i] = -__builtin_inff();
+          if (bad || tok < see_first || tok > see_last) lg[n][i] = -__builtin_inff();
         }
     }
     // ---- maximum: left behind by up to 2^8, so that it seldom changes
@@ -415,10 +428,10 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
       const float nm = fmaxf(m, row_max<RT>(big) * unit);
       float f = m == nm ? 1.f : __builtin_amdgcn_exp2f(m - nm);  // 0 from minus infinity
       m = nm;
+      f *= pu / old_pu;
       l *= f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) low[g] *= f;
-      f *= pu / old_pu;
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -431,7 +444,8 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(lg[n][i], unit, -mi));
+        // in the weights' unit, a power of two
+        p[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(lg[n][i], unit, -mi)) * pu;
         l += p[n][i];
       }
 #pragma unroll
@@ -441,23 +455,20 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
       uint32_t hi[NT][2], rest[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        u32x4 sl =
+        const u32x4 sl =
             *(const u32x4*)(lds + ((NG + g) * kAttTokens + 16 * quarter + 4 * product(n)) * 4);
-        _Float16 h[4], t[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (edge && unseen[n][i]) sl[i] = 0;  // whatever it holds
-          low[g] = __builtin_fmaf(p[n][i], att_f16(sl[i] >> 16), low[g]);
-          const float w = p[n][i] * pu, s = att_f16(sl[i]);
-          h[i] = (_Float16)(w * s);
-          t[i] = (_Float16)__builtin_fmaf(w, s, -(float)h[i]);
-        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          hi[n][k] = (uint32_t)__builtin_bit_cast(uint16_t, h[k]) |
-                     (uint32_t)__builtin_bit_cast(uint16_t, h[k + 2]) << 16;
-          rest[n][k] = (uint32_t)__builtin_bit_cast(uint16_t, t[k]) |
-                       (uint32_t)__builtin_bit_cast(uint16_t, t[k + 2]) << 16;
+          lvq_half2 h, t;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float w = p[n][2 * i + k], s = att_f16(sl[2 * i + k]);
+            h[i] = (_Float16)(w * s);
+            t[i] = (_Float16)__builtin_fmaf(w, s, -(float)h[i]);
+            low[g] = __builtin_fmaf(w, att_f16(sl[2 * i + k] >> 16), low[g]);
+          }
+          hi[n][k] = __builtin_bit_cast(uint32_t, h);
+          rest[n][k] = __builtin_bit_cast(uint32_t, t);
         }
       }
 #pragma unroll
@@ -491,18 +502,18 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
   float* const part_o = (float*)lds;
   float* const part_m = (float*)(lds + att_part_bytes(RT, DIM));
   float* const part_l = part_m + RT;
-  const float sum = quarter_sum(column_sum<RT>(l)), back = kCodeUnit / pu;
+  const float back = 1.f / pu, sum = quarter_sum(column_sum<RT>(l)) * back;
   if (lane < RT) part_m[lane] = m, part_l[lane] = sum;
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    const float lo = quarter_sum(column_sum<RT>(low[g]));
+    const float lo = quarter_sum(column_sum<RT>(low[g])) * back;
 #pragma unroll
     for (int s = g * GS; s < (g + 1) * GS; ++s)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         f32x4_t v = acc[s][h];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(column_sum<RT>(v[i]), back, lo);
+        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(column_sum<RT>(v[i]), back * kCodeUnit, lo);
         if (t16 < RT) *(f32x4_t*)(part_o + t16 * DIM + 32 * s + 16 * h + 4 * quarter) = v;
       }
   }
@@ -589,7 +600,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(AttArgs a) {
 // ---------------------------------------------------------------- launch
 
 // Workgroups that a sequence's tokens are split over, at most: enough to fill the chip
-// about twice, and no more than there are tokens for.
+// once, two workgroups per CU, and no more than there are tokens for.
 inline int att_splits(const KvPages& c, int queries, int window, int tiles) {
   long long tokens = (long long)c.max_pages << c.page_shift;
   if (window > 0 && window + queries + kAttTokens < tokens)
@@ -597,7 +608,7 @@ inline int att_splits(const KvPages& c, int queries, int window, int tiles) {
   const long long most =
       (tokens + kAttTokens * kAttWaves - 1) / (kAttTokens * kAttWaves);
   const long long wgs = (long long)c.seqs * c.kv_heads * tiles;
-  long long want = (6LL * device_cus() + wgs - 1) / (wgs > 0 ? wgs : 1);
+  long long want = (2LL * device_cus() + wgs - 1) / (wgs > 0 ? wgs : 1);
   want = want < most ? want : most;
   return want < 1 ? 1 : (int)want;
 }
