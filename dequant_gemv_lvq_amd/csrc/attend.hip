@@ -52,11 +52,12 @@ struct AttArgs {
 };
 static_assert(sizeof(AttArgs) < 128, "launches of 128 bytes and more are slower");
 
-// What a sequence's workgroups share: the tokens any of its queries sees, in units of 64.
+// The tokens any query of a sequence sees, in blocks of 64, and over how many workgroups
+// they are split: block n (from the first) goes to wave n % waves of workgroup n / waves,
+// all modulo the whole.  So a workgroup's first blocks do not depend on the length, and
+// their pages' numbers are asked for before it is known.
 struct Span {
-  int first, last;   // blocks of 64 tokens [first, last)
-  int parts, each;   // workgroups, and blocks of each
-  int len;
+  int first, last, parts, len;
 };
 __device__ __forceinline__ Span att_span(const KvPages& c, int len, int queries, int window,
                                          int splits) {
@@ -70,12 +71,8 @@ __device__ __forceinline__ Span att_span(const KvPages& c, int len, int queries,
   }
   s.first = first;
   s.last = (s.len + kAttTokens - 1) / kAttTokens;
-  const int n = s.last - s.first;
-  int parts = (n + kAttWaves - 1) / kAttWaves;
-  parts = parts < splits ? parts : splits;
-  parts = parts < 1 ? 1 : parts;
-  s.each = (n + parts - 1) / parts;
-  s.parts = s.each ? (n + s.each - 1) / s.each : 1;
+  const int parts = (s.last - s.first + kAttWaves - 1) / kAttWaves;
+  s.parts = parts < 1 ? 1 : parts < splits ? parts : splits;
   return s;
 }
 
@@ -177,12 +174,12 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int seq = blockIdx.z, part = blockIdx.y;
   const int head = blockIdx.x / a.tiles, tile = blockIdx.x - head * a.tiles;
-  const Span sp = att_span(a.c, a.lens[seq], a.queries, a.window, a.splits);
-  if (part >= sp.parts) return;
   const int per = a.heads / a.c.kv_heads, rows = per * a.queries;
   const int row0 = tile * 16;
-  const int b0 = sp.first + part * sp.each;
-  const int b1 = b0 + sp.each < sp.last ? b0 + sp.each : sp.last;
+  const int stride = kAttWaves * a.splits;
+  const int len = a.lens[seq];
+  int b = part * kAttWaves + wv;
+  if (a.window > 0) b += att_span(a.c, len, a.queries, a.window, a.splits).first;
 
   uint8_t* const lds = smem[wv];
   const int64_t page_size = kv_page_size(a.c);
@@ -226,18 +223,20 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
     for (int s = 0; s < KS; ++s) __builtin_memcpy(&x.v[s], own + 8 * DIM + (16 * s + t16) * 16, 16);
   };
 
-  int b = b0 + wv;
-  const uint8_t* own;
-  int page = -1, page_n = -1, key_page_n = -1;
+  // the pages' numbers of this wave's first two blocks, then the length
+  int bn = b + stride, key_page = -1, page = -1, key_page_n = -1, page_n = -1;
+  if (a.c.max_pages) {
+    key_page = page_of(b, kblk), page = page_of(b, quarter);
+    key_page_n = page_of(bn, kblk), page_n = page_of(bn, quarter);
+  }
+  const Span sp = att_span(a.c, len, a.queries, a.window, a.splits);
+  if (part >= sp.parts) return;
+  const int b1 = sp.last;
   // the loads of the loop are one sequence without branches, so that each wait counts
   // just the loads behind the one it is for: at the end the last block again
-  int bn = b + kAttWaves < b1 ? b + kAttWaves : b;
+  if (bn >= b1) bn = b, key_page_n = key_page, page_n = page;
   if (b < b1) {
-    const int key_page = page_of(b, kblk);
-    page = page_of(b, quarter);
-    key_page_n = page_of(bn, kblk);
-    page_n = page_of(bn, quarter);
-    own = block_at(b, quarter, page);
+    const uint8_t* own = block_at(b, quarter, page);
     load_k(block_at(b, kblk, key_page), own);
     load_v(own);
   }
@@ -328,7 +327,7 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
   // the weights' unit: 2^6 over a power of two above the largest scale so far
   float smax = 0.f, pu = 1.f;
 
-  for (; b < b1; b += kAttWaves) {
+  for (; b < b1; b += stride) {
     const int t0 = b * kAttTokens;
     const bool bad = outside(page);
     const bool edge = t0 < all_first || t0 + kAttTokens - 1 > all_last || __any(bad);
@@ -398,7 +397,7 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
     const int page_b = page_n;
     const uint8_t* own_n = block_at(bn, quarter, page_n);
     const uint8_t* key_n = block_at(bn, kblk, key_page_n);
-    bn = bn + kAttWaves < b1 ? bn + kAttWaves : bn;
+    bn = bn + stride < b1 ? bn + stride : bn;
     key_page_n = page_of(bn, kblk);
     page_n = page_of(bn, quarter);
     load_k(key_n, own_n);
@@ -554,42 +553,62 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
 }
 
 // Joins the parts of a row: a workgroup per row, its parts dealt to groups of DIM / 4
-// threads, four channels per thread.
+// threads, four channels per thread.  The parts are asked for before the length says how many
+// there are (the others hold anything, within the workspace), so that it all takes one trip.
 template <int DIM>
 __global__ void __launch_bounds__(256) attend_join_kernel(AttArgs a) {
-  constexpr int T = DIM / 4, N = 256 / T;
+  constexpr int T = DIM / 4, N = 256 / T, U = 8;
   __shared__ f32x4_t part[N][T];
-  __shared__ float sums[N];
+  __shared__ float maxima[N], sums[N];
   const int per = a.heads / a.c.kv_heads, rows = per * a.queries;
   const int seq = blockIdx.y, head = blockIdx.x / rows, r = blockIdx.x - head * rows;
-  const Span sp = att_span(a.c, a.lens[seq], a.queries, a.window, a.splits);
-  if (sp.parts == 1) return;  // written by its only workgroup
+  const int len = a.lens[seq];
   const size_t n = (size_t)rows * a.splits;
   const size_t at = ((size_t)seq * a.c.kv_heads + head) * n + r;
   const float* ml = a.parts + (size_t)a.c.seqs * a.c.kv_heads * n * DIM + 2 * at;
   const float* o = a.parts + at * DIM;
-  float big = -__builtin_inff();
-  for (int p = threadIdx.x & (kWave - 1); p < sp.parts; p += kWave)
-    big = fmaxf(big, ml[(size_t)2 * p * rows]);
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) big = fmaxf(big, __shfl_xor(big, d, kWave));
   const int g = threadIdx.x / T, c = threadIdx.x - g * T;
-  float sum = 0.f;
+  float big = -__builtin_inff(), sum = 0.f;
   f32x4_t v = {0, 0, 0, 0};
-#pragma unroll 4
-  for (int p = g; p < sp.parts; p += N) {
-    const float mp = ml[(size_t)2 * p * rows];
-    const float f = mp == big ? 1.f : __builtin_amdgcn_exp2f(mp - big);
-    sum = __builtin_fmaf(ml[(size_t)2 * p * rows + 1], f, sum);
-    f32x4_t w;
-    __builtin_memcpy(&w, o + (size_t)p * rows * DIM + 4 * c, 16);
-    v += w * f;
+  int parts = a.splits;
+  for (int p0 = g; p0 < parts; p0 += U * N) {
+    f32x4_t w[U];
+    float mp[U], lp[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int p = p0 + k * N < a.splits ? p0 + k * N : p0;
+      __builtin_memcpy(&w[k], o + (size_t)p * rows * DIM + 4 * c, 16);
+      mp[k] = ml[(size_t)2 * p * rows], lp[k] = ml[(size_t)2 * p * rows + 1];
+    }
+    parts = att_span(a.c, len, a.queries, a.window, a.splits).parts;
+    float top = big;
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (p0 + k * N < parts) top = fmaxf(top, mp[k]);
+    const float f = big == top ? 1.f : __builtin_amdgcn_exp2f(big - top);
+    big = top, sum *= f, v *= f;
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (p0 + k * N < parts) {
+        const float e = mp[k] == top ? 1.f : __builtin_amdgcn_exp2f(mp[k] - top);
+        sum = __builtin_fmaf(lp[k], e, sum);
+        v += w[k] * e;
+      }
   }
+  parts = att_span(a.c, len, a.queries, a.window, a.splits).parts;
+  if (parts == 1) return;  // written by its only workgroup
   part[g][c] = v;
-  if (c == 0) sums[g] = sum;
+  if (c == 0) maxima[g] = big, sums[g] = sum;
   __syncthreads();
   if (g == 0) {
-    for (int k = 1; k < N; ++k) v += part[k][c], sum += sums[k];
+    float top = big;
+    for (int k = 1; k < N; ++k) top = fmaxf(top, maxima[k]);
+    sum = 0.f, v = f32x4_t{0, 0, 0, 0};
+    for (int k = 0; k < N; ++k) {
+      const float e = maxima[k] == top ? 1.f : __builtin_amdgcn_exp2f(maxima[k] - top);
+      sum = __builtin_fmaf(sums[k], e, sum);
+      v += part[k][c] * e;
+    }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int query = r / per, h = head * per + r - query * per;
     att_store4(a.out, a.out_type,
