@@ -20,7 +20,7 @@
 namespace lvq {
 
 constexpr float kMoeUnit = 0x1p-18f;   // of a code inside an fp16
-constexpr int kGateWaves = 16, kDownWaves = 8;
+constexpr int kGateWaves = 16;
 constexpr int kMaxPairs = LVQ_MAX_MOE_TOKENS * LVQ_MAX_MOE_TOP;
 constexpr int kMaxExperts = 512;
 
@@ -116,9 +116,10 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 // The top of a token's logits, by a wave: expert j goes to lane j's *id and *weight.
 // Values are compared as integers of the same order; equal ones go by their index.  A NaN
 // is below everything, and makes the token's weights NaN.
+// S: values per lane.
+template <int S>
 __device__ __forceinline__ void choose(const float* logits, int experts, int top, bool renormalize,
                                        int lane, int* id, float* weight) {
-  constexpr int S = kMaxExperts / kWave;
   float v[S];
   uint32_t key[S];
   bool nan = false;
@@ -166,47 +167,75 @@ __device__ __forceinline__ void choose(const float* logits, int experts, int top
   *weight = nan ? __builtin_nanf("") : p / total;
 }
 
-// The pairs (token, chosen expert) by expert, and the jobs: up to four tokens of one expert.
-struct Jobs {
-  uint16_t expert[kMaxPairs], first[kMaxPairs], count[kMaxPairs];
-  uint16_t pair[kMaxPairs];   // sorted by expert, then by token
-  uint16_t flags[kMaxPairs];
-  uint16_t ids[kMaxPairs];    // of each pair
+// A job: some tokens of one expert, up to four in the second launch and two in the third.  Its
+// activations are rows first, first + 1, ... of the workspace: the pairs (token, chosen
+// expert) sorted by expert, then by token.
+struct Job {
+  uint16_t expert, first;
+  uint16_t tokens;  // four bits each
+  uint16_t count;
+};
+// What the second launch leaves for the third.
+struct JobList {
+  int n, pad[3];
+  Job job[kMaxPairs];
+  float weight[kMaxPairs];  // of a row of activations
+};
+struct JobSpace {
+  uint16_t mask[kMaxExperts];   // tokens that chose the expert
+  uint16_t start[kMaxExperts];  // its first row
+  uint32_t total[kMaxExperts / kWave];
   int n;
+  Job job[kMaxPairs];
 };
 
-// ids[] is filled; every thread of the workgroup calls.
-__device__ __forceinline__ void make_jobs(Jobs& j, int pairs, int threads) {
+// From the masks (complete, but for a barrier) the jobs, and the third launch's (to `list`
+// unless NULL).  Every thread of the workgroup, at least kMaxExperts of them, calls.
+__device__ __forceinline__ void make_jobs(JobSpace& j, JobList* list) {
   __syncthreads();
-  for (int p = threadIdx.x; p < pairs; p += threads) {
-    const int e = j.ids[p];
-    int before = 0, start = 0, same = 0;
-    for (int q = 0; q < pairs; ++q) {
-      const int o = j.ids[q];
-      start += o < e;
-      same += o == e;
-      before += o == e && q < p;
+  const int e = threadIdx.x, lane = e & (kWave - 1), wv = e / kWave;
+  uint32_t m = 0, sum = 0, own = 0;
+  if (e < kMaxExperts) {
+    m = j.mask[e];
+    const uint32_t c = __builtin_popcount(m);
+    own = sum = c | ((c + 3) / 4) << 10 | ((c + 1) / 2) << 20;  // rows, jobs of four, of two
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+      const uint32_t o = __shfl_up(sum, d, kWave);
+      if (lane >= d) sum += o;
     }
-    j.pair[start + before] = (uint16_t)p;
-    // a job starts at every fourth token of an expert; how many it holds
-    const int left = same - before;
-    j.flags[start + before] = (uint16_t)(before % 4 ? 0 : left < 4 ? left : 4);
+    if (lane == kWave - 1) j.total[wv] = sum;
   }
   __syncthreads();
-  if (threadIdx.x < kWave) {
-    int n = 0;
-    for (int p0 = 0; p0 < pairs; p0 += kWave) {
-      const int p = p0 + threadIdx.x;
-      const int c = p < pairs ? j.flags[p] : 0;
-      const uint64_t who = __ballot(c != 0);
-      if (c) {
-        const int at = n + __builtin_popcountll(who & ((1ull << threadIdx.x) - 1));
-        j.expert[at] = j.ids[j.pair[p]];
-        j.first[at] = (uint16_t)p, j.count[at] = (uint16_t)c;
-      }
-      n += __builtin_popcountll(who);
+  if (e < kMaxExperts) {
+    uint32_t base = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kMaxExperts / kWave; ++w) {
+      base += w < wv ? j.total[w] : 0;
+      all += j.total[w];
     }
-    if (threadIdx.x == 0) j.n = n;
+    base += sum - own;
+    int row = base & 1023, at = base >> 10 & 1023, at2 = base >> 20;
+    j.start[e] = (uint16_t)row;
+    for (int left = own & 1023; left > 0; left -= 4, row += 4) {
+      const int n = left < 4 ? left : 4;
+      uint32_t t = 0;
+      for (int b = 0; b < n; ++b) {
+        t |= (uint32_t)__builtin_ctz(m) << (4 * b);
+        m &= m - 1;
+      }
+      j.job[at++] = Job{(uint16_t)e, (uint16_t)row, (uint16_t)t, (uint16_t)n};
+      if (list) {
+        list->job[at2++] = Job{(uint16_t)e, (uint16_t)row, (uint16_t)t, (uint16_t)(n < 2 ? n : 2)};
+        if (n > 2)
+          list->job[at2++] =
+              Job{(uint16_t)e, (uint16_t)(row + 2), (uint16_t)(t >> 8), (uint16_t)(n - 2)};
+      }
+    }
+    if (e == 0) {
+      j.n = (int)(all >> 10 & 1023);
+      if (list) list->n = (int)(all >> 20);
+    }
   }
   __syncthreads();
 }
@@ -219,14 +248,13 @@ struct GateArgs {
   const uint16_t* zero;
   const uint16_t* x;
   const float* logits;
-  int32_t* ids;      // workspace, then the caller's (may be NULL)
-  float* weights;
-  int32_t* ids_out;
+  JobList* jobs;
+  int32_t* ids_out;  // may be NULL
   float* weights_out;
   uint16_t* act;     // [pairs][pitch] rounded values, then as many rests
   int hidden, inner, wgs;
   uint16_t tokens, experts, top;
-  uint8_t gshift, renormalize;
+  uint8_t gshift, renormalize, waves;
 };
 static_assert(sizeof(GateArgs) < 128, "launches of 128 bytes and more are slower");
 
@@ -235,6 +263,15 @@ static_assert(sizeof(GateArgs) < 128, "launches of 128 bytes and more are slower
 __host__ __device__ inline int x_row_bytes(int steps) { return steps * 1024 + 32; }
 inline size_t gate_lds_bytes(int tokens, int steps) {
   return (size_t)tokens * (x_row_bytes(steps) + steps * 64);
+}
+
+// Activations in the workspace: a row of whole steps, each as four words of 16 units, so that a
+// load of one word of all units is of adjacent bytes; the eight values of a word in the
+// order of the operands' pairs (the bits of their number reversed).
+__host__ __device__ inline int act_pitch(int inner) { return (inner + 511) / 512 * 512; }
+__device__ __forceinline__ int act_place(int c) {
+  return (c & ~511) + (c >> 3 & 3) * 128 + (c >> 5 & 15) * 8 +
+         ((c & 1) << 2 | (c & 2) | (c >> 2 & 1));
 }
 
 // Four steps of codes of a gate and an up quad; scales (low) and zeros of their groups.
@@ -247,7 +284,7 @@ struct GateChunk {
 template <int NS, bool Z>
 __global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ Jobs jobs;
+  __shared__ JobSpace jobs;
   const int nunits = (a.hidden + 31) / 32, steps = (nunits + 15) / 16;
   const int groups = ((nunits - 1) >> a.gshift) + 1;
   const int row_x = x_row_bytes(steps);
@@ -256,8 +293,22 @@ __global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a)
   const int lane = threadIdx.x & (kWave - 1), ul = lane >> 2, r4 = lane & 3;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  // 1. x into LDS, and minus the sums of its units, as the products start from them
-  for (int i = wv; i < a.tokens * steps; i += kGateWaves) {
+  const int nw = a.waves;
+
+  // 1. the choice, a token per wave
+  if (a.tokens > 1)
+    for (int e = threadIdx.x; e < kMaxExperts; e += nw * kWave) jobs.mask[e] = 0;
+  int id = 0;
+  float weight = 0.f;
+  const bool chooses = wv < a.tokens;
+  if (chooses) {
+    const float* l = a.logits + (size_t)wv * a.experts;
+    if (a.experts <= 2 * kWave) choose<2>(l, a.experts, a.top, a.renormalize, lane, &id, &weight);
+    else choose<kMaxExperts / kWave>(l, a.experts, a.top, a.renormalize, lane, &id, &weight);
+  }
+
+  // 2. x into LDS, and minus the sums of its units, as the products start from them
+  for (int i = wv; i < a.tokens * steps; i += nw) {
     const int t = i / steps, st = i - t * steps, c = (st * 64 + lane) * 8;
     const uint16_t* row = a.x + (size_t)t * a.hidden;
     u32x4_t v = {0, 0, 0, 0};
@@ -274,46 +325,55 @@ __global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a)
     s = dpp_add<0x4E, 0xF>(dpp_add<0xB1, 0xF>(s));
     if (r4 == 0) sums[(t * steps + st) * 16 + ul] = s * ((Z ? -1.f : -8.f) * kMoeUnit);
   }
-
-  // 2. the choice
-  for (int t = wv; t < a.tokens; t += kGateWaves) {
-    int id;
-    float w;
-    choose(a.logits + (size_t)t * a.experts, a.experts, a.top, a.renormalize, lane, &id, &w);
-    if (lane < a.top) {
-      const int p = t * a.top + lane;
-      jobs.ids[p] = (uint16_t)id;
-      if (blockIdx.x == 0) {
-        a.ids[p] = id, a.weights[p] = w;
-        if (a.ids_out) a.ids_out[p] = id;
-        if (a.weights_out) a.weights_out[p] = w;
-      }
-    }
+  const bool chose = chooses && lane < a.top;
+  JobList* const list = blockIdx.x == 0 ? a.jobs : nullptr;
+  int at = lane;
+  if (a.tokens == 1) {  // a job per chosen expert, as they come
+    const Job job = {(uint16_t)id, (uint16_t)lane, 0, 1};
+    if (chose) jobs.job[lane] = job;
+    if (threadIdx.x == 0) jobs.n = a.top;
+    if (list && chose) list->job[lane] = job;
+    if (list && threadIdx.x == 0) list->n = a.top;
+    __syncthreads();
+  } else {
+    __syncthreads();
+    // two experts may share a word: or-ed in whole words
+    if (chose) atomicOr((uint32_t*)jobs.mask + id / 2, (uint32_t)1 << (wv + 16 * (id & 1)));
+    make_jobs(jobs, list);
+    if (chose) at = jobs.start[id] + __builtin_popcount(jobs.mask[id] & ((1u << wv) - 1));
   }
-  make_jobs(jobs, a.tokens * a.top, kGateWaves * kWave);
+  if (list && chose) {
+    list->weight[at] = weight;
+    if (a.ids_out) a.ids_out[wv * a.top + lane] = id;
+    if (a.weights_out) a.weights_out[wv * a.top + lane] = weight;
+  }
 
   // 3. items: a job and four rows of the activation, whole rows of the weights
-  const int pitch = ((a.inner + 31) / 32) * 32, quads = pitch / 4;
+  // the padding of the last unit is written too, as zeros
+  const int quads = (a.inner + 31) / 32 * 8;
   const int row_bytes = nunits * 16, chunks = (steps + 3) / 4;
-  const int items = jobs.n * quads, stride = a.wgs * kGateWaves;
-  const size_t lo = (size_t)a.tokens * a.top * pitch;
+  const int items = jobs.n * quads, stride = a.wgs * nw;
+  const size_t lo = (size_t)a.tokens * a.top * act_pitch(a.inner);
   struct Cursor {
     int item, chunk;
   };
-  Cursor ld = {(int)blockIdx.x * kGateWaves + wv, 0}, at = ld;
+  Cursor ld = {(int)blockIdx.x * nw + wv, 0}, cu = ld;
   auto advance = [&](Cursor& c) {
     if (++c.chunk == chunks) c.chunk = 0, c.item += stride;
   };
   const int lane_off = r4 * row_bytes + ul * 16;
   GateChunk<NS> ring[2];
   auto load = [&](GateChunk<NS>& k) {
-    if (ld.item >= items) return;
-    const int job = ld.item / quads, quad = ld.item - job * quads, t0 = ld.chunk * 4;
-    const size_t e = jobs.expert[job];
+    // no branch around the loop's loads, so that each wait counts just those behind the one
+    // it is for; past the last item they are of empty ranges
+    const bool none = ld.item >= items;
+    const int item = none ? 0 : ld.item;
+    const int job = item / quads, quad = item - job * quads, t0 = ld.chunk * 4;
+    const size_t e = __builtin_amdgcn_readfirstlane(jobs.job[job].expert);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int row = quad * 4 + (h ? a.inner : 0), left = 2 * a.inner - row;
-      const int rows = left < 0 ? 0 : left < 4 ? left : 4;
+      const int rows = none || left < 0 ? 0 : left < 4 ? left : 4;
       const size_t first = e * 2 * a.inner + (rows ? row : 0);
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
@@ -331,7 +391,7 @@ __global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int row = quad * 4 + (h ? a.inner : 0), left = 2 * a.inner - row;
-      const int rows = left < 0 ? 0 : left < 4 ? left : 4;
+      const int rows = none || left < 0 ? 0 : left < 4 ? left : 4;
       const size_t first = e * 2 * a.inner + (rows ? row : 0);
       const uint8_t* base = a.codes + first * row_bytes + t0 * 256;
       const uint32_t bytes = rows ? rows * row_bytes - t0 * 256 : 0;
@@ -350,10 +410,13 @@ __global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a)
     for (int b = 0; b < 4; ++b) acc[h][b] = 0.f;
   const int from = (((ul >> a.gshift) << 2) | r4) << 2, from_step = (16 >> a.gshift) << 4;
   auto consume = [&](const GateChunk<NS>& k) {
-    if (at.item >= items) return;
-    const int job = at.item / quads, quad = at.item - job * quads, t0 = at.chunk * 4;
-    const int first = jobs.first[job], nb = jobs.count[job];
-    auto token = [&](int b) { return (int)jobs.pair[first + (b < nb ? b : 0)] / a.top; };
+    if (cu.item >= items) return;
+    const int job = cu.item / quads, quad = cu.item - job * quads, t0 = cu.chunk * 4;
+    const Job jb = jobs.job[job];
+    const int nb = __builtin_amdgcn_readfirstlane(jb.count);
+    const int first = __builtin_amdgcn_readfirstlane(jb.first);
+    const int tokens = __builtin_amdgcn_readfirstlane(jb.tokens);
+    auto token = [&](int b) { return tokens >> (4 * b) & 15; };  // 0 past the last
     const uint8_t* xl = xs + token(r4) * row_x + ul * 16 + t0 * 1024;
     const float* sl[4];
 #pragma unroll
@@ -399,8 +462,8 @@ __global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a)
         for (int b = 0; b < 4; ++b) acc[h][b] = __builtin_fmaf(s, c[h][b], acc[h][b]);
       }
     }
-    advance(at);
-    if (at.chunk) return;
+    advance(cu);
+    if (cu.chunk) return;
     // the rows' end: sums over the units, the activation in lane 4 b + i of token b, row i
     float g = 0.f, u = 0.f;
 #pragma unroll
@@ -419,21 +482,21 @@ __global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a)
       const int row = quad * 4 + r4;
       if (row >= a.inner) v = 0.f;
       const _Float16 hi = (_Float16)v, rest = (_Float16)(v - (float)hi);
-      // in the order of the operands' pairs: bits of the column within eight reversed
-      const int col = (row & ~7) | (row & 1) << 2 | (row & 2) | (row >> 2 & 1);
-      const size_t to = (size_t)jobs.pair[first + ul] * pitch + col;
+      const size_t to = (size_t)(first + ul) * act_pitch(a.inner) + act_place(row);
       a.act[to] = __builtin_bit_cast(uint16_t, hi);
       a.act[lo + to] = __builtin_bit_cast(uint16_t, rest);
     }
   };
-  load(ring[0]);
-  load(ring[1]);
-  while (at.item < items) {
+  if (ld.item < items) load(ring[0]);
+  if (ld.item < items) load(ring[1]);
+  while (ld.item < items) {
     consume(ring[0]);
     load(ring[0]);
     consume(ring[1]);
     load(ring[1]);
   }
+  consume(ring[0]);
+  consume(ring[1]);
 }
 
 // ---------------------------------------------------------------- down
@@ -443,8 +506,7 @@ struct DownArgs {
   const uint16_t* scale;
   const uint16_t* zero;
   const uint16_t* act;
-  const int32_t* ids;
-  const float* weights;
+  const JobList* jobs;
   float* y;
   int hidden, inner;
   uint16_t tokens, top;
@@ -452,35 +514,36 @@ struct DownArgs {
 };
 static_assert(sizeof(DownArgs) < 128, "launches of 128 bytes and more are slower");
 
-// A workgroup: NQ quads of rows, all jobs; their steps are dealt to the waves in equal parts.
-template <int NQ, bool Z>
+// A workgroup: 8 rows, all jobs; their steps are dealt to its waves in equal parts.  A lane's
+// four operand rows are the rounded values and the rests of two tokens, so that one
+// product takes both: with a row per token, and the rests in a product of their own, a step's loads
+// of activations were eight, three quarters of them for tokens that were not there, and
+// the loads are what the launch is made of.
+constexpr int kDownWaves = 16, kDownQuads = 2;
+
+// NS: loads of scales per step (8 groups of 8 rows each).
+template <int NS, bool Z>
 __global__ void __launch_bounds__(kDownWaves* kWave) moe_down_kernel(DownArgs a) {
-  constexpr int R = 4 * NQ;
-  __shared__ Jobs jobs;
-  __shared__ float wts[kMaxPairs];
-  __shared__ float part[kDownWaves][LVQ_MAX_MOE_TOKENS * R];
+  constexpr int NQ = kDownQuads, R = 4 * NQ, W = kDownWaves, RING = 3;
+  __shared__ float part[W][LVQ_MAX_MOE_TOKENS * R];
   const int lane = threadIdx.x & (kWave - 1), ul = lane >> 2, r4 = lane & 3;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int pairs = a.tokens * a.top;
-  for (int p = threadIdx.x; p < pairs; p += kDownWaves * kWave) {
-    jobs.ids[p] = (uint16_t)a.ids[p];
-    wts[p] = a.weights[p];
-  }
   for (int i = lane; i < a.tokens * R; i += kWave) part[wv][i] = 0.f;
-  make_jobs(jobs, pairs, kDownWaves * kWave);
 
   const int nunits = (a.inner + 31) / 32, steps = (nunits + 15) / 16;
   const int groups = ((nunits - 1) >> a.gshift) + 1;
-  const int pitch = nunits * 32, row_bytes = nunits * 16;
-  const int all = jobs.n * steps, per = (all + kDownWaves - 1) / kDownWaves;
+  const int pitch = act_pitch(a.inner), row_bytes = nunits * 16;
+  const int all = a.jobs->n * steps, per = (all + W - 1) / W;
   const int f0 = wv * per < all ? wv * per : all, f1 = f0 + per < all ? f0 + per : all;
   const int row0 = blockIdx.x * R;
+  const int rows = a.hidden - row0 < R ? a.hidden - row0 : R;
   const uint32_t act_bytes = (uint32_t)pairs * pitch * 2;
 
   struct Step {
-    u32x4_t x[2][4];
+    u32x4_t x[4];
     u32x4_t w[NQ];
-    uint16_t s[NQ], z[NQ];
+    uint16_t s[NS], z[NS];
   };
   struct Cursor {
     int f, job, t;
@@ -491,122 +554,128 @@ __global__ void __launch_bounds__(kDownWaves* kWave) moe_down_kernel(DownArgs a)
     if (++c.t == steps) c.t = 0, ++c.job;
   };
   Cursor ld = start(f0), at = ld;
+  Job job_n = a.jobs->job[ld.job < kMaxPairs ? ld.job : 0];  // of the next load
+  // scales: lane (ul, r4) asks for row 4 (ul / 8) + r4 of the rows, group ul % 8 of the step's
+  const int scale_row = 4 * (ul >> 3) + r4;
   auto load = [&](Step& k) {
-    if (ld.f >= f1) return;
-    const int first = jobs.first[ld.job], nb = jobs.count[ld.job];
-    const size_t e = jobs.expert[ld.job];
+    // no branch around the loads, as in the gate's
+    const bool past = ld.f >= f1;
+    const size_t e = job_n.expert;
     const int u = ld.t * 16 + ul;
-    const int pair = jobs.pair[first + (r4 < nb ? r4 : 0)];
-    const bool none = r4 >= nb || u >= nunits;
-    const uint32_t xo = none ? 0x80000000u : (uint32_t)pair * (pitch * 2) + u * 64;
+    const bool none = past || (r4 >> 1) >= job_n.count || u >= nunits;
+    const uint32_t xo = none ? 0x80000000u
+                             : (r4 & 1) * act_bytes + (uint32_t)(job_n.first + (r4 >> 1)) * (pitch * 2) +
+                                   ld.t * 1024 + ul * 16;
+    const size_t fr = e * a.hidden + row0;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const int row = row0 + 4 * q, left = a.hidden - row;
-      const int rows = left < 0 ? 0 : left < 4 ? left : 4;
-      const size_t fr = e * a.hidden + (rows ? row : 0);
-      const int g = u >> a.gshift;
-      const int off = ((r4 * groups + g) * 2) | ((groups - 1 - g) & (int)0x80000000);
-      const uint32_t sb = (uint32_t)(rows * groups) * 2;
-      k.s[q] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.scale + fr * groups, sb), off, 0, 0);
+    for (int n = 0; n < NS; ++n) {
+      const int g = ((ld.t * 16) >> a.gshift) + n * 8 + (ul & 7);
+      const int off = ((scale_row * groups + g) * 2) | ((groups - 1 - g) & (int)0x80000000);
+      const uint32_t sb = past ? 0 : (uint32_t)(rows * groups) * 2;
+      k.s[n] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.scale + fr * groups, sb), off, 0, 0);
       if constexpr (Z)
-        k.z[q] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.zero + fr * groups, sb), off, 0, 0);
-      const uint32_t bytes = rows ? rows * row_bytes - ld.t * 256 : 0;
-      k.w[q] = __builtin_bit_cast(
-          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                       q4_rsrc(a.codes + fr * row_bytes + ld.t * 256, bytes),
-                       r4 * row_bytes + ul * 16, 0, 2));
+        k.z[n] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.zero + fr * groups, sb), off, 0, 0);
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int w = 0; w < 4; ++w)
+      k.x[w] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(q4_rsrc(a.act, 2 * act_bytes), (int)xo,
+                                                         w * 256, 0));
+    const auto codes = q4_rsrc(a.codes + fr * row_bytes + ld.t * 256,
+                               past ? 0 : rows * row_bytes - ld.t * 256);
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        k.x[h][w] = __builtin_bit_cast(
-            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                         q4_rsrc((const uint8_t*)a.act + (size_t)h * act_bytes, act_bytes), (int)xo,
-                         w * 16, 0));
+    for (int q = 0; q < NQ; ++q)
+      k.w[q] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(codes, (4 * q + r4) * row_bytes + ul * 16, 0,
+                                                         2));
     next(ld);
+    job_n = a.jobs->job[ld.f < f1 ? ld.job : 0];
   };
   float acc[NQ][4];
 #pragma unroll
   for (int q = 0; q < NQ; ++q)
 #pragma unroll
     for (int b = 0; b < 4; ++b) acc[q][b] = 0.f;
+  const int rel = ul >> a.gshift;  // this lane's group of the step's
   auto consume = [&](const Step& k) {
     if (at.f >= f1) return;
     constexpr uint32_t kOne = 0x00400040u, m = 0x03C003C0u;
     const half4_t ones = __builtin_bit_cast(half4_t, u32x2_t{kOne, kOne});
     float4_t sum = {0, 0, 0, 0};
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const u32x4_t x = k.x[h][w];
-        sum = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}),
-                                                 ones, sum, 0, 0, 0);
-        sum = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}),
-                                                 ones, sum, 0, 0, 0);
-      }
+    for (int w = 0; w < 4; ++w) {
+      const u32x4_t x = k.x[w];
+      sum = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}), ones,
+                                               sum, 0, 0, 0);
+      sum = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}), ones,
+                                               sum, 0, 0, 0);
+    }
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const float z = Z ? -f16_to_f32(k.z[q]) : -8.f;
+      // from the lane that holds the scale: row r4 of quad q, group rel
+      uint32_t sz = 0;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        const uint32_t both = (uint32_t)k.s[n] | (Z ? (uint32_t)k.z[n] << 16 : 0x48000000u);
+        const uint32_t v = (uint32_t)__builtin_amdgcn_ds_bpermute(
+            ((q * 8 + (rel & 7)) * 4 + r4) * 4, (int)both);
+        sz = n == 0 || (rel >> 3) == n ? v : sz;
+      }
+      const float z = -f16_to_f32(sz >> 16);
       float4_t c;
 #pragma unroll
       for (int b = 0; b < 4; ++b) c[b] = z * sum[b];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
+        const u32x4_t x = k.x[w];
         const uint32_t v = k.w[q][w];
-        const half4_t lo = __builtin_bit_cast(half4_t, u32x2_t{(v << 6) & m, (v >> 2) & m});
-        const half4_t hi = __builtin_bit_cast(half4_t, u32x2_t{(v << 2) & m, (v >> 6) & m});
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32x4_t x = k.x[h][w];
-          c = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}), lo,
-                                                 c, 0, 0, 0);
-          c = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}), hi,
-                                                 c, 0, 0, 0);
-        }
+        c = __builtin_amdgcn_mfma_f32_4x4x4f16(
+            __builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}),
+            __builtin_bit_cast(half4_t, u32x2_t{(v << 6) & m, (v >> 2) & m}), c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_4x4x4f16(
+            __builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}),
+            __builtin_bit_cast(half4_t, u32x2_t{(v << 2) & m, (v >> 6) & m}), c, 0, 0, 0);
       }
-      const float s = f16_to_f32(k.s[q]);
+      const float s = f16_to_f32(sz);
 #pragma unroll
       for (int b = 0; b < 4; ++b) acc[q][b] = __builtin_fmaf(s, c[b], acc[q][b]);
     }
     const int job = at.job;
     next(at);
     if (at.f < f1 && at.t) return;
-    const int first = jobs.first[job], nb = jobs.count[job];
+    const Job jb = a.jobs->job[job];
+    const float weight = ul < jb.count ? a.jobs->weight[jb.first + ul] : 0.f;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      float v = 0.f;
+      const float v0 = sum_blocks(acc[q][0] + acc[q][1]);
+      const float v1 = jb.count > 1 ? sum_blocks(acc[q][2] + acc[q][3]) : 0.f;
+      if (ul < jb.count) {
+        float* to = &part[wv][(jb.tokens >> (4 * ul) & 15) * R + 4 * q + r4];
+        *to = __builtin_fmaf(weight, (ul ? v1 : v0) * (1.f / kMoeUnit), *to);
+      }
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (b < nb) {
-          const float s = sum_blocks(acc[q][b]);
-          v = ul == b ? s : v;
-        }
-        acc[q][b] = 0.f;
-      }
-      if (ul < nb) {
-        const int p = jobs.pair[first + ul];
-        float* to = &part[wv][p / a.top * R + 4 * q + r4];
-        *to = __builtin_fmaf(wts[p], v * (1.f / kMoeUnit), *to);
-      }
+      for (int b = 0; b < 4; ++b) acc[q][b] = 0.f;
     }
   };
-  Step ring[2];
-  load(ring[0]);
-  load(ring[1]);
-  while (at.f < f1) {
-    consume(ring[0]);
-    load(ring[0]);
-    consume(ring[1]);
-    load(ring[1]);
+  Step ring[RING];
+#pragma unroll
+  for (int d = 0; d < RING; ++d)
+    if (ld.f < f1) load(ring[d]);
+  while (ld.f < f1) {
+#pragma unroll
+    for (int d = 0; d < RING; ++d) {
+      consume(ring[d]);
+      load(ring[d]);
+    }
   }
+#pragma unroll
+  for (int d = 0; d < RING; ++d) consume(ring[d]);
   __syncthreads();
-  for (int i = threadIdx.x; i < a.tokens * R; i += kDownWaves * kWave) {
+  for (int i = threadIdx.x; i < a.tokens * R; i += W * kWave) {
     const int t = i / R, r = row0 + i - t * R;
     float v = part[0][i];
 #pragma unroll
-    for (int w = 1; w < kDownWaves; ++w) v += part[w][i];
+    for (int w = 1; w < W; ++w) v += part[w][i];
     if (r < a.hidden) a.y[(size_t)t * a.hidden + r] = v;
   }
 }
@@ -614,17 +683,16 @@ __global__ void __launch_bounds__(kDownWaves* kWave) moe_down_kernel(DownArgs a)
 // ---------------------------------------------------------------- launch
 
 struct MoeSpace {
-  size_t logits, ids, weights, act, all;
+  size_t logits, jobs, act, all;
 };
 inline MoeSpace moe_space(int tokens, int inner, int experts, int top) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   MoeSpace s;
   const size_t pairs = (size_t)tokens * top;
   s.logits = 0;
-  s.ids = up((size_t)tokens * experts * 4);
-  s.weights = s.ids + up(pairs * 4);
-  s.act = s.weights + up(pairs * 4);
-  s.all = s.act + up(pairs * ((inner + 31) / 32 * 32) * 4);
+  s.jobs = up((size_t)tokens * experts * 4);
+  s.act = s.jobs + up(sizeof(JobList));
+  s.all = s.act + up(pairs * act_pitch(inner) * 4);
   return s;
 }
 
@@ -637,7 +705,7 @@ inline bool moe_sizes_ok(int tokens, int hidden, int inner, int experts, int top
 
 template <int NS, bool Z>
 int launch_gate(const GateArgs& a, size_t lds, hipStream_t st) {
-  hipLaunchKernelGGL((moe_gate_kernel<NS, Z>), dim3(a.wgs), dim3(kGateWaves * kWave), lds, st, a);
+  hipLaunchKernelGGL((moe_gate_kernel<NS, Z>), dim3(a.wgs), dim3(a.waves * kWave), lds, st, a);
   return launch_status();
 }
 template <bool Z>
@@ -647,11 +715,12 @@ int launch_gate(const GateArgs& a, size_t lds, hipStream_t st) {
                          : launch_gate<1, Z>(a, lds, st);
 }
 
-template <int NQ>
+template <int NS>
 int launch_down(const DownArgs& a, hipStream_t st) {
-  const dim3 grid((a.hidden + 4 * NQ - 1) / (4 * NQ)), block(kDownWaves * kWave);
-  if (a.zero) hipLaunchKernelGGL((moe_down_kernel<NQ, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((moe_down_kernel<NQ, false>), grid, block, 0, st, a);
+  const int rows = 4 * kDownQuads;
+  const dim3 grid((a.hidden + rows - 1) / rows), block(kDownWaves * kWave);
+  if (a.zero) hipLaunchKernelGGL((moe_down_kernel<NS, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((moe_down_kernel<NS, false>), grid, block, 0, st, a);
   return launch_status();
 }
 
@@ -714,7 +783,7 @@ extern "C" int q4_moe(const uint16_t* x, int tokens, int hidden, const void* rou
   }
   const int steps = steps_of(hidden);
   const size_t lds = gate_lds_bytes(tokens, steps);
-  if (lds + sizeof(Jobs) > device_lds_bytes()) return LVQ_E_SHAPE;
+  if (lds + sizeof(JobSpace) > device_lds_bytes()) return LVQ_E_SHAPE;
   uint8_t* w = (uint8_t*)workspace;
   hipStream_t st = (hipStream_t)stream;
   RouterArgs r = {x, router, (float*)(w + sp.logits), tokens, hidden, experts, router_type};
@@ -724,18 +793,24 @@ extern "C" int q4_moe(const uint16_t* x, int tokens, int hidden, const void* rou
   if (e) return e;
   GateArgs g;
   g.codes = gu_codes, g.scale = gu_scale, g.zero = gu_zero, g.x = x;
-  g.logits = r.logits, g.ids = (int32_t*)(w + sp.ids), g.weights = (float*)(w + sp.weights);
+  g.logits = r.logits, g.jobs = (JobList*)(w + sp.jobs);
   g.ids_out = ids_out, g.weights_out = weights_out, g.act = (uint16_t*)(w + sp.act);
   g.hidden = hidden, g.inner = inner;
   g.tokens = (uint16_t)tokens, g.experts = (uint16_t)experts, g.top = (uint16_t)top;
   g.gshift = (uint8_t)gs, g.renormalize = (uint8_t)renormalize;
   // at most a job per pair
   const long long items = (long long)pairs * units_of(inner) * 8;
-  const long long wgs = (items + kGateWaves - 1) / kGateWaves;
-  g.wgs = wgs < device_cus() ? (int)wgs : device_cus();
+  // a workgroup per CU, of as many waves as there are items for; the jobs of more than
+  // one token take kMaxExperts threads to sort
+  const int cus = device_cus(), least = tokens > 1 ? kMaxExperts / kWave : 1;
+  const long long need = (items + cus - 1) / cus;
+  const int waves = need > kGateWaves ? kGateWaves : need < least ? least : (int)need;
+  g.waves = (uint8_t)(waves < tokens ? tokens : waves);
+  const long long wgs = (items + g.waves - 1) / g.waves;
+  g.wgs = wgs < cus ? (int)wgs : cus;
   e = gu_zero ? launch_gate<true>(g, lds, st) : launch_gate<false>(g, lds, st);
   if (e) return e;
-  DownArgs d = {down_codes, down_scale, down_zero, g.act, g.ids, g.weights, y, hidden, inner,
+  DownArgs d = {down_codes, down_scale, down_zero, g.act, g.jobs, y, hidden, inner,
                 (uint16_t)tokens, (uint16_t)top, (uint8_t)ds};
-  return hidden >= 16 * device_cus() ? launch_down<4>(d, st) : launch_down<2>(d, st);
+  return ds == 0 ? launch_down<2>(d, st) : launch_down<1>(d, st);
 }
