@@ -170,7 +170,7 @@ __device__ __forceinline__ void choose(const float* logits, int experts, int top
 // A job: some tokens of one expert, up to four in the second launch and two in the third.  Its
 // activations are rows first, first + 1, ... of the workspace: the pairs (token, chosen
 // expert) sorted by expert, then by token.
-struct Job {
+struct __attribute__((aligned(8))) Job {
   uint16_t expert, first;
   uint16_t tokens;  // four bits each
   uint16_t count;
@@ -487,19 +487,29 @@ __global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a)
       a.act[lo + to] = __builtin_bit_cast(uint16_t, rest);
     }
   };
-  if (ld.item < items) load(ring[0]);
-  if (ld.item < items) load(ring[1]);
-  while (ld.item < items) {
-    consume(ring[0]);
+  if (ld.item + (chunks > 1 ? 0 : stride) < items) {  // two at least
     load(ring[0]);
-    consume(ring[1]);
     load(ring[1]);
+    while (ld.item < items) {
+      consume(ring[0]);
+      load(ring[0]);
+      consume(ring[1]);
+      load(ring[1]);
+    }
+  } else if (ld.item < items) {
+    load(ring[0]);
   }
   consume(ring[0]);
   consume(ring[1]);
 }
 
 // ---------------------------------------------------------------- down
+
+// Orders a wave's LDS accesses (its LDS instructions execute in order).
+__device__ __forceinline__ void lds_in_order() {
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
 
 struct DownArgs {
   const uint8_t* codes;
@@ -516,29 +526,51 @@ static_assert(sizeof(DownArgs) < 128, "launches of 128 bytes and more are slower
 
 // A workgroup: 8 rows, all jobs; their steps are dealt to its waves in equal parts.  A lane's
 // four operand rows are the rounded values and the rests of two tokens, so that one
-// product takes both: with a row per token, and the rests in a product of their own, a step's loads
-// of activations were eight, three quarters of them for tokens that were not there, and
-// the loads are what the launch is made of.
+// product takes both.  Codes and activations are loaded as they lie, 64 lanes one behind the
+// other, and reach their lanes through LDS: loaded by the lanes that multiply them,
+// four neighbours each read another row, and such a load takes the cache four times as
+// long (sixteen tokens, 2048x768: 31 us like that).
 constexpr int kDownWaves = 16, kDownQuads = 2;
+// LDS: four rows of 16 units, rows 32 bytes further apart than they are long, so that the
+// eight lanes that read at once (two units of four rows) lie in different banks
+constexpr int kCodesRow = 256 + 32, kActRow = 1024 + 32;
+constexpr int kDownLds = kDownQuads * 4 * kCodesRow + 4 * kActRow;
 
 // NS: loads of scales per step (8 groups of 8 rows each).
 template <int NS, bool Z>
 __global__ void __launch_bounds__(kDownWaves* kWave) moe_down_kernel(DownArgs a) {
   constexpr int NQ = kDownQuads, R = 4 * NQ, W = kDownWaves, RING = 3;
   __shared__ float part[W][LVQ_MAX_MOE_TOKENS * R];
+  __shared__ __attribute__((aligned(16))) uint8_t stage[W][kDownLds];
   const int lane = threadIdx.x & (kWave - 1), ul = lane >> 2, r4 = lane & 3;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint8_t* const codes_lds = stage[wv];
+  uint8_t* const act_lds = codes_lds + NQ * 4 * kCodesRow;
   const int pairs = a.tokens * a.top;
   for (int i = lane; i < a.tokens * R; i += kWave) part[wv][i] = 0.f;
+  // the list into LDS: a load from memory in the loop would wait for all that are on their way
+  __shared__ Job jobs[kMaxPairs];
+  __shared__ float weights[kMaxPairs];
+  const int n_jobs = a.jobs->n;
+  if ((int)threadIdx.x < pairs) {
+    jobs[threadIdx.x] = a.jobs->job[threadIdx.x];
+    weights[threadIdx.x] = a.jobs->weight[threadIdx.x];
+  }
+  __syncthreads();
+  auto job_at = [&](int i) {
+    const uint64_t j = *(const uint64_t*)&jobs[i];
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)j);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(j >> 32));
+    return __builtin_bit_cast(Job, (uint64_t)hi << 32 | lo);
+  };
 
   const int nunits = (a.inner + 31) / 32, steps = (nunits + 15) / 16;
   const int groups = ((nunits - 1) >> a.gshift) + 1;
   const int pitch = act_pitch(a.inner), row_bytes = nunits * 16;
-  const int all = a.jobs->n * steps, per = (all + W - 1) / W;
+  const int all = n_jobs * steps, per = (all + W - 1) / W;
   const int f0 = wv * per < all ? wv * per : all, f1 = f0 + per < all ? f0 + per : all;
   const int row0 = blockIdx.x * R;
   const int rows = a.hidden - row0 < R ? a.hidden - row0 : R;
-  const uint32_t act_bytes = (uint32_t)pairs * pitch * 2;
 
   struct Step {
     u32x4_t x[4];
@@ -554,42 +586,53 @@ __global__ void __launch_bounds__(kDownWaves* kWave) moe_down_kernel(DownArgs a)
     if (++c.t == steps) c.t = 0, ++c.job;
   };
   Cursor ld = start(f0), at = ld;
-  Job job_n = a.jobs->job[ld.job < kMaxPairs ? ld.job : 0];  // of the next load
   // scales: lane (ul, r4) asks for row 4 (ul / 8) + r4 of the rows, group ul % 8 of the step's
-  const int scale_row = 4 * (ul >> 3) + r4;
+  const int scale_off = (4 * (ul >> 3) + r4) * groups + (ul & 7);
+  const int code_off = (lane >> 4) * row_bytes + (lane & 15) * 16;
+  const auto act = q4_rsrc(a.act, 2 * pairs * pitch * 2);
+  // where the job of the next load begins
+  const uint8_t* codes;
+  size_t scales;
+  int act_row, count;
+  auto enter = [&](int i) {
+    const Job j = job_at(i);
+    const size_t first = (size_t)j.expert * a.hidden + row0;
+    codes = a.codes + first * row_bytes;
+    scales = first * groups;
+    act_row = j.first * (pitch * 2), count = j.count;
+  };
+  if (f0 < f1) enter(ld.job);
   auto load = [&](Step& k) {
     // no branch around the loads, as in the gate's
     const bool past = ld.f >= f1;
-    const size_t e = job_n.expert;
-    const int u = ld.t * 16 + ul;
-    const bool none = past || (r4 >> 1) >= job_n.count || u >= nunits;
-    const uint32_t xo = none ? 0x80000000u
-                             : (r4 & 1) * act_bytes + (uint32_t)(job_n.first + (r4 >> 1)) * (pitch * 2) +
-                                   ld.t * 1024 + ul * 16;
-    const size_t fr = e * a.hidden + row0;
+    const uint32_t sb = past ? 0 : (uint32_t)(rows * groups) * 2;
+    const int g0 = (ld.t * 16) >> a.gshift;
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
-      const int g = ((ld.t * 16) >> a.gshift) + n * 8 + (ul & 7);
-      const int off = ((scale_row * groups + g) * 2) | ((groups - 1 - g) & (int)0x80000000);
-      const uint32_t sb = past ? 0 : (uint32_t)(rows * groups) * 2;
-      k.s[n] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.scale + fr * groups, sb), off, 0, 0);
+      const int off = ((scale_off + g0 + n * 8) * 2) |
+                      ((groups - 1 - g0 - n * 8 - (ul & 7)) & (int)0x80000000);
+      k.s[n] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.scale + scales, sb), off, 0, 0);
       if constexpr (Z)
-        k.z[n] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.zero + fr * groups, sb), off, 0, 0);
+        k.z[n] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.zero + scales, sb), off, 0, 0);
     }
+    // row i: token i / 2 of the job, the rounded values or the rests
+    const int there = past || ld.t * 16 + (lane & 15) >= nunits ? 0x80000000 : lane * 16;
+    const int second = count > 1 ? there : 0x80000000;
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
-      k.x[w] = __builtin_bit_cast(
-          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(q4_rsrc(a.act, 2 * act_bytes), (int)xo,
-                                                         w * 256, 0));
-    const auto codes = q4_rsrc(a.codes + fr * row_bytes + ld.t * 256,
-                               past ? 0 : rows * row_bytes - ld.t * 256);
+    for (int i = 0; i < 4; ++i)
+      k.x[i] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                       act, i < 2 ? there : second,
+                       act_row + ld.t * 1024 + (i >> 1) * (pitch * 2) + (i & 1) * pairs * (pitch * 2),
+                       0));
+    const auto range = q4_rsrc(codes + ld.t * 256, past ? 0 : rows * row_bytes - ld.t * 256);
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
-      k.w[q] = __builtin_bit_cast(
-          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(codes, (4 * q + r4) * row_bytes + ul * 16, 0,
-                                                         2));
+      k.w[q] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                               range, code_off, 4 * q * row_bytes, 2));
+    const int job = ld.job;
     next(ld);
-    job_n = a.jobs->job[ld.f < f1 ? ld.job : 0];
+    if (ld.job != job && ld.f < f1) enter(ld.job);
   };
   float acc[NQ][4];
 #pragma unroll
@@ -601,14 +644,42 @@ __global__ void __launch_bounds__(kDownWaves* kWave) moe_down_kernel(DownArgs a)
     if (at.f >= f1) return;
     constexpr uint32_t kOne = 0x00400040u, m = 0x03C003C0u;
     const half4_t ones = __builtin_bit_cast(half4_t, u32x2_t{kOne, kOne});
-    float4_t sum = {0, 0, 0, 0};
+    u32x4_t xo[4], wo[NQ];
+    lds_in_order();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *(u32x4_t*)(act_lds + i * kActRow + lane * 16) = k.x[i];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+      *(u32x4_t*)(codes_lds + (4 * q + (lane >> 4)) * kCodesRow + (lane & 15) * 16) = k.w[q];
+    lds_in_order();
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+      wo[q] = *(const u32x4_t*)(codes_lds + (4 * q + r4) * kCodesRow + ul * 16);
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      xo[w] = *(const u32x4_t*)(act_lds + r4 * kActRow + w * 256 + ul * 16);
+    // the sums of x and of each quad's products: chains of their own
+    float4_t sum = {0, 0, 0, 0}, c[NQ];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) c[q] = float4_t{0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const u32x4_t x = k.x[w];
-      sum = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}), ones,
-                                               sum, 0, 0, 0);
-      sum = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}), ones,
-                                               sum, 0, 0, 0);
+      const half4_t x0 = __builtin_bit_cast(half4_t, u32x2_t{xo[w].x, xo[w].y});
+      const half4_t x1 = __builtin_bit_cast(half4_t, u32x2_t{xo[w].z, xo[w].w});
+      sum = __builtin_amdgcn_mfma_f32_4x4x4f16(x0, ones, sum, 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const uint32_t v = wo[q][w];
+        c[q] = __builtin_amdgcn_mfma_f32_4x4x4f16(
+            x0, __builtin_bit_cast(half4_t, u32x2_t{(v << 6) & m, (v >> 2) & m}), c[q], 0, 0, 0);
+      }
+      sum = __builtin_amdgcn_mfma_f32_4x4x4f16(x1, ones, sum, 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const uint32_t v = wo[q][w];
+        c[q] = __builtin_amdgcn_mfma_f32_4x4x4f16(
+            x1, __builtin_bit_cast(half4_t, u32x2_t{(v << 2) & m, (v >> 6) & m}), c[q], 0, 0, 0);
+      }
     }
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
@@ -621,30 +692,16 @@ __global__ void __launch_bounds__(kDownWaves* kWave) moe_down_kernel(DownArgs a)
             ((q * 8 + (rel & 7)) * 4 + r4) * 4, (int)both);
         sz = n == 0 || (rel >> 3) == n ? v : sz;
       }
-      const float z = -f16_to_f32(sz >> 16);
-      float4_t c;
+      const float s = f16_to_f32(sz), z = f16_to_f32(sz >> 16);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) c[b] = z * sum[b];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const u32x4_t x = k.x[w];
-        const uint32_t v = k.w[q][w];
-        c = __builtin_amdgcn_mfma_f32_4x4x4f16(
-            __builtin_bit_cast(half4_t, u32x2_t{x.x, x.y}),
-            __builtin_bit_cast(half4_t, u32x2_t{(v << 6) & m, (v >> 2) & m}), c, 0, 0, 0);
-        c = __builtin_amdgcn_mfma_f32_4x4x4f16(
-            __builtin_bit_cast(half4_t, u32x2_t{x.z, x.w}),
-            __builtin_bit_cast(half4_t, u32x2_t{(v << 2) & m, (v >> 6) & m}), c, 0, 0, 0);
-      }
-      const float s = f16_to_f32(sz);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) acc[q][b] = __builtin_fmaf(s, c[b], acc[q][b]);
+      for (int b = 0; b < 4; ++b)
+        acc[q][b] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[b], c[q][b]), acc[q][b]);
     }
     const int job = at.job;
     next(at);
     if (at.f < f1 && at.t) return;
-    const Job jb = a.jobs->job[job];
-    const float weight = ul < jb.count ? a.jobs->weight[jb.first + ul] : 0.f;
+    const Job jb = job_at(job);
+    const float weight = ul < jb.count ? weights[jb.first + ul] : 0.f;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       const float v0 = sum_blocks(acc[q][0] + acc[q][1]);
@@ -658,15 +715,22 @@ __global__ void __launch_bounds__(kDownWaves* kWave) moe_down_kernel(DownArgs a)
     }
   };
   Step ring[RING];
+  // the loop is entered with a whole ring on its way, as every round of it leaves one: else its
+  // first wait would be for everything
+  if (f1 - f0 >= RING) {
 #pragma unroll
-  for (int d = 0; d < RING; ++d)
-    if (ld.f < f1) load(ring[d]);
-  while (ld.f < f1) {
+    for (int d = 0; d < RING; ++d) load(ring[d]);
+    while (ld.f < f1) {
 #pragma unroll
-    for (int d = 0; d < RING; ++d) {
-      consume(ring[d]);
-      load(ring[d]);
+      for (int d = 0; d < RING; ++d) {
+        consume(ring[d]);
+        load(ring[d]);
+      }
     }
+  } else {
+#pragma unroll
+    for (int d = 0; d < RING - 1; ++d)
+      if (ld.f < f1) load(ring[d]);
   }
 #pragma unroll
   for (int d = 0; d < RING; ++d) consume(ring[d]);
