@@ -412,12 +412,14 @@ def _types(*names):
 _TYPES = {t: code for name, code in (("float32", LVQ_F32), ("float16", LVQ_F16),
                                      ("bfloat16", LVQ_BF16), ("int8", LVQ_I8),
                                      ("float8_e4m3fn", LVQ_E4M3)) for t in _types(name)}
+_FLOAT_TYPES = {t: c for t, c in _TYPES.items() if c <= LVQ_BF16}
 # fp16 bit patterns are also accepted as 16-bit integers, codes as any bytes
 _F16_BITS = _types("float16", "int16", "uint16")
 _BYTES = _types("uint8", "int8")
 _WORDS = _types("int32", "uint32")
 _F32 = _types("float32")
 _INT32 = getattr(_torch, "int32", None)
+_INTS = _types("int32")
 _FLOATS = _types("float32", "float16", "bfloat16")
 _EIGHT = _types("int8", "float8_e4m3fn")
 _OUTS = _types("float16") + _EIGHT
@@ -582,27 +584,50 @@ def q4_moe(x, router, gate_up, down, inner: int, top: int, y, workspace, renorma
     gc, gs, gz, gg = gate_up
     dc, ds, dz, dg = down
     gg, dg = int(gg), int(dg)
-    _in_32_bits(tokens, hidden, inner, experts, top, gg, dg, 2 * experts * max(inner, hidden))
+    rows_gu, rows_down = experts * 2 * inner, experts * hidden
+    if (tokens | hidden | inner | experts | top | gg | dg | rows_gu | rows_down) >> 31:
+        _in_32_bits(tokens, hidden, inner, experts, top, gg, dg, rows_gu, rows_down)
     rp, rt = _typed(router, "router", _FLOATS, experts, hidden, dev)
     n_gu, n_down = _n_groups(hidden, gg), _n_groups(inner, dg)
-    rows_gu, rows_down = experts * 2 * inner, experts * hidden
+    u_gu, u_down = -(-hidden // 32) * 16, -(-inner // 32) * 16
     e = _lib.q4_moe(_array(x, "x", _F16_BITS, tokens, hidden, dev), tokens, hidden, rp, rt, experts,
-                    top, 1 if renormalize else 0, _codes(gc, rows_gu, -(-hidden // 32), dev),
-                    _array(gs, "scale", _F16_BITS, rows_gu, n_gu, dev),
-                    _array(gz, "zero", _F16_BITS, rows_gu, n_gu, dev), gg,
-                    _codes(dc, rows_down, -(-inner // 32), dev),
-                    _array(ds, "scale", _F16_BITS, rows_down, n_down, dev),
-                    _array(dz, "zero", _F16_BITS, rows_down, n_down, dev), dg, inner,
+                    top, 1 if renormalize else 0,
+                    _matrices(gc, "codes", _BYTES, experts, 2 * inner, u_gu, dev),
+                    _matrices(gs, "scale", _F16_BITS, experts, 2 * inner, n_gu, dev),
+                    _matrices(gz, "zero", _F16_BITS, experts, 2 * inner, n_gu, dev), gg,
+                    _matrices(dc, "codes", _BYTES, experts, hidden, u_down, dev),
+                    _matrices(ds, "scale", _F16_BITS, experts, hidden, n_down, dev),
+                    _matrices(dz, "zero", _F16_BITS, experts, hidden, n_down, dev), dg, inner,
                     _array(y, "y", _F32, tokens, hidden, dev),
-                    _array(ids, "ids", _types("int32"), tokens, top, dev),
+                    None if ids is None else _array(ids, "ids", _INTS, tokens, top, dev),
                     _array(weights, "weights", _F32, tokens, top, dev),
                     *_space(workspace, dev), stream)
     if e:
         _check(e)
 
 
+def _matrices(t, name, types, experts, rows, width, dev):
+    """_array() of the experts' matrices, `rows` rows each; codes as 32-bit words too."""
+    if t is None:
+        return None
+    try:
+        if (t.dtype in types and t.shape == (experts, rows, width) and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+        if types is _BYTES and t.dtype in _WORDS:
+            return _array(t, name, _WORDS, experts * rows, width // 4, dev)
+    except AttributeError:
+        pass
+    return _array(t, name, types, experts * rows, width, dev)
+
+
 def _space(t, dev):
     """(address, bytes) of a workspace, a contiguous tensor of bytes."""
+    try:
+        if t.dtype in _BYTES and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr(), t.numel()
+    except AttributeError:
+        pass
     if not isinstance(t, _Tensor):
         _refuse(t, "workspace", _BYTES, 0, 0, dev)
     n = t.numel()
@@ -612,6 +637,14 @@ def _space(t, dev):
 def _rows_of(t, name, dev):
     """(address, type, rows, cols, row stride) of a 2-D tensor of floats whose
     columns are adjacent."""
+    try:
+        # the usual case first, in as few of torch's calls as it takes
+        kind = _FLOAT_TYPES[t.dtype]
+        (rows, cols), (stride, step) = t.shape, t.stride()
+        if step == 1 and rows > 0 and t.get_device() == dev:
+            return t.data_ptr(), kind, rows, cols, stride if rows > 1 else cols
+    except (AttributeError, KeyError, TypeError, ValueError):
+        pass
     if not isinstance(t, _Tensor) or t.dtype not in _FLOATS or t.get_device() != dev:
         _refuse(t, name, _FLOATS, 0, 0, dev)
     shape, strides = t.shape, t.stride()
@@ -764,8 +797,7 @@ def kv_cache(pool, table, kv_heads: int, dim: int, page: int, group: int = 0) ->
 def _index(t, name, n, dev):
     """Address of a contiguous int32 tensor of n values, one for each token or sequence."""
     try:
-        if (t.dtype is _INT32 and t.get_device() == dev and t.shape == (n,)
-                and t.is_contiguous()):
+        if t.dtype is _INT32 and t.shape == (n,) and t.get_device() == dev and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
@@ -797,14 +829,14 @@ def kv_append(cache: KvCache, k, v, pos, seq=None, cos=None, sin=None, interleav
     rot = positions = heads = qstride = 0
     qot = LVQ_F16
     if cos is not None or sin is not None:
-        if cos is None or sin is None or len(cos.shape) != 2:
-            raise ValueError("cos and sin go together, of two dimensions")
+        if cos is None or sin is None or len(cos.shape) != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin go together, of two dimensions and one shape")
         positions, half = cos.shape
         rot = 2 * half
-        if positions >> 31 or rot >> 31:
+        if (positions | rot) >> 31:
             _in_32_bits(positions, rot)
-        cp = _same(cos, "cos", _F32, positions, half, dev)
-        sp = _same(sin, "sin", _F32, positions, half, dev)
+        cp = _array(cos, "cos", _F32, positions, half, dev)
+        sp = _array(sin, "sin", _F32, positions, half, dev)
     if q is not None or q_out is not None:
         if q is None or q_out is None:
             raise ValueError("q and q_out go together")
@@ -819,13 +851,6 @@ def kv_append(cache: KvCache, k, v, pos, seq=None, cos=None, sin=None, interleav
                            1 if interleaved else 0, qp, qstride, heads, qop, qot, stream)
     if e:
         _check(e)
-
-
-def _same(t, name, types, rows, width, dev):
-    """Address of a contiguous tensor of exactly this shape."""
-    if isinstance(t, _Tensor) and t.shape == (rows, width):
-        return _array(t, name, types, rows, width, dev)
-    _refuse(t, name, types, rows, width, dev)
 
 
 def kv_read(cache: KvCache, pos, k_out, v_out, seq=None, stream=None):

@@ -106,23 +106,28 @@ __host__ __device__ inline uint32_t q_workgroups(int tokens, int heads, int dim)
   return (q_threads(tokens, heads, dim) + n - 1) / n;
 }
 
-// Angles 8 u .. 8 u + 7 of a position.
+// Angles 8 u .. 8 u + 7 of a position (of a position past the table: of its last or none).
+__device__ __forceinline__ size_t angle_row(const AppendArgs& a, int pos) {
+  const int p = pos < 0 ? 0 : pos < a.positions ? pos : a.positions - 1;
+  return (size_t)p * (a.rot / 2);
+}
 __device__ __forceinline__ void angles(const AppendArgs& a, int pos, int u, float (&c)[8],
                                        float (&s)[8]) {
-  const size_t at = (size_t)pos * (a.rot / 2) + 8 * u;
+  if (a.positions == 0) return;
+  const size_t at = angle_row(a, pos) + 8 * u;
   __builtin_memcpy(c, a.cos + at, 32);
   __builtin_memcpy(s, a.sin + at, 32);
 }
 
-// Sequence and position of a token; false where it is to be left out.
-__device__ __forceinline__ bool token_at(const AppendArgs& a, int token, int* seq, int* pos,
-                                         int* page) {
-  if (token < 0 || token >= a.tokens) return false;
-  *seq = a.seq ? a.seq[token] : token;
-  *pos = a.pos[token];
-  if (a.rot && *pos >= a.positions) return false;
-  *page = kv_page(a.c, *seq, *pos);
-  return *page >= 0;
+// Sequence and position of a token, and its page; -1 where it is to be left out.
+struct Where {
+  int seq, pos;
+};
+__device__ __forceinline__ Where ask(const AppendArgs& a, int token) {
+  return {a.seq ? a.seq[token] : token, a.pos[token]};
+}
+__device__ __forceinline__ int find(const AppendArgs& a, Where w) {
+  return a.rot && w.pos >= a.positions ? -1 : kv_page(a.c, w.seq, w.pos);
 }
 
 // q: a thread turns 16 channels of a head, two chunks of eight that belong together.
@@ -130,8 +135,9 @@ __device__ __forceinline__ void rotate_q(const AppendArgs& a) {
   const uint32_t per_head = a.c.dim / 16, per = a.heads * per_head;
   const uint32_t i = blockIdx.x * (uint32_t)append_threads(a.c.dim) + threadIdx.x;
   const int token = (int)(i / per);
-  int seq, pos, page;
-  if (!token_at(a, token, &seq, &pos, &page)) return;
+  if (token >= a.tokens) return;
+  // the place and the values are asked for together, then the angles and the page
+  const Where at = ask(a, token);
   const uint32_t r = i - token * per;
   const int head = (int)(r / per_head), u = (int)(r - head * per_head);
   const bool turned = u * 16 < a.rot;
@@ -141,12 +147,13 @@ __device__ __forceinline__ void rotate_q(const AppendArgs& a) {
   const int c1 = halves ? c0 + a.rot / 2 : c0 + 8;
   const uint8_t* row = (const uint8_t*)a.q + (int64_t)token * a.q_stride * (a.type == LVQ_F32 ? 4 : 2);
   const Raw8 r0 = raw8(row, a.type, c0), r1 = raw8(row, a.type, c1);
+  float c[8], s[8];
+  if (turned) angles(a, at.pos, u, c, s);
+  if (find(a, at) < 0) return;
   float x[8], y[8];
   widen(r0, a.type, x);
   widen(r1, a.type, y);
   if (turned) {
-    float c[8], s[8];
-    angles(a, pos, u, c, s);
     if (halves) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -231,42 +238,49 @@ __device__ __forceinline__ void store_kv(const AppendArgs& a, int block, uint8_t
   // long run of positions are whole blocks
   const int shift = a.tokens > kBlockTokens ? a.pos[0] & (kBlockTokens - 1) : 0;
   const int token = t * kBlockTokens - shift + i;
-  int seq = 0, pos = 0, page = -1;
-  // with 64 channels half of the threads have no token
-  const bool there = i < kBlockTokens && token_at(a, token, &seq, &pos, &page);
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = 0.f;
   const int e = 8 * lane;
-  if (there) {
+  int pos = 0, page = -1;
+  // with 64 channels half of the threads have no token
+  if (i < kBlockTokens && token >= 0 && token < a.tokens) {
+    const Where where = ask(a, token);
+    pos = where.pos;
     const int64_t step = (int64_t)token * (a.type == LVQ_F32 ? 4 : 2);
     const uint8_t* row = values ? (const uint8_t*)a.v + step * a.v_stride
                                 : (const uint8_t*)a.k + step * a.k_stride;
-    widen(raw8(row, a.type, head * dim + e), a.type, v);
-    if (!values && e < a.rot) {
-      float c[8], s[8];
-      if (a.style == kHalves) {
-        const bool first = e < a.rot / 2;
-        float o[8];
-        widen(raw8(row, a.type, head * dim + (first ? e + a.rot / 2 : e - a.rot / 2)), a.type, o);
-        angles(a, pos, (first ? e : e - a.rot / 2) / 8, c, s);
+    const bool turned = !values && e < a.rot, halves = a.style == kHalves;
+    const bool first = e < a.rot / 2;  // of the two halves
+    const int partner = turned && halves ? (first ? e + a.rot / 2 : e - a.rot / 2) : e;
+    const Raw8 own = raw8(row, a.type, head * dim + e);
+    const Raw8 other = raw8(row, a.type, head * dim + partner);
+    float c[8], s[8], o[8];
+    if (turned && halves) {
+      angles(a, pos, (first ? e : partner) / 8, c, s);
+    } else if (turned && a.positions) {
+      const size_t at = angle_row(a, pos) + e / 2;
+      __builtin_memcpy(c, a.cos + at, 16);
+      __builtin_memcpy(s, a.sin + at, 16);
+    }
+    page = find(a, where);
+    widen(own, a.type, v);
+    if (turned && halves) {
+      widen(other, a.type, o);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[j] = first ? minus_products(v[j], c[j], o[j], s[j])
-                       : plus_products(v[j], c[j], o[j], s[j]);
-      } else {
-        const size_t at = (size_t)pos * (a.rot / 2) + e / 2;
-        __builtin_memcpy(c, a.cos + at, 16);
-        __builtin_memcpy(s, a.sin + at, 16);
+      for (int j = 0; j < 8; ++j)
+        v[j] = first ? minus_products(v[j], c[j], o[j], s[j])
+                     : plus_products(v[j], c[j], o[j], s[j]);
+    } else if (turned) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float p = v[2 * j], q = v[2 * j + 1];
-          v[2 * j] = minus_products(p, c[j], q, s[j]);
-          v[2 * j + 1] = plus_products(q, c[j], p, s[j]);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float p = v[2 * j], q = v[2 * j + 1];
+        v[2 * j] = minus_products(p, c[j], q, s[j]);
+        v[2 * j + 1] = plus_products(q, c[j], p, s[j]);
       }
     }
   }
+  const bool there = page >= 0;
   int code[8];
   const int per_group = lanes / a.c.groups;
   const uint32_t meta = to_codes(v, per_group, code);
@@ -332,49 +346,67 @@ struct ReadArgs {
   uint8_t type;
 };
 
-// A thread reads eight channels of a token's head, of the keys and of the values.
-__global__ void __launch_bounds__(256) kv_read_kernel(ReadArgs a) {
-  const uint32_t lanes = a.c.dim / 8, per = a.c.kv_heads * lanes;
-  const uint32_t n = blockIdx.x * 256 + threadIdx.x;
-  const int token = (int)(n / per);
-  if (token >= a.tokens) return;
-  const uint32_t r = n - token * per;
-  const int head = (int)(r / lanes), lane = (int)(r - head * lanes);
-  const int seq = a.seq ? a.seq[token] : token, pos = a.pos[token];
-  const int page = kv_page(a.c, seq, pos);
-  const int dim = a.c.dim, in = pos & (kBlockTokens - 1);
-  const int group = lane / (lanes / a.c.groups);
-  const uint8_t* at = page < 0 ? nullptr : kv_block(a.c, page, head, pos);
-  const size_t row = (size_t)token * a.c.kv_heads * dim * (a.type == LVQ_F32 ? 4 : 2);
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    void* out = which ? a.v_out : a.k_out;
-    if (!out) continue;
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-    if (at) {
-      const uint32_t m =
-          *(const uint32_t*)(at + 16 * dim + which * 64 * a.c.groups + 64 * group + 4 * in);
-      const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)m);
-      const float l = (float)__builtin_bit_cast(_Float16, (uint16_t)(m >> 16));
-      uint32_t w = 0;
-      if (which == 0)
-        w = *(const uint32_t*)(at + in * (dim / 2) + (lane & 3) * (dim / 8) + (lane >> 2) * 4);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t c;
-        if (which == 0) {
-          c = (w >> (4 * (j / 2) + 16 * (j % 2))) & 15;
-        } else {
-          const int pair = 16 * (lane >> 2) + 8 * (lane & 1) + j;
-          c = (at[8 * dim + pair * kBlockTokens + in] >> (lane & 2 ? 4 : 0)) & 15;
-        }
-        v[j] = rounded(__builtin_fmaf((float)c, s, l));
-      }
-    }
-    store8((uint8_t*)out + row, a.type, head * dim + 8 * lane, v);
+// Keys or values of one head of 16 tokens, eight channels per thread.  The values of a
+// whole block come in as it lies and are turned in LDS; of others, byte by byte.
+__global__ void __launch_bounds__(512) kv_read_kernel(ReadArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kBlockTokens];
+  __shared__ uint64_t block0;
+  const int dim = a.c.dim, lanes = dim / 8;
+  const int per_tile = a.c.kv_heads * (a.k_out && a.v_out ? 2 : 1);
+  const int t = blockIdx.x / per_tile, which = blockIdx.x - t * per_tile;
+  const bool values = !a.k_out || which >= a.c.kv_heads;
+  const int head = a.k_out && values ? which - a.c.kv_heads : which;
+  const int i = threadIdx.x / lanes, lane = threadIdx.x - i * lanes;
+  // tiles begin where the first token's block begins, as where they are stored
+  const int shift = a.tokens > kBlockTokens ? a.pos[0] & (kBlockTokens - 1) : 0;
+  const int token = t * kBlockTokens - shift + i;
+  const bool mine = i < kBlockTokens && token >= 0 && token < a.tokens;
+  int pos = 0, page = -1;
+  if (mine) {
+    pos = a.pos[token];
+    page = kv_page(a.c, a.seq ? a.seq[token] : token, pos);
   }
+  const bool there = page >= 0;
+  const int in = pos & (kBlockTokens - 1), group = lane / (lanes / a.c.groups);
+  const uint8_t* at = there ? kv_block(a.c, page, head, pos) : nullptr;
+  uint32_t m = 0, code[8];
+  if (there)
+    m = *(const uint32_t*)(at + 16 * dim + (values ? 64 * a.c.groups : 0) + 64 * group + 4 * in);
+  if (!values) {
+    uint32_t w = 0;
+    if (there) w = *(const uint32_t*)(at + in * (dim / 2) + (lane & 3) * (dim / 8) + (lane >> 2) * 4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) code[j] = (w >> (4 * (j / 2) + 16 * (j % 2))) & 15;
+  } else {
+    if (threadIdx.x == 0) block0 = (uint64_t)at;
+    __syncthreads();
+    const bool whole =
+        __syncthreads_and(i >= kBlockTokens || (there && in == i && (uint64_t)at == block0));
+    if (whole) {
+      if ((int)threadIdx.x < dim / 2)
+        ((uint4*)tile)[threadIdx.x] =
+            *(const uint4*)((const uint8_t*)block0 + 8 * dim + threadIdx.x * 16);
+      __syncthreads();
+    }
+    const uint8_t* from = at + 8 * dim;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int pair = 16 * (lane >> 2) + 8 * (lane & 1) + j;
+      uint32_t b = 0;
+      if (whole) b = i < kBlockTokens ? tile[pair * kBlockTokens + in] : 0;
+      else if (there) b = from[pair * kBlockTokens + in];
+      code[j] = (b >> (lane & 2 ? 4 : 0)) & 15;
+    }
+  }
+  if (!mine) return;
+  const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)m);
+  const float l = (float)__builtin_bit_cast(_Float16, (uint16_t)(m >> 16));
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = there ? rounded(__builtin_fmaf((float)code[j], s, l)) : 0.f;
+  uint8_t* out = (uint8_t*)(values ? a.v_out : a.k_out) +
+                 (size_t)token * a.c.kv_heads * dim * (a.type == LVQ_F32 ? 4 : 2);
+  store8(out, a.type, head * dim + 8 * lane, v);
 }
 
 // ---------------------------------------------------------------- checks
@@ -501,9 +533,11 @@ extern "C" int lvq_kv_read(const lvq_kv_cache* cache, const int32_t* seq, const 
   if (ranges_overlap(k_out, n, v_out, n)) return LVQ_E_SHAPE;
   a.seq = seq, a.pos = pos, a.k_out = k_out, a.v_out = v_out;
   a.tokens = tokens, a.type = (uint8_t)out_type;
-  const long long wgs = ((long long)tokens * cache->kv_heads * (cache->dim / 8) + 255) / 256;
-  if (wgs >= INT32_MAX / 256) return LVQ_E_SHAPE;  // threads are counted in 32 bits
+  const long long tiles = (tokens + kBlockTokens - 1LL) / kBlockTokens + (tokens > kBlockTokens);
+  const long long wgs = tiles * cache->kv_heads * (k_out && v_out ? 2 : 1);
+  if (wgs >= INT32_MAX / 4) return LVQ_E_SHAPE;
   clear_hip_error();
-  hipLaunchKernelGGL(kv_read_kernel, dim3((unsigned)wgs), dim3(256), 0, (hipStream_t)stream, a);
+  hipLaunchKernelGGL(kv_read_kernel, dim3((unsigned)wgs), dim3(append_threads(cache->dim)), 0,
+                     (hipStream_t)stream, a);
   return launch_status();
 }
