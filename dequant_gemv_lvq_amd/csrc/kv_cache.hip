@@ -96,7 +96,7 @@ struct AppendArgs {
 };
 
 // Threads of a workgroup: 16 tokens of dim / 8 lanes, four waves at least.
-__host__ __device__ inline int append_threads(int dim) { return dim <= 128 ? 256 : 2 * dim; }
+__host__ __device__ constexpr int append_threads(int dim) { return dim <= 128 ? 256 : 2 * dim; }
 // Threads that rotate q, 16 channels each.
 __host__ __device__ inline uint32_t q_threads(int tokens, int heads, int dim) {
   return (uint32_t)tokens * heads * (dim / 16);
@@ -131,17 +131,23 @@ __device__ __forceinline__ int find(const AppendArgs& a, Where w) {
 }
 
 // q: a thread turns 16 channels of a head, two chunks of eight that belong together.
+template <int DIM>
 __device__ __forceinline__ void rotate_q(const AppendArgs& a) {
-  const uint32_t per_head = a.c.dim / 16, per = a.heads * per_head;
-  const uint32_t i = blockIdx.x * (uint32_t)append_threads(a.c.dim) + threadIdx.x;
-  const int token = (int)(i / per);
+  constexpr uint32_t kPerHead = DIM / 16;
+  const uint32_t per = a.heads * kPerHead;
+  // the workgroup's first token by a division, the thread's from there: below 2^20 a float's
+  // quotient of whole numbers, half a unit off the borders, is never off
+  const uint32_t first = blockIdx.x * (uint32_t)append_threads(DIM), token0 = first / per;
+  const uint32_t in = first - token0 * per + threadIdx.x;
+  const uint32_t more = (uint32_t)(((float)in + 0.5f) * (1.f / (float)per));
+  const int token = (int)(token0 + more);
   if (token >= a.tokens) return;
   // the place and the values are asked for together, then the angles and the page
   const Where at = ask(a, token);
-  const uint32_t r = i - token * per;
-  const int head = (int)(r / per_head), u = (int)(r - head * per_head);
+  const uint32_t r = in - more * per;
+  const int head = (int)(r / kPerHead), u = (int)(r % kPerHead);
   const bool turned = u * 16 < a.rot;
-  const int base = head * a.c.dim;
+  const int base = head * DIM;
   const bool halves = turned && a.style == kHalves;
   const int c0 = base + (halves ? 8 * u : 16 * u);
   const int c1 = halves ? c0 + a.rot / 2 : c0 + 8;
@@ -174,7 +180,7 @@ __device__ __forceinline__ void rotate_q(const AppendArgs& a) {
     }
   }
   uint8_t* out = (uint8_t*)a.q_out +
-                 (size_t)token * a.heads * a.c.dim * (a.q_type == LVQ_F32 ? 4 : 2);
+                 (size_t)token * a.heads * DIM * (a.q_type == LVQ_F32 ? 4 : 2);
   store8(out, a.q_type, c0, x);
   store8(out, a.q_type, c1, y);
 }
@@ -195,40 +201,40 @@ __device__ __forceinline__ float lanes_min(float v, int lanes) {
   return v;
 }
 
-// Eight values of a group spread over `lanes` lanes -> eight codes, and the group's
-// scale and low end (fp16 bits, scale in the low half).
-__device__ __forceinline__ uint32_t to_codes(const float (&v)[8], int lanes, int (&code)[8]) {
+// Eight values of a group spread over `lanes` lanes -> eight codes, each plus kCodeBias, and
+// the group's scale and low end (fp16 bits, scale in the low half).  A NaN makes the
+// smallest value minus infinity; with an infinity the scale is infinite, and reads as NaN.
+constexpr uint32_t kCodeBias = 0x4B400000u;  // 1.5 * 2^23: a sum with it is rounded to a whole number
+__device__ __forceinline__ uint32_t to_codes(const float (&v)[8], int lanes, uint32_t (&code)[8]) {
 #pragma clang fp contract(off)
-  float least = v[0], most = v[0];
-  bool bad = false;
+  float least = v[0], most = v[0], sum = v[0];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 1; i < 8; ++i) {
     least = fminf(least, v[i]);
     most = fmaxf(most, v[i]);
-    bad |= !(fabsf(v[i]) < __builtin_inff());
+    sum += v[i];
   }
-  // an infinity or a NaN: the group's low end is NaN
-  float worst = bad ? -1.f : 0.f;
+  if (sum != sum) least = -__builtin_inff();
   least = lanes_min(least, lanes);
   most = -lanes_min(-most, lanes);
-  worst = lanes_min(worst, lanes);
   const _Float16 s = (_Float16)rounded((most - least) * (1.f / 15.f));
-  const _Float16 l = worst < 0.f ? (_Float16)__builtin_nanf("") : (_Float16)least;
+  const _Float16 l = (_Float16)least;
   const float sf = (float)s, lf = (float)l;
-  const float per = sf > 0.f && worst == 0.f ? 1.f / sf : 0.f;
+  const float per = sf > 0.f ? 1.f / sf : 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float d = v[i] - lf;
-    const float t = __builtin_rintf(d * per);
-    code[i] = (int)fminf(fmaxf(t, 0.f), 15.f);
+    const float d = rounded((v[i] - lf) * per);
+    code[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_fmed3f(d, 0.f, 15.f) +
+                                               __builtin_bit_cast(float, kCodeBias));
   }
   return (uint32_t)__builtin_bit_cast(uint16_t, s) |
          (uint32_t)__builtin_bit_cast(uint16_t, l) << 16;
 }
 
 // Keys or values of one head of 16 tokens: dim / 8 lanes per token, eight channels each.
+template <int DIM>
 __device__ __forceinline__ void store_kv(const AppendArgs& a, int block, uint8_t* tile) {
-  const int dim = a.c.dim, lanes = dim / 8;
+  constexpr int dim = DIM, lanes = dim / 8;
   const int per_tile = 2 * a.c.kv_heads;
   const int t = block / per_tile, which = block - t * per_tile;
   const bool values = which >= a.c.kv_heads;
@@ -281,19 +287,19 @@ __device__ __forceinline__ void store_kv(const AppendArgs& a, int block, uint8_t
     }
   }
   const bool there = page >= 0;
-  int code[8];
-  const int per_group = lanes / a.c.groups;
-  const uint32_t meta = to_codes(v, per_group, code);
+  uint32_t code[8];
+  const int group_shift = __builtin_ctz(lanes) - __builtin_ctz(a.c.groups);
+  const uint32_t meta = to_codes(v, 1 << group_shift, code);
   const int in = pos & (kBlockTokens - 1);
   uint8_t* at = there ? kv_block(a.c, page, head, pos) : nullptr;
-  if (there && lane % per_group == 0)
-    *(uint32_t*)(at + 16 * dim + (values ? 64 * a.c.groups : 0) + 64 * (lane / per_group) +
+  if (there && (lane & ((1 << group_shift) - 1)) == 0)
+    *(uint32_t*)(at + 16 * dim + (values ? 64 * a.c.groups : 0) + 64 * (lane >> group_shift) +
                  4 * in) = meta;
   if (!values) {
     // channel 8 lane + j is field j/2 + 4 (j%2) of word lane/4 of quarter lane%4
-    uint32_t w = 0;
+    uint32_t w = 0;  // modulo 2^32 the biases are one constant
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w |= (uint32_t)code[j] << (4 * (j / 2) + 16 * (j % 2));
+    for (int j = 0; j < 8; ++j) w += (code[j] - kCodeBias) << (4 * (j / 2) + 16 * (j % 2));
     if (there) *(uint32_t*)(at + in * (dim / 2) + (lane & 3) * (dim / 8) + (lane >> 2) * 4) = w;
     return;
   }
@@ -302,8 +308,8 @@ __device__ __forceinline__ void store_kv(const AppendArgs& a, int block, uint8_t
   uint32_t lo = 0, hi = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    lo |= (uint32_t)code[j] << (8 * j);
-    hi |= (uint32_t)code[4 + j] << (8 * j);
+    lo += (code[j] - kCodeBias) << (8 * j);
+    hi += (code[4 + j] - kCodeBias) << (8 * j);
   }
   const uint32_t other_lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)lo, 0x4E, 0xF, 0xF, false);
   const uint32_t other_hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)hi, 0x4E, 0xF, 0xF, false);
@@ -329,11 +335,12 @@ __device__ __forceinline__ void store_kv(const AppendArgs& a, int block, uint8_t
   }
 }
 
-__global__ void __launch_bounds__(512) kv_append_kernel(AppendArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kBlockTokens];
-  const uint32_t rotating = q_workgroups(a.tokens, a.heads, a.c.dim);
-  if (blockIdx.x < rotating) rotate_q(a);
-  else store_kv(a, (int)(blockIdx.x - rotating), tile);
+template <int DIM>
+__global__ void __launch_bounds__(append_threads(DIM)) kv_append_kernel(AppendArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t tile[DIM / 2 * kBlockTokens];
+  const uint32_t rotating = q_workgroups(a.tokens, a.heads, DIM);
+  if (blockIdx.x < rotating) rotate_q<DIM>(a);
+  else store_kv<DIM>(a, (int)(blockIdx.x - rotating), tile);
 }
 
 // ---------------------------------------------------------------- reading back
@@ -348,10 +355,11 @@ struct ReadArgs {
 
 // Keys or values of one head of 16 tokens, eight channels per thread.  The values of a
 // whole block come in as it lies and are turned in LDS; of others, byte by byte.
-__global__ void __launch_bounds__(512) kv_read_kernel(ReadArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kBlockTokens];
+template <int DIM>
+__global__ void __launch_bounds__(append_threads(DIM)) kv_read_kernel(ReadArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t tile[DIM / 2 * kBlockTokens];
   __shared__ uint64_t block0;
-  const int dim = a.c.dim, lanes = dim / 8;
+  constexpr int dim = DIM, lanes = dim / 8;
   const int per_tile = a.c.kv_heads * (a.k_out && a.v_out ? 2 : 1);
   const int t = blockIdx.x / per_tile, which = blockIdx.x - t * per_tile;
   const bool values = !a.k_out || which >= a.c.kv_heads;
@@ -367,7 +375,7 @@ __global__ void __launch_bounds__(512) kv_read_kernel(ReadArgs a) {
     page = kv_page(a.c, a.seq ? a.seq[token] : token, pos);
   }
   const bool there = page >= 0;
-  const int in = pos & (kBlockTokens - 1), group = lane / (lanes / a.c.groups);
+  const int in = pos & (kBlockTokens - 1), group = lane >> (__builtin_ctz(lanes) - __builtin_ctz(a.c.groups));
   const uint8_t* at = there ? kv_block(a.c, page, head, pos) : nullptr;
   uint32_t m = 0, code[8];
   if (there)
@@ -507,8 +515,11 @@ extern "C" int lvq_kv_append(const lvq_kv_cache* cache, const void* k, int64_t k
     return LVQ_E_SHAPE;
   const unsigned all = q_workgroups(tokens, heads, dim) + (unsigned)(tiles * 2 * cache->kv_heads);
   clear_hip_error();
-  hipLaunchKernelGGL(kv_append_kernel, dim3(all), dim3(append_threads(dim)), 0,
-                     (hipStream_t)stream, a);
+  const dim3 grid(all), threads(append_threads(dim));
+  hipStream_t st = (hipStream_t)stream;
+  if (dim == 64) hipLaunchKernelGGL(kv_append_kernel<64>, grid, threads, 0, st, a);
+  else if (dim == 128) hipLaunchKernelGGL(kv_append_kernel<128>, grid, threads, 0, st, a);
+  else hipLaunchKernelGGL(kv_append_kernel<256>, grid, threads, 0, st, a);
   return launch_status();
 }
 
@@ -537,7 +548,10 @@ extern "C" int lvq_kv_read(const lvq_kv_cache* cache, const int32_t* seq, const 
   const long long wgs = tiles * cache->kv_heads * (k_out && v_out ? 2 : 1);
   if (wgs >= INT32_MAX / 4) return LVQ_E_SHAPE;
   clear_hip_error();
-  hipLaunchKernelGGL(kv_read_kernel, dim3((unsigned)wgs), dim3(append_threads(cache->dim)), 0,
-                     (hipStream_t)stream, a);
+  const dim3 grid((unsigned)wgs), threads(append_threads(cache->dim));
+  hipStream_t st = (hipStream_t)stream;
+  if (cache->dim == 64) hipLaunchKernelGGL(kv_read_kernel<64>, grid, threads, 0, st, a);
+  else if (cache->dim == 128) hipLaunchKernelGGL(kv_read_kernel<128>, grid, threads, 0, st, a);
+  else hipLaunchKernelGGL(kv_read_kernel<256>, grid, threads, 0, st, a);
   return launch_status();
 }
