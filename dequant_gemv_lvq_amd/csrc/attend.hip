@@ -32,7 +32,9 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kAttWaves = 4;
+constexpr int kAttWaves = 4;    // of a workgroup, more where that saves the second launch
+constexpr int kAttMostWaves = 8;
+constexpr int kAttWhole = 8;    // blocks of a sequence that eight waves take alone
 constexpr int kAttTokens = 64;  // of a wave at a time
 constexpr uint32_t kCodeMask = 0x03C003C0u;
 constexpr float kCodeUnit = 0x1p18f;
@@ -48,7 +50,7 @@ struct AttArgs {
   float scale;    // of the logits, in powers of two
   int window, splits;
   uint16_t tiles;  // of rows
-  uint8_t q_type, out_type;
+  uint8_t q_type, out_type, waves;
 };
 static_assert(sizeof(AttArgs) < 128, "launches of 128 bytes and more are slower");
 
@@ -60,7 +62,7 @@ struct Span {
   int first, last, parts, len;
 };
 __device__ __forceinline__ Span att_span(const KvPages& c, int len, int queries, int window,
-                                         int splits) {
+                                         int splits, int waves) {
   Span s;
   const int most = c.pages ? c.max_pages << c.page_shift : 0;
   s.len = len < 0 ? 0 : len > most ? most : len;
@@ -71,7 +73,7 @@ __device__ __forceinline__ Span att_span(const KvPages& c, int len, int queries,
   }
   s.first = first;
   s.last = (s.len + kAttTokens - 1) / kAttTokens;
-  const int parts = (s.last - s.first + kAttWaves - 1) / kAttWaves;
+  const int parts = (s.last - s.first + waves - 1) / waves;
   s.parts = parts < 1 ? 1 : parts < splits ? parts : splits;
   return s;
 }
@@ -159,29 +161,37 @@ constexpr int att_wave_bytes(int RT, int dim, int groups) {
   return a > b ? a : b;
 }
 
+// Waves of a workgroup at most, as the registers allow.
+constexpr int att_most_waves(int dim, int groups) {
+  return dim == 256 && groups > 2 ? kAttWaves : kAttMostWaves;
+}
+
 // Waves of a SIMD that the registers are to leave room for.
 constexpr int att_waves(int dim, int groups) {
   return dim == 64 || (dim == 128 && groups == 1) ? 3 : dim == 128 || groups <= 2 ? 2 : 1;
 }
 
 template <int DIM, int RT, int NG>
-__global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_kernel(AttArgs a) {
+__global__ void __launch_bounds__(att_most_waves(DIM, NG) * kWave, att_waves(DIM, NG))
+    attend_kernel(AttArgs a) {
   constexpr int KS = DIM / 32;       // steps of 32 channels
   constexpr int GS = KS / NG;        // of a group
   constexpr int NT = RT / 4;         // products (of four tokens a lane) that a lane keeps
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kAttWaves][att_wave_bytes(RT, DIM, NG)];
+  constexpr int kLds = att_wave_bytes(RT, DIM, NG), kPart = att_part_bytes(RT, DIM);
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int nw = a.waves;
   const int lane = threadIdx.x & (kWave - 1), t16 = lane & 15, quarter = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int seq = blockIdx.z, part = blockIdx.y;
   const int head = blockIdx.x / a.tiles, tile = blockIdx.x - head * a.tiles;
   const int per = a.heads / a.c.kv_heads, rows = per * a.queries;
   const int row0 = tile * 16;
-  const int stride = kAttWaves * a.splits;
+  const int stride = nw * a.splits;
   const int len = a.lens[seq];
-  int b = part * kAttWaves + wv;
-  if (a.window > 0) b += att_span(a.c, len, a.queries, a.window, a.splits).first;
+  int b = part * nw + wv;
+  if (a.window > 0) b += att_span(a.c, len, a.queries, a.window, a.splits, a.waves).first;
 
-  uint8_t* const lds = smem[wv];
+  uint8_t* const lds = smem + wv * kLds;
   const int64_t page_size = kv_page_size(a.c);
   constexpr int kBlock = kv_block_bytes(DIM, NG);
   const int blocks_mask = (1 << (a.c.page_shift - 4)) - 1;
@@ -229,7 +239,7 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
     key_page = page_of(b, kblk), page = page_of(b, quarter);
     key_page_n = page_of(bn, kblk), page_n = page_of(bn, quarter);
   }
-  const Span sp = att_span(a.c, len, a.queries, a.window, a.splits);
+  const Span sp = att_span(a.c, len, a.queries, a.window, a.splits, a.waves);
   if (part >= sp.parts) return;
   const int b1 = sp.last;
   // the loads of the loop are one sequence without branches, so that each wait counts
@@ -519,21 +529,33 @@ __global__ void __launch_bounds__(kAttWaves* kWave, att_waves(DIM, NG)) attend_k
   __syncthreads();
 
   // ---- the workgroup's: four channels of a row per thread
-  for (int at4 = threadIdx.x; at4 < RT * (DIM / 4); at4 += kAttWaves * kWave) {
+  for (int at4 = threadIdx.x; at4 < RT * (DIM / 4); at4 += nw * kWave) {
     const int r = at4 / (DIM / 4), c = (at4 - r * (DIM / 4)) * 4;
     if (row0 + r >= rows) break;
-    float most = -__builtin_inff();
-#pragma unroll
-    for (int w = 0; w < kAttWaves; ++w)
-      most = fmaxf(most, ((float*)(smem[w] + att_part_bytes(RT, DIM)))[r]);
-    float sum = 0.f;
+    float most = -__builtin_inff(), sum = 0.f;
     f32x4_t v = {0, 0, 0, 0};
+    // four waves at a time, all their values asked for at once
+    for (int w0 = 0; w0 < nw; w0 += kAttWaves) {
+      float mw[kAttWaves], lw[kAttWaves];
+      f32x4_t ow[kAttWaves];
 #pragma unroll
-    for (int w = 0; w < kAttWaves; ++w) {
-      const float* ml = (float*)(smem[w] + att_part_bytes(RT, DIM));
-      const float f = ml[r] == most ? 1.f : __builtin_amdgcn_exp2f(ml[r] - most);
-      sum = __builtin_fmaf(ml[RT + r], f, sum);
-      v += *(const f32x4_t*)((float*)smem[w] + r * DIM + c) * f;
+      for (int w = 0; w < kAttWaves; ++w) {
+        const uint8_t* from = smem + (w0 + w) * kLds;
+        mw[w] = ((const float*)(from + kPart))[r];
+        lw[w] = ((const float*)(from + kPart))[RT + r];
+        ow[w] = *(const f32x4_t*)((const float*)from + r * DIM + c);
+      }
+      float top = most;
+#pragma unroll
+      for (int w = 0; w < kAttWaves; ++w) top = fmaxf(top, mw[w]);
+      const float f = most == top ? 1.f : __builtin_amdgcn_exp2f(most - top);
+      most = top, sum *= f, v *= f;
+#pragma unroll
+      for (int w = 0; w < kAttWaves; ++w) {
+        const float e = mw[w] == top ? 1.f : __builtin_amdgcn_exp2f(mw[w] - top);
+        sum = __builtin_fmaf(lw[w], e, sum);
+        v += ow[w] * e;
+      }
     }
     if (sp.parts == 1) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -580,7 +602,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(AttArgs a) {
       __builtin_memcpy(&w[k], o + (size_t)p * rows * DIM + 4 * c, 16);
       mp[k] = ml[(size_t)2 * p * rows], lp[k] = ml[(size_t)2 * p * rows + 1];
     }
-    parts = att_span(a.c, len, a.queries, a.window, a.splits).parts;
+    parts = att_span(a.c, len, a.queries, a.window, a.splits, a.waves).parts;
     float top = big;
 #pragma unroll
     for (int k = 0; k < U; ++k)
@@ -595,7 +617,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(AttArgs a) {
         v += w[k] * e;
       }
   }
-  parts = att_span(a.c, len, a.queries, a.window, a.splits).parts;
+  parts = att_span(a.c, len, a.queries, a.window, a.splits, a.waves).parts;
   if (parts == 1) return;  // written by its only workgroup
   part[g][c] = v;
   if (c == 0) maxima[g] = big, sums[g] = sum;
@@ -618,15 +640,28 @@ __global__ void __launch_bounds__(256) attend_join_kernel(AttArgs a) {
 
 // ---------------------------------------------------------------- launch
 
+// Blocks of 64 tokens that a sequence has at most (that its queries see).
+inline long long att_blocks(const KvPages& c, int queries, int window) {
+  long long tokens = (long long)c.max_pages << c.page_shift;
+  if (window > 0 && (long long)window + queries + kAttTokens < tokens)
+    tokens = (long long)window + queries + kAttTokens;
+  return (tokens + kAttTokens - 1) / kAttTokens;
+}
+
+// Waves of a workgroup: four, and eight where a sequence then needs no second workgroup.
+inline int att_wave_count(const KvPages& c, int queries, int window) {
+  const long long n = att_blocks(c, queries, window);
+  const int most = att_most_waves(c.dim, c.groups);
+  return n > kAttWaves && n <= kAttWhole * most / kAttMostWaves ? most : kAttWaves;
+}
+
 // Workgroups that a sequence's tokens are split over, at most: enough to fill the chip
 // once, two workgroups per CU, and no more than there are tokens for.
 inline int att_splits(const KvPages& c, int queries, int window, int tiles) {
-  long long tokens = (long long)c.max_pages << c.page_shift;
-  if (window > 0 && window + queries + kAttTokens < tokens)
-    tokens = window + queries + kAttTokens;
-  const long long most =
-      (tokens + kAttTokens * kAttWaves - 1) / (kAttTokens * kAttWaves);
-  const long long wgs = (long long)c.seqs * c.kv_heads * tiles;
+  const long long n = att_blocks(c, queries, window);
+  const int waves = att_wave_count(c, queries, window);
+  if (waves > kAttWaves) return 1;
+  const long long most = (n + waves - 1) / waves, wgs = (long long)c.seqs * c.kv_heads * tiles;
   long long want = (2LL * device_cus() + wgs - 1) / (wgs > 0 ? wgs : 1);
   want = want < most ? want : most;
   return want < 1 ? 1 : (int)want;
@@ -638,9 +673,10 @@ inline size_t att_space(const KvPages& c, int heads, int queries, int splits) {
 
 template <int DIM, int RT, int NG>
 int launch_attend(const AttArgs& a, hipStream_t st) {
-  const dim3 grid(a.c.kv_heads * a.tiles, a.splits, a.c.seqs), block(kAttWaves * kWave);
+  const dim3 grid(a.c.kv_heads * a.tiles, a.splits, a.c.seqs), block(a.waves * kWave);
   clear_hip_error();
-  hipLaunchKernelGGL((attend_kernel<DIM, RT, NG>), grid, block, 0, st, a);
+  hipLaunchKernelGGL((attend_kernel<DIM, RT, NG>), grid, block,
+                     a.waves * att_wave_bytes(RT, DIM, NG), st, a);
   if (a.splits > 1)
     hipLaunchKernelGGL(attend_join_kernel<DIM>, dim3(a.heads * a.queries, a.c.seqs), dim3(256), 0,
                        st, a);
@@ -710,6 +746,7 @@ extern "C" int lvq_attend(const lvq_kv_cache* cache, const void* q, int q_type, 
   const int rows = heads / a.c.kv_heads * queries;
   a.tiles = (uint16_t)att_tiles(a.c, heads, queries);
   a.splits = att_splits(a.c, queries, window, a.tiles);
+  a.waves = (uint8_t)att_wave_count(a.c, queries, window);
   const size_t space = att_space(a.c, heads, queries, a.splits);
   if (space && !workspace) return LVQ_E_NULL;
   if (workspace_bytes < space) return LVQ_E_SHAPE;
@@ -723,7 +760,8 @@ extern "C" int lvq_attend(const lvq_kv_cache* cache, const void* q, int q_type, 
       if (ranges_overlap(made[i], made_bytes[i], in[j], in_bytes[j])) return LVQ_E_SHAPE;
   if (ranges_overlap(made[0], made_bytes[0], made[1], made_bytes[1])) return LVQ_E_SHAPE;
   a.lens = lens, a.q = q, a.out = out, a.parts = (float*)workspace, a.q_stride = q_stride;
-  a.scale = scale * 1.44269504f, a.window = window;
+  // a window past any length is none that matters, and keeps sums of positions in range
+  a.scale = scale * 1.44269504f, a.window = window < (1 << 30) ? window : 1 << 30;
   a.heads = (uint16_t)heads, a.queries = (uint16_t)queries;
   a.q_type = (uint8_t)q_type, a.out_type = (uint8_t)out_type;
   hipStream_t st = (hipStream_t)stream;
