@@ -425,8 +425,8 @@ int kv_pages(const lvq_kv_cache* c, KvPages* p) {
       c->kv_heads < 1 || c->kv_heads > kKvMaxHeads || c->pages < 0 || c->seqs < 0 ||
       c->max_pages < 0)
     return LVQ_E_SHAPE;
-  // positions are 32-bit
-  if ((int64_t)c->max_pages * c->page > INT32_MAX) return LVQ_E_SHAPE;
+  // positions, and sums of a few of them, are 32-bit
+  if ((int64_t)c->max_pages * c->page > (1 << 30)) return LVQ_E_SHAPE;
   if ((c->pages && !c->pool) || (c->seqs && c->max_pages && !c->table)) return LVQ_E_NULL;
   if (!aligned16(c->pool) || !aligned16(c->table)) return LVQ_E_ALIGN;
   p->pool = (uint8_t*)c->pool, p->table = c->table, p->pages = c->pages;

@@ -515,7 +515,7 @@ int lvq_silu_mul(const void* gate, const void* up, int in_type, int64_t in_strid
 typedef struct {
   void* pool;           /* device, [pages] pages of lvq_kv_page_bytes bytes */
   const int32_t* table; /* device, [seqs][max_pages] page numbers */
-  int pages, seqs, max_pages; /* >= 0; max_pages * page < 2^31 */
+  int pages, seqs, max_pages; /* >= 0; max_pages * page <= 2^30 */
   int kv_heads;         /* 1..1024 */
   int dim;              /* channels of a head: 64, 128 or 256 */
   int page;             /* tokens of a page: 16, 32, 64, 128, 256, 512 or 1024 */
@@ -535,8 +535,8 @@ size_t lvq_kv_page_bytes(int kv_heads, int dim, int page, int group);
  *   scale = fp16((max - min) * fp32(1/15)),  low = fp16(min),
  *   code = (v - low) * (1 / scale) rounded to the nearest (ties to even), within 0..15,
  *   0 where the scale is 0
- * A group that holds an infinity or a NaN is stored as NaN (its low end); magnitudes past
- * fp16's range make its scale or low end infinite.
+ * A group that holds an infinity or a NaN gets an infinite scale and reads as NaN, and one with
+ * magnitudes past fp16's range an infinite scale or low end (NaN or infinities).
  *   k, v       fp32, fp16 or bf16 (type), [tokens] rows of kv_heads * dim values, k_stride
  *              and v_stride values from one row's start to the next's (< 2^31)
  *   seq, pos   device, int32 [tokens]
@@ -576,11 +576,13 @@ int lvq_kv_read(const lvq_kv_cache* cache, const int32_t* seq, const int32_t* po
  *   workspace  device, lvq_attend_workspace bytes, its content of no account before and
  *              after; calls that may run at the same time need one each
  * A query that sees nothing (a length of 0, or fewer tokens than queries before it) gets
- * zeros.  Tokens on pages outside the pool are not seen.  What a query does not see has no
- * effect on it, whatever it holds; a NaN or an infinity that it sees gives NaN.  Sums and
- * weights are fp32, the weights times the values' scales in two fp16 (22 bits).  The result
- * is the same from run to run; how a sequence is split, and so the order of its sums,
- * depends on its length, the cache's sizes and the device.  cache->seqs <= 65535. */
+ * zeros.  Tokens on pages outside the pool are not seen.  What no query of a sequence sees
+ * has no effect on it, whatever it holds, nor has a NaN or an infinity that only its other queries
+ * see; one that a query sees gives NaN.  Sums and weights are fp32, the weights times the
+ * values' scales in two fp16 (22 bits, in a unit that goes by the largest scale so far, of
+ * any query's tokens).  The result is the same from run to run; how a sequence is split, and
+ * so the order of its sums, depends on its length, the cache's sizes, the window and the
+ * device.  cache->seqs <= 65535. */
 #define LVQ_MAX_QUERIES 16
 size_t lvq_attend_workspace(const lvq_kv_cache* cache, int heads, int queries);
 int lvq_attend(const lvq_kv_cache* cache, const void* q, int q_type, int64_t q_stride, int heads,

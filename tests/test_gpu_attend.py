@@ -122,6 +122,49 @@ def test_long(length):
     _check(c, cache, 8, [length], 2)
 
 
+def test_sequences_in_order_of_length():
+    """Long tables and many sequences: they begin by length, equal ones, empty ones and ones
+    out of range among them."""
+    r = np.random.default_rng(8)
+    for seqs, kv_heads in ((40, 16), (64, 8), (2, 300)):
+        c, _ = _cache(kv_heads, 64, 64, 0, 1, 8)
+        c.table = r.integers(0, c.pool.shape[0], (seqs, 64)).astype(np.int32)
+        lens = r.choice([0, 1, 5, 70, 70, 129, 190, -4], seqs)
+        _check(c, _upload(c), kv_heads, lens.tolist(), 1)
+        assert lvq.attend_workspace_bytes(_upload(c), kv_heads) == 0 or seqs * kv_heads < 512
+
+
+def test_far_pages():
+    """Pages past 4 GiB of the pool hold what a near one holds."""
+    size = lvq.kv_page_bytes(8, 128, 1024)
+    pages = (5 << 30) // size
+    c, near = _cache(8, 128, 1024, 0, 1, 1)
+    pool = torch.empty(pages, size, dtype=torch.uint8, device=DEV)
+    for to in (0, pages - 1):
+        pool[to].copy_(near.pool[int(c.table[0, 0])])
+    q = _q(1, 32 * 128, "f16")[0]
+    want = _call(near, q, [1000], 1)
+    for first in (0, pages - 1):
+        far = lvq.kv_cache(pool, _ints([[first]]), 8, 128, 1024)
+        assert torch.equal(_call(far, q, [1000], 1), want)
+
+
+@pytest.mark.parametrize("kv_heads,dim,group,per,queries", [
+    (2, 64, 0, 4, 1), (1, 128, 32, 8, 2), (1, 256, 0, 16, 1), (2, 128, 0, 6, 1)])
+def test_error_in_the_whole(kv_heads, dim, group, per, queries):
+    """The norm of the error over the norm of the result.  Independent roundings of half a step: the
+    logits' errors are below dim^1/2 2^-24 of their terms' norm (a few), the sums' and the
+    weights' below 2^-22; 2^-19 leaves them a factor of four.  A weight or a value kept in one
+    fp16 (2^-12 and more of each term) does not pass."""
+    c, cache = _cache(kv_heads, dim, 64, group, 2, 16)
+    lens, heads = [1024, 515], per * kv_heads
+    qd, qh = _q(2 * queries, heads * dim, "f16", seed=3)
+    got = _call(cache, qd, lens, queries).double().cpu().numpy()
+    want, _ = ok.attend(c, qh.reshape(2, queries, heads, dim), lens, queries, dim ** -0.5)
+    want = want.reshape(got.shape)
+    assert np.linalg.norm(got - want) <= 2.0 ** -19 * np.linalg.norm(want)
+
+
 def test_exact_average():
     """q of zeros: the plain average of the values, whole numbers here, exactly."""
     c, _ = _cache(2, 64, 16, 0, 2, 8)

@@ -134,6 +134,20 @@ def test_heads_of_q(heads):
     _append(st, [0] * 21, list(range(70, 91)), "f16", heads=heads)
 
 
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+def test_rows_of_any_alignment(kind):
+    """Rows that start at any value of a wider buffer."""
+    st = Setup(2, 64, 16, 32, 1, 6)
+    wide, host = _rows(37, 701, kind, 2)
+    k, v = wide[:, 3:131], wide[:, 250:378]
+    q, q_out = wide[:, 401:657], torch.empty(37, 256, device=DEV)
+    pos = list(range(11, 48))
+    lvq.kv_append(st.cache, k, v, _ints(pos), seq=_ints([0] * 37), q=q, q_out=q_out)
+    st.want.store([0] * 37, pos, host[:, 3:131].reshape(37, 2, 64), host[:, 250:378].reshape(37, 2, 64))
+    assert np.array_equal(st.pool(), st.want.pool)
+    assert np.array_equal(q_out.cpu().numpy(), host[:, 401:657])
+
+
 def test_mixed_tokens_in_any_order():
     """Several sequences' tokens shuffled: no run fills a block."""
     st = Setup(2, 128, 16, 64, 4, 6)

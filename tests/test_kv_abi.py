@@ -62,7 +62,7 @@ def test_caches_that_are_refused(call):
         a = dict(kv_heads=2, dim=64, page=16, group=32)
         a.update(bad)
         assert lib.lvq_kv_page_bytes(*a.values()) == 0
-    for bad in (dict(pages=-1), dict(seqs=-1), dict(max_pages=-1), dict(max_pages=1 << 27),
+    for bad in (dict(pages=-1), dict(seqs=-1), dict(max_pages=-1), dict(max_pages=1 << 27), dict(max_pages=(1 << 26) + 1),
                 dict(max_pages=1 << 21, page=1024)):
         assert call(**bad) == E.LVQ_E_SHAPE, bad
     assert call(pool=None) == E.LVQ_E_NULL and call(table=None) == E.LVQ_E_NULL
