@@ -7,7 +7,10 @@
 //   4 bits     per token, head and group of channels: s = fp16((max - min) / 15),
 //              l = fp16(min), code = clamp(rne((v - l) / s), 0, 15), value = s code + l
 //
-// Both are streams: a few operations per value.
+// Both are streams: a few operations per value, but two dependent reads (position, then
+// page) before a store knows its place.  8192 tokens of 32 query and 8 key/value heads of 128
+// channels: storing moves 181 MB in 45 us (4.0 TB/s), reading back 42 MB in 15 us; a kernel
+// that does nothing takes 2 to 3.  Tokens of one step are a launch each way, 3.7 and 4.2 us.
 
 #include "kv_cache.h"
 
@@ -353,17 +356,27 @@ struct ReadArgs {
   uint8_t type;
 };
 
-// Keys or values of one head of 16 tokens, eight channels per thread.  The values of a
+// H: heads of a workgroup.  It waits for positions, then pages, then the cache: where tokens are
+// many, four heads' loads are on their way at once (8192 tokens, 8 heads: 15.4 us, 18 with one);
+// where few, one, so that more workgroups share the work.
+constexpr int kReadHeads = 4;
+inline int heads_at_once(const KvPages& c, long long tiles) {
+  return tiles * c.kv_heads >= 8LL * device_cus() ? kReadHeads : 1;
+}
+
+// Keys or values of H heads of 16 tokens, eight channels per thread.  The values of a
 // whole block come in as it lies and are turned in LDS; of others, byte by byte.
-template <int DIM>
+template <int DIM, int H>
 __global__ void __launch_bounds__(append_threads(DIM)) kv_read_kernel(ReadArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t tile[DIM / 2 * kBlockTokens];
+  __shared__ __attribute__((aligned(16))) uint8_t tile[H][DIM / 2 * kBlockTokens];
   __shared__ uint64_t block0;
   constexpr int dim = DIM, lanes = dim / 8;
-  const int per_tile = a.c.kv_heads * (a.k_out && a.v_out ? 2 : 1);
+  const int per_kind = (a.c.kv_heads + H - 1) / H;
+  const int per_tile = per_kind * (a.k_out && a.v_out ? 2 : 1);
   const int t = blockIdx.x / per_tile, which = blockIdx.x - t * per_tile;
-  const bool values = !a.k_out || which >= a.c.kv_heads;
-  const int head = a.k_out && values ? which - a.c.kv_heads : which;
+  const bool values = !a.k_out || which >= per_kind;
+  const int head0 = (a.k_out && values ? which - per_kind : which) * H;
+  const int heads = a.c.kv_heads - head0 < H ? a.c.kv_heads - head0 : H;
   const int i = threadIdx.x / lanes, lane = threadIdx.x - i * lanes;
   // tiles begin where the first token's block begins, as where they are stored
   const int shift = a.tokens > kBlockTokens ? a.pos[0] & (kBlockTokens - 1) : 0;
@@ -375,46 +388,60 @@ __global__ void __launch_bounds__(append_threads(DIM)) kv_read_kernel(ReadArgs a
     page = kv_page(a.c, a.seq ? a.seq[token] : token, pos);
   }
   const bool there = page >= 0;
-  const int in = pos & (kBlockTokens - 1), group = lane >> (__builtin_ctz(lanes) - __builtin_ctz(a.c.groups));
-  const uint8_t* at = there ? kv_block(a.c, page, head, pos) : nullptr;
-  uint32_t m = 0, code[8];
-  if (there)
-    m = *(const uint32_t*)(at + 16 * dim + (values ? 64 * a.c.groups : 0) + 64 * group + 4 * in);
-  if (!values) {
-    uint32_t w = 0;
-    if (there) w = *(const uint32_t*)(at + in * (dim / 2) + (lane & 3) * (dim / 8) + (lane >> 2) * 4);
+  const int in = pos & (kBlockTokens - 1);
+  const int group = lane >> (__builtin_ctz(lanes) - __builtin_ctz(a.c.groups));
+  const uint8_t* const at0 = there ? kv_block(a.c, page, head0, pos) : nullptr;
+  const int64_t next_head =
+      (int64_t)(kv_block_bytes(dim, a.c.groups)) << (a.c.page_shift - 4);
+  uint32_t m[H], w[H];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) code[j] = (w >> (4 * (j / 2) + 16 * (j % 2))) & 15;
-  } else {
-    if (threadIdx.x == 0) block0 = (uint64_t)at;
+  for (int h = 0; h < H; ++h) {
+    m[h] = w[h] = 0;
+    if (!there || h >= heads) continue;
+    const uint8_t* at = at0 + h * next_head;
+    m[h] = *(const uint32_t*)(at + 16 * dim + (values ? 64 * a.c.groups : 0) + 64 * group + 4 * in);
+    if (!values)
+      w[h] = *(const uint32_t*)(at + in * (dim / 2) + (lane & 3) * (dim / 8) + (lane >> 2) * 4);
+  }
+  bool whole = false;
+  if (values) {
+    if (threadIdx.x == 0) block0 = (uint64_t)at0;
     __syncthreads();
-    const bool whole =
-        __syncthreads_and(i >= kBlockTokens || (there && in == i && (uint64_t)at == block0));
+    whole = __syncthreads_and(i >= kBlockTokens || (there && in == i && (uint64_t)at0 == block0));
     if (whole) {
-      if ((int)threadIdx.x < dim / 2)
-        ((uint4*)tile)[threadIdx.x] =
-            *(const uint4*)((const uint8_t*)block0 + 8 * dim + threadIdx.x * 16);
+      for (int n = threadIdx.x; n < heads * (dim / 2); n += append_threads(dim)) {
+        const int h = n / (dim / 2), pair = n - h * (dim / 2);
+        ((uint4*)tile[h])[pair] =
+            *(const uint4*)((const uint8_t*)block0 + h * next_head + 8 * dim + pair * 16);
+      }
       __syncthreads();
-    }
-    const uint8_t* from = at + 8 * dim;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int pair = 16 * (lane >> 2) + 8 * (lane & 1) + j;
-      uint32_t b = 0;
-      if (whole) b = i < kBlockTokens ? tile[pair * kBlockTokens + in] : 0;
-      else if (there) b = from[pair * kBlockTokens + in];
-      code[j] = (b >> (lane & 2 ? 4 : 0)) & 15;
     }
   }
   if (!mine) return;
-  const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)m);
-  const float l = (float)__builtin_bit_cast(_Float16, (uint16_t)(m >> 16));
-  float v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = there ? rounded(__builtin_fmaf((float)code[j], s, l)) : 0.f;
   uint8_t* out = (uint8_t*)(values ? a.v_out : a.k_out) +
                  (size_t)token * a.c.kv_heads * dim * (a.type == LVQ_F32 ? 4 : 2);
-  store8(out, a.type, head * dim + 8 * lane, v);
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    if (h >= heads) break;
+    const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)m[h]);
+    const float l = (float)__builtin_bit_cast(_Float16, (uint16_t)(m[h] >> 16));
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t code;
+      if (!values) {
+        code = w[h] >> (4 * (j / 2) + 16 * (j % 2));
+      } else {
+        const int byte = (16 * (lane >> 2) + 8 * (lane & 1) + j) * kBlockTokens + in;
+        uint32_t b = 0;
+        if (whole) b = tile[h][byte];
+        else if (there) b = at0[h * next_head + 8 * dim + byte];
+        code = b >> (lane & 2 ? 4 : 0);
+      }
+      v[j] = there ? rounded(__builtin_fmaf((float)(code & 15), s, l)) : 0.f;
+    }
+    store8(out, a.type, (head0 + h) * dim + 8 * lane, v);
+  }
 }
 
 // ---------------------------------------------------------------- checks
@@ -545,13 +572,18 @@ extern "C" int lvq_kv_read(const lvq_kv_cache* cache, const int32_t* seq, const 
   a.seq = seq, a.pos = pos, a.k_out = k_out, a.v_out = v_out;
   a.tokens = tokens, a.type = (uint8_t)out_type;
   const long long tiles = (tokens + kBlockTokens - 1LL) / kBlockTokens + (tokens > kBlockTokens);
-  const long long wgs = tiles * cache->kv_heads * (k_out && v_out ? 2 : 1);
-  if (wgs >= INT32_MAX / 4) return LVQ_E_SHAPE;
-  clear_hip_error();
-  const dim3 grid((unsigned)wgs), threads(append_threads(cache->dim));
+  const int kinds = k_out && v_out ? 2 : 1, at_once = heads_at_once(a.c, tiles);
+  if (tiles * cache->kv_heads * kinds >= INT32_MAX / 4) return LVQ_E_SHAPE;
+  const dim3 grid((unsigned)(tiles * kinds * ((cache->kv_heads + at_once - 1) / at_once)));
+  const dim3 threads(append_threads(cache->dim));
   hipStream_t st = (hipStream_t)stream;
-  if (cache->dim == 64) hipLaunchKernelGGL(kv_read_kernel<64>, grid, threads, 0, st, a);
-  else if (cache->dim == 128) hipLaunchKernelGGL(kv_read_kernel<128>, grid, threads, 0, st, a);
-  else hipLaunchKernelGGL(kv_read_kernel<256>, grid, threads, 0, st, a);
+  clear_hip_error();
+  auto launch = [&](auto one, auto many) {
+    if (at_once == 1) hipLaunchKernelGGL(one, grid, threads, 0, st, a);
+    else hipLaunchKernelGGL(many, grid, threads, 0, st, a);
+  };
+  if (cache->dim == 64) launch(kv_read_kernel<64, 1>, kv_read_kernel<64, kReadHeads>);
+  else if (cache->dim == 128) launch(kv_read_kernel<128, 1>, kv_read_kernel<128, kReadHeads>);
+  else launch(kv_read_kernel<256, 1>, kv_read_kernel<256, kReadHeads>);
   return launch_status();
 }

@@ -250,6 +250,31 @@ def test_read(kv_heads, dim, page, group, kind):
         assert torch.equal(got.cpu(), torch.from_numpy(want32).to(FLOATS[kind]))
 
 
+@pytest.mark.parametrize("kv_heads,dim,group", [(7, 128, 32), (5, 64, 0), (9, 256, 64)])
+@pytest.mark.parametrize("order", ["run", "shuffled"])
+def test_read_of_many(kv_heads, dim, group, order):
+    """Many tokens at once read what few at a time do."""
+    n = 16 * 8 * 256 // kv_heads + 100
+    page = 256
+    st = Setup(kv_heads, dim, page, group, 1, -(-(n + 5) // page))
+    r = np.random.default_rng(6)
+    meta = st.want.blocks()[..., 16 * dim:]
+    meta[:] = (r.uniform(-3, 3, meta.shape[:-1] + (64 * st.want.groups,)).astype(np.float16)
+               .view(np.uint8))
+    st.dpool.copy_(torch.from_numpy(st.want.pool))
+    pos = 5 + (np.arange(n) if order == "run" else r.permutation(n))
+    pos[3000:3010] = -1
+    pos, seq = _ints(pos), _ints(np.zeros(n))
+    out = [torch.full((n, kv_heads * dim), 5.0, device=DEV) for _ in range(5)]
+    lvq.kv_read(st.cache, pos, out[0], out[1], seq=seq)
+    lvq.kv_read(st.cache, pos, None, out[2], seq=seq)
+    for i in range(0, n, 100):
+        part = slice(i, min(n, i + 100))
+        lvq.kv_read(st.cache, pos[part], out[3][part], out[4][part], seq=seq[part])
+    assert torch.equal(out[0], out[3]) and torch.equal(out[1], out[4])
+    assert torch.equal(out[2], out[4]) and not out[0][3000:3010].any()
+
+
 def test_far_pages():
     """Pages past 4 GiB of the pool."""
     page_bytes = lvq.kv_page_bytes(8, 128, 1024)
