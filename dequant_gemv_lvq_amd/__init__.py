@@ -128,8 +128,9 @@ EXPORTED = ("lvq_strerror", "lvq_last_error_index", "lvq_class_table", "lvq_layo
             "lvq_rank", "lvq_gemv", "lvq_gemv_gain",
             "lvq_unfold", "lvq_gemv_fused", "lvq_gemv_noweights", "lvq_decode",
             "bpdq_gemv", "trellis_gemv", "fp16_gemv", "q4_gemv", "q4_gemv_q8",
-            "q4_moe_workspace", "q4_moe", "lvq_rms_norm", "lvq_silu_mul", "lvq_kv_page_bytes", "lvq_kv_append", "lvq_kv_read",
-            "lvq_attend_workspace", "lvq_attend", "lvq_rotate", "lvq_gemv_rotated",
+            "q4_moe_workspace", "q4_moe", "lvq_rms_norm", "lvq_silu_mul", "lvq_kv_page_bytes",
+            "lvq_kv_append", "lvq_kv_read", "lvq_attend_workspace", "lvq_attend", "lvq_rotate",
+            "lvq_gemv_rotated",
             "lvq_stream_read", "lvq_stream_read_geom", "lvq_gemv_launch_info")
 
 
@@ -748,15 +749,26 @@ class KvCache:
     """A key/value cache in 4 bits as kv_append(), kv_read() and attend() take it: the
     pool of pages and the table of pages per sequence, both the caller's tensors."""
 
-    __slots__ = ("pool", "table", "_struct", "_ref")
+    __slots__ = ("_pool", "_table", "_struct", "_ref", "_sizes")
+
+    @property
+    def pool(self):
+        return self._pool
+
+    @property
+    def table(self):
+        return self._table
 
     def _here(self, dev):
-        """Address of the description; its tensors are looked at anew in every call."""
-        s, pool, table = self._struct, self.pool, self.table
+        """Address of the description; its tensors are looked at anew in every call, as they
+        may have been moved or resized in place."""
+        s, pool, table = self._struct, self._pool, self._table
         if pool.get_device() != dev:
             _refuse(pool, "pool", _types("uint8"), s.pages, 0, dev)
         if table.get_device() != dev:
             _refuse(table, "table", _types("int32"), s.seqs, s.max_pages, dev)
+        if (pool.numel(), table.numel()) != self._sizes:
+            raise ValueError("the cache's pool or table has changed its size")
         s.pool, s.table = pool.data_ptr(), table.data_ptr()
         return self._ref
 
@@ -787,7 +799,8 @@ def kv_cache(pool, table, kv_heads: int, dim: int, page: int, group: int = 0) ->
             strerror(LVQ_E_SHAPE), pool.shape[1], size))
     _in_32_bits(pool.shape[0], table.shape[0], table.shape[1])
     c = KvCache()
-    c.pool, c.table = pool, table
+    c._pool, c._table = pool, table
+    c._sizes = pool.numel(), table.numel()
     c._struct = _CacheStruct(0, 0, pool.shape[0], table.shape[0], table.shape[1], int(kv_heads),
                              int(dim), int(page), int(group))
     c._ref = ctypes.addressof(c._struct)

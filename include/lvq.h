@@ -571,7 +571,7 @@ int lvq_kv_read(const lvq_kv_cache* cache, const int32_t* seq, const int32_t* po
  *   heads      a multiple of kv_heads, at most 1024; queries 1..LVQ_MAX_QUERIES
  *   lens       device, int32 [seqs]: tokens of each sequence, the queries' own included
  *              (a length past the table counts as the table's end, a negative one as 0)
- *   scale      above 0, finite
+ *   scale      above 0, finite; times a query's magnitudes below 2^100 (past it, NaN)
  *   out        fp32, fp16 or bf16 (out_type) [seqs * queries][heads * dim]
  *   workspace  device, lvq_attend_workspace bytes, its content of no account before and
  *              after; calls that may run at the same time need one each

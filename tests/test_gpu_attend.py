@@ -101,6 +101,15 @@ def test_queries_and_windows(queries, window):
     _check(c, cache, 6, [640, 300, queries, max(queries - 1, 0), 65], queries, window)
 
 
+@pytest.mark.parametrize("window", [250, 300, 410, 2000])
+@pytest.mark.parametrize("dim,group", [(64, 0), (128, 64), (256, 0), (256, 32)])
+def test_windows_in_long_tables(window, dim, group):
+    """Windows that one workgroup takes alone, and one that none does."""
+    c, cache = _cache(2, dim, 64, group, 3, 100)
+    _check(c, cache, 8, [6400, window + 70, 3333], 2, window)
+    _check(c, cache, 24, [1, 6399, window], 1, window, q="bf16", out="bf16")
+
+
 @pytest.mark.parametrize("per,queries", [(7, 3), (16, 2), (9, 16), (4, 4), (1, 16)])
 @pytest.mark.parametrize("dim,group", [(64, 0), (128, 32), (256, 128)])
 def test_more_rows_than_a_tile(per, queries, dim, group):

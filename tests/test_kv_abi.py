@@ -239,6 +239,20 @@ def test_binding_refuses_caches(library):
         lvq.kv_page_bytes(2 ** 32 + 1, 64, 16)
 
 
+def test_binding_refuses_a_cache_that_has_changed(library):
+    size = ok.page_bytes(2, 64, 16, 32)
+    for change in (lambda c: c.pool.resize_(2, size), lambda c: c.table.resize_(3, 1)):
+        c = _host_cache()
+        change(c)
+        with pytest.raises(ValueError, match="size"):
+            _do_append(cache=c)
+    c = _host_cache()
+    for name in ("pool", "table"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name)[:1])
+    assert not library.calls
+
+
 def test_host_tensors_are_refused():
     for call in (_do_append, _do_read, _do_attend):
         with pytest.raises(ValueError, match="on the GPU"):
