@@ -32,9 +32,9 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kAttWaves = 4;    // of a workgroup, more where that saves the second launch
+constexpr int kAttWaves = 4;    // of a workgroup, more where that saves time
 constexpr int kAttMostWaves = 8;
-constexpr int kAttWhole = 8;    // blocks of a sequence that eight waves take alone
+constexpr int kAttWhole = 8;    // blocks of a sequence that a workgroup takes alone
 constexpr int kAttTokens = 64;  // of a wave at a time
 constexpr uint32_t kCodeMask = 0x03C003C0u;
 constexpr float kCodeUnit = 0x1p18f;
@@ -177,18 +177,13 @@ constexpr int att_wave_bytes(int RT, int dim, int groups) {
   return a > b ? a : b;
 }
 
-// Waves of a workgroup at most, as the registers allow.
-constexpr int att_most_waves(int dim, int groups) {
-  return dim == 256 && groups > 2 ? kAttWaves : kAttMostWaves;
-}
-
 // Waves of a SIMD that the registers are to leave room for.
 constexpr int att_waves(int dim, int groups) {
-  return dim == 64 || (dim == 128 && groups == 1) ? 3 : dim == 128 || groups <= 2 ? 2 : 1;
+  return dim == 64 || (dim == 128 && groups == 1) ? 3 : 2;
 }
 
 template <int DIM, int RT, int NG>
-__global__ void __launch_bounds__(att_most_waves(DIM, NG) * kWave, att_waves(DIM, NG))
+__global__ void __launch_bounds__(kAttMostWaves* kWave, att_waves(DIM, NG))
     attend_kernel(AttArgs a) {
   constexpr int KS = DIM / 32;       // steps of 32 channels
   constexpr int GS = KS / NG;        // of a group
@@ -407,7 +402,9 @@ __global__ void __launch_bounds__(att_most_waves(DIM, NG) * kWave, att_waves(DIM
       for (int n = 0; n < NT; ++n) {
         f32x4_t e;
         if constexpr (RT == 4) e = col & 2 ? (col & 1 ? d[3] : d[2]) : (col & 1 ? d[1] : d[0]);
-        else if constexpr (RT == 8) e = col ? d[2 * n + 1] : d[2 * n];
+        else if constexpr (RT == 8)  // by value: a choice of whole vectors goes through memory
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = col ? d[2 * n + 1][i] : d[2 * n][i];
         else e = d[n];
         const u32x4 sl =
             *(const u32x4*)(lds + (g * kAttTokens + 16 * quarter + 4 * product(n)) * 4);
@@ -664,23 +661,26 @@ inline long long att_blocks(const KvPages& c, int queries, int window) {
   return (tokens + kAttTokens - 1) / kAttTokens;
 }
 
-// Waves of a workgroup: four, and eight where a sequence then needs no second workgroup.
-inline int att_wave_count(const KvPages& c, int queries, int window) {
-  const long long n = att_blocks(c, queries, window);
-  const int most = att_most_waves(c.dim, c.groups);
-  return n > kAttWaves && n <= kAttWhole * most / kAttMostWaves ? most : kAttWaves;
-}
-
-// Workgroups that a sequence's tokens are split over, at most: enough to fill the chip
-// once, two workgroups per CU, and no more than there are tokens for.
-inline int att_splits(const KvPages& c, int queries, int window, int tiles) {
-  const long long n = att_blocks(c, queries, window);
-  const int waves = att_wave_count(c, queries, window);
-  if (waves > kAttWaves) return 1;
-  const long long most = (n + waves - 1) / waves, wgs = (long long)c.seqs * c.kv_heads * tiles;
-  long long want = (2LL * device_cus() + wgs - 1) / (wgs > 0 ? wgs : 1);
-  want = want < most ? want : most;
-  return want < 1 ? 1 : (int)want;
+// How a sequence's tokens are split: waves of a workgroup and, at most, workgroups.
+struct Split {
+  int waves, parts;
+};
+inline Split att_split(const KvPages& c, int queries, int window, int tiles) {
+  const long long n = att_blocks(c, queries, window), wgs = (long long)c.seqs * c.kv_heads * tiles;
+  const int cus = device_cus();
+  // Few tokens: a workgroup alone, without the second launch, and of eight waves if it has a CU
+  // to itself (500 tokens of 128 channels, 8 key/value heads: 16 sequences 8.0 us; 57
+  // sequences 11.5 us with four waves, 14.4 with eight, of which a CU then holds one)
+  if (n <= kAttWhole) return {n > kAttWaves && wgs < cus ? kAttMostWaves : kAttWaves, 1};
+  // Else enough workgroups to fill the chip once, two per CU. A few too many would begin when the
+  // first have ended, so parts are rounded down (7 of 60000 tokens: 73 parts 15.2 us, 74 18.0;
+  // 72 of up to 3733: 7 parts 12.2, 8 13.6), but for less than four, where a third fewer cost
+  // more (160 of up to 6000: 3 parts 21.4, 4 19.2).
+  const long long down = 2LL * cus / (wgs > 0 ? wgs : 1);
+  const long long want = down < 4 ? (2LL * cus + wgs - 1) / (wgs > 0 ? wgs : 1) : down;
+  // and no more than there are tokens for
+  const long long most = (n + kAttWaves - 1) / kAttWaves, parts = want < most ? want : most;
+  return {kAttWaves, parts < 1 ? 1 : (int)parts};
 }
 
 inline size_t att_space(const KvPages& c, int heads, int queries, int splits) {
@@ -737,7 +737,7 @@ extern "C" size_t lvq_attend_workspace(const lvq_kv_cache* cache, int heads, int
   KvPages c;
   if (kv_pages(cache, &c) || att_sizes(c, heads, queries)) return 0;
   return att_space(c, heads, queries,
-                   att_splits(c, queries, 0, att_tiles(c, heads, queries)));
+                   att_split(c, queries, 0, att_tiles(c, heads, queries)).parts);
 }
 
 extern "C" int lvq_attend(const lvq_kv_cache* cache, const void* q, int q_type, int64_t q_stride,
@@ -761,8 +761,8 @@ extern "C" int lvq_attend(const lvq_kv_cache* cache, const void* q, int q_type, 
     return LVQ_E_ALIGN;
   const int rows = heads / a.c.kv_heads * queries;
   a.tiles = (uint16_t)att_tiles(a.c, heads, queries);
-  a.splits = att_splits(a.c, queries, window, a.tiles);
-  a.waves = (uint8_t)att_wave_count(a.c, queries, window);
+  const Split split = att_split(a.c, queries, window, a.tiles);
+  a.splits = split.parts, a.waves = (uint8_t)split.waves;
   // in order where a workgroup may have long to run: it costs a trip to memory
   const int per_seq = a.c.kv_heads * a.tiles * a.splits;
   const bool ordered = a.c.seqs > 1 && a.c.seqs <= kWave &&
