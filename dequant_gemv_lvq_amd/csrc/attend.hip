@@ -55,7 +55,7 @@ struct AttArgs {
   void* out;
   float* parts;   // [seqs][kv_heads][splits][rows][dim], then {maximum, sum} of each
   int64_t q_stride;  // values
-  float scale;    // of the logits, in powers of two
+  float scale, scale_rest;  // of the logits, in powers of two: rounded down, and the rest
   int window, splits;
   uint16_t tiles;  // of rows
   uint8_t q_type, out_type, waves;
@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(kAttMostWaves* kWave, att_waves(DIM, NG))
   // q: operand column t16 (row t16 % RT), channels 32 s + 8 quarter .. + 7 of step s
   half8_t qa[KS];
   float qs[NG], unit = a.scale * kCodeUnit;  // sums of the row's q over a group, a logit's unit
+  float unit_rest = a.scale_rest * kCodeUnit;
   const int r = row0 + (t16 & (RT - 1));
   int see_first = 0, see_last = sp.len - 1;  // rows past the last: not stored
   {
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kAttMostWaves* kWave, att_waves(DIM, NG))
       top = top == 0x7F800000u || top == 0 ? 0x3F800000u : top;
       top = top < 0x01000000u ? 0x01000000u : top > 0x7E000000u ? 0x7E000000u : top;
       const float down = __builtin_bit_cast(float, 0x7F000000u - top);
-      unit *= __builtin_bit_cast(float, top);
+      unit *= __builtin_bit_cast(float, top), unit_rest *= __builtin_bit_cast(float, top);
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -328,6 +329,7 @@ __global__ void __launch_bounds__(kAttMostWaves* kWave, att_waves(DIM, NG))
       for (int i = 0; i < 8; ++i) qs[s / GS] += (float)qa[s][i];
 #pragma unroll
     for (int g = 0; g < NG; ++g) qs[g] = quarter_sum(qs[g]) * (1.f / kCodeUnit);
+    unit_rest = fmaxf(unit_rest, 0x1p-126f);  // above 0: times minus infinity it is no NaN
   }
   // tokens that every row sees, and the first that any does
   int all_first = 0, any_first = 0, all_last;
@@ -474,8 +476,11 @@ __global__ void __launch_bounds__(kAttMostWaves* kWave, att_waves(DIM, NG))
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        // in the weights' unit, a power of two
-        p[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(lg[n][i], unit, -mi)) * pu;
+        // the unit's rounding would change logits by 2^-24 of themselves, weights by that times
+        // the logit (128 channels, 131072 tokens: 1e-5 of the result); in the weights'
+        // unit, a power of two
+        const float x = __builtin_fmaf(lg[n][i], unit_rest, __builtin_fmaf(lg[n][i], unit, -mi));
+        p[n][i] = __builtin_amdgcn_exp2f(x) * pu;
         l += p[n][i];
       }
 #pragma unroll
@@ -490,14 +495,22 @@ __global__ void __launch_bounds__(kAttMostWaves* kWave, att_waves(DIM, NG))
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           lvq_half2 h, t;
+          float w[2], s[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float w = p[n][2 * i + k], s = att_f16(sl[2 * i + k]);
-            h[i] = (_Float16)(w * s);
-            t[i] = (_Float16)__builtin_fmaf(w, s, -(float)h[i]);
-            low[g] = __builtin_fmaf(w, att_f16(sl[2 * i + k] >> 16), low[g]);
+            w[i] = p[n][2 * i + k], s[i] = att_f16(sl[2 * i + k]);
+            h[i] = (_Float16)(w[i] * s[i]);
+            low[g] = __builtin_fmaf(w[i], att_f16(sl[2 * i + k] >> 16), low[g]);
           }
-          hi[n][k] = __builtin_bit_cast(uint32_t, h);
+          // the rounded values as they are, for the rests too: rounded anew from w s by an
+          // instruction that multiplies and rounds at once, a value between two fp16 may be
+          // the other of them
+          uint32_t both = __builtin_bit_cast(uint32_t, h);
+          asm("" : "+v"(both));
+          h = __builtin_bit_cast(lvq_half2, both);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) t[i] = (_Float16)__builtin_fmaf(w[i], s[i], -(float)h[i]);
+          hi[n][k] = both;
           rest[n][k] = __builtin_bit_cast(uint32_t, t);
         }
       }
@@ -790,7 +803,10 @@ extern "C" int lvq_attend(const lvq_kv_cache* cache, const void* q, int q_type, 
   if (ranges_overlap(made[0], made_bytes[0], made[1], made_bytes[1])) return LVQ_E_SHAPE;
   a.lens = lens, a.q = q, a.out = out, a.parts = (float*)workspace, a.q_stride = q_stride;
   // a window past any length is none that matters, and keeps sums of positions in range
-  a.scale = scale * 1.44269504f, a.window = window < (1 << 30) ? window : 1 << 30;
+  const double powers = (double)scale * 1.4426950408889634;
+  a.scale = (float)powers;
+  if ((double)a.scale > powers) a.scale = __builtin_nextafterf(a.scale, 0.f);
+  a.scale_rest = (float)(powers - (double)a.scale), a.window = window < (1 << 30) ? window : 1 << 30;
   a.heads = (uint16_t)heads, a.queries = (uint16_t)queries;
   a.q_type = (uint8_t)q_type, a.out_type = (uint8_t)out_type;
   hipStream_t st = (hipStream_t)stream;

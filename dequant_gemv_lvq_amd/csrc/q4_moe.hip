@@ -489,6 +489,7 @@ __global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a)
       float v = g * 0.25f * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0.25f, 0.25f)) * u;
       const int row = quad * 4 + r4;
       if (row >= a.inner) v = 0.f;
+      asm("" : "+v"(v));  // one value for both: not multiplied and rounded at once for either
       const _Float16 hi = (_Float16)v, rest = (_Float16)(v - (float)hi);
       const size_t to = (size_t)(first + ul) * act_pitch(a.inner) + act_place(row);
       a.act[to] = __builtin_bit_cast(uint16_t, hi);

@@ -174,6 +174,17 @@ def test_error_in_the_whole(kv_heads, dim, group, per, queries):
     assert np.linalg.norm(got - want) <= 2.0 ** -19 * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("per,group", [(4, 0), (8, 64), (16, 32)])
+def test_many_rows_of_few_tokens(per, group):
+    """So many weights that some lie between two fp16: the rounded value and the rest are of one
+    rounding. A scale so small that nothing else is off by as much as one of the values."""
+    r = np.random.default_rng(11)
+    seqs = 8192 // (8 * per)
+    c, cache = _cache(8, 128, 16, group, seqs, 1, seed=5)
+    _check(c, cache, 8 * per, r.integers(2, 7, seqs).tolist(), 1, scale=1e-3)
+    _check(c, cache, 8 * per, r.integers(2, 17, seqs).tolist(), 1, scale=1e-3, seed=2)
+
+
 def test_exact_average():
     """q of zeros: the plain average of the values, whole numbers here, exactly."""
     c, _ = _cache(2, 64, 16, 0, 2, 8)
