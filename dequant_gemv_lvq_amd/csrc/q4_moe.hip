@@ -13,7 +13,7 @@
 // codes are fp16 subnormals (bits 6..9 of the mantissa), scale and zero are applied in the
 // lane in fp32.  Up to four tokens of an expert share a pass over its weights (a job).  x
 // sits in LDS.  The activations between the products are kept as two fp16, the rounded
-// value and the rest (22 bits), which the down product multiplies side by side.
+// value and the rest times 2^11 (22 bits), which the down product multiplies side by side.
 //
 // What bounds it, and what it measured (GPU, one call; 128 experts of 2048 x 768, 8 chosen):
 // one token, the three launches and in each a few trips to memory (router 3.0 us, gate and up
@@ -28,6 +28,8 @@
 namespace lvq {
 
 constexpr float kMoeUnit = 0x1p-18f;   // of a code inside an fp16
+// Of an activation's rest: as large as the value was, so that it is a normal number where that is.
+constexpr float kRestUnit = 0x1p11f;
 constexpr int kGateWaves = 16;
 constexpr int kMaxPairs = LVQ_MAX_MOE_TOKENS * LVQ_MAX_MOE_TOP;
 constexpr int kMaxExperts = 512;
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a)
       const int row = quad * 4 + r4;
       if (row >= a.inner) v = 0.f;
       asm("" : "+v"(v));  // one value for both: not multiplied and rounded at once for either
-      const _Float16 hi = (_Float16)v, rest = (_Float16)(v - (float)hi);
+      const _Float16 hi = (_Float16)v, rest = (_Float16)((v - (float)hi) * kRestUnit);
       const size_t to = (size_t)(first + ul) * act_pitch(a.inner) + act_place(row);
       a.act[to] = __builtin_bit_cast(uint16_t, hi);
       a.act[lo + to] = __builtin_bit_cast(uint16_t, rest);
@@ -713,8 +715,9 @@ __global__ void __launch_bounds__(kDownWaves* kWave) moe_down_kernel(DownArgs a)
     const float weight = ul < jb.count ? weights[jb.first + ul] : 0.f;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const float v0 = sum_blocks(acc[q][0] + acc[q][1]);
-      const float v1 = jb.count > 1 ? sum_blocks(acc[q][2] + acc[q][3]) : 0.f;
+      constexpr float back = 1.f / kRestUnit;
+      const float v0 = sum_blocks(__builtin_fmaf(acc[q][1], back, acc[q][0]));
+      const float v1 = jb.count > 1 ? sum_blocks(__builtin_fmaf(acc[q][3], back, acc[q][2])) : 0.f;
       if (ul < jb.count) {
         float* to = &part[wv][(jb.tokens >> (4 * ul) & 15) * R + 4 * q + r4];
         *to = __builtin_fmaf(weight, (ul ? v1 : v0) * (1.f / kMoeUnit), *to);

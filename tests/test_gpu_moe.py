@@ -126,6 +126,22 @@ def test_largest_x():
     m.check(m.x(2))
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+def test_small_activations(zeros):
+    """Activations of 2^-11 or so, whose rests are below the normal numbers, are kept as well as
+    others: sums of a few hundred products in fp32, each off by 2^-20 of the result at most."""
+    m = Layer(512, 256, 8, 2, 64, zeros)
+    x = m.x(4) * 2.0 ** -5
+    y, ids, w = m.run(x)
+    xh = x.double().cpu().numpy()
+    want_ids, want_w, dw, gap = om.choose(xh, m.router.double().numpy(), 2, True)
+    assert gap > 1 and np.array_equal(ids.cpu().numpy(), want_ids)
+    want, _ = om.layer(xh, want_ids, want_w, dw, m.gu.expert, m.down.expert)
+    err = np.linalg.norm(y.double().cpu().numpy() - want) / np.linalg.norm(want)
+    print("error of small activations %.3g" % err)
+    assert err <= 2.0 ** -18
+
+
 def test_all_tokens_through_one_expert():
     """One expert far above the others for every token: jobs of four tokens, the last short."""
     m = Layer(256, 80, 6, 2, 32, True)
