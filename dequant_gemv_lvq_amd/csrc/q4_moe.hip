@@ -403,13 +403,15 @@ __global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a)
       const int row = quad * 4 + (h ? a.inner : 0), left = 2 * a.inner - row;
       const int rows = none || left < 0 ? 0 : left < 4 ? left : 4;
       const size_t first = e * 2 * a.inner + (rows ? row : 0);
+      // offsets in the base and the lanes, as in the down product: the range then holds whether or
+      // not a scalar offset counts in its check
       const uint8_t* base = a.codes + first * row_bytes + t0 * 256;
       const uint32_t bytes = rows ? rows * row_bytes - t0 * 256 : 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         k.w[h][i] = __builtin_bit_cast(
             u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(q4_rsrc(base, t0 + i < steps ? bytes : 0),
-                                                           lane_off, i * 256, 2));
+                                                           lane_off + i * 256, 0, 2));
     }
     advance(ld);
   };
@@ -599,18 +601,21 @@ __global__ void __launch_bounds__(kDownWaves* kWave) moe_down_kernel(DownArgs a)
   Cursor ld = start(f0), at = ld;
   // scales: lane (ul, r4) asks for row 4 (ul / 8) + r4 of the rows, group ul % 8 of the step's
   const int scale_off = (4 * (ul >> 3) + r4) * groups + (ul & 7);
-  const int code_off = (lane >> 4) * row_bytes + (lane & 15) * 16;
-  const auto act = q4_rsrc(a.act, 2 * pairs * pitch * 2);
+  int code_off[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) code_off[q] = (4 * q + (lane >> 4)) * row_bytes + (lane & 15) * 16;
+  const size_t rests = (size_t)pairs * pitch;
   // where the job of the next load begins
   const uint8_t* codes;
   size_t scales;
-  int act_row, count;
+  const uint16_t* act;
+  int count;
   auto enter = [&](int i) {
     const Job j = job_at(i);
     const size_t first = (size_t)j.expert * a.hidden + row0;
     codes = a.codes + first * row_bytes;
     scales = first * groups;
-    act_row = j.first * (pitch * 2), count = j.count;
+    act = a.act + (size_t)j.first * pitch, count = j.count;
   };
   if (f0 < f1) enter(ld.job);
   auto load = [&](Step& k) {
@@ -626,21 +631,22 @@ __global__ void __launch_bounds__(kDownWaves* kWave) moe_down_kernel(DownArgs a)
       if constexpr (Z)
         k.z[n] = __builtin_amdgcn_raw_buffer_load_b16(q4_rsrc(a.zero + scales, sb), off, 0, 0);
     }
-    // row i: token i / 2 of the job, the rounded values or the rests
-    const int there = past || ld.t * 16 + (lane & 15) >= nunits ? 0x80000000 : lane * 16;
-    const int second = count > 1 ? there : 0x80000000;
+    // row i: token i / 2 of the job, the rounded values or the rests; a range of the step's 1024
+    // bytes each, an empty one where there is no second token
+    const int there = ld.t * 16 + (lane & 15) >= nunits ? 0x80000000 : lane * 16;
+    const uint32_t one = past ? 0 : 1024, two = count > 1 ? one : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       k.x[i] = __builtin_bit_cast(
           u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                       act, i < 2 ? there : second,
-                       act_row + ld.t * 1024 + (i >> 1) * (pitch * 2) + (i & 1) * pairs * (pitch * 2),
-                       0));
+                       q4_rsrc(act + ld.t * 512 + (i >> 1) * pitch + (i & 1) * rests,
+                               i < 2 ? one : two),
+                       there, 0, 0));
     const auto range = q4_rsrc(codes + ld.t * 256, past ? 0 : rows * row_bytes - ld.t * 256);
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
       k.w[q] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                               range, code_off, 4 * q * row_bytes, 2));
+                                               range, code_off[q], 0, 2));
     const int job = ld.job;
     next(ld);
     if (ld.job != job && ld.f < f1) enter(ld.job);

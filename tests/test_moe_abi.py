@@ -100,3 +100,27 @@ def test_binding_refuses(library):
 def test_host_tensors_are_refused():
     with pytest.raises(ValueError, match="on the GPU"):
         lvq.q4_moe(**_args())
+
+
+def test_loads_are_checked_without_a_scalar_offset():
+    """A buffer load's range is that of its descriptor; the compiler leaves open whether the
+    scalar offset counts in the check, so none is given and a range is exact either way."""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(lvq.__file__), "csrc", "q4_moe.hip")
+    with open(path) as f:
+        text = f.read()
+    calls = 0
+    for m in re.finditer(r"__builtin_amdgcn_raw_buffer_load_\w+\(", text):
+        depth, args = 1, [""]
+        for ch in text[m.end():]:
+            depth += (ch in "([{") - (ch in ")]}")
+            if depth == 0:
+                break
+            if ch == "," and depth == 1:
+                args.append("")
+            else:
+                args[-1] += ch
+        assert len(args) == 4 and args[2].strip() == "0", args
+        calls += 1
+    assert calls
