@@ -367,20 +367,27 @@ __global__ void __launch_bounds__(kAttMostWaves* kWave, att_waves(DIM, NG))
       uint32_t ks[NG], vs[NG];
 #pragma unroll
       for (int g = 0; g < NG; ++g) ks[g] = x.ks[g], vs[g] = x.vs[g];
+      // a scale or low end that is not finite becomes a NaN of the token's logit: zero times it is
+      // one, and joins the first pair
+      lvq_half2 not_a_number = {0, 0};
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (uint32_t w : {ks[g], vs[g]})
+          not_a_number = __builtin_elementwise_fma(as_half2(w), lvq_half2{0, 0}, not_a_number);
+      ks[0] = __builtin_bit_cast(uint32_t, as_half2(ks[0]) + not_a_number);
       if (edge) {
-        // what no row sees is 0, whatever it holds; a value that is not finite becomes a
-        // NaN of the logit, for the rows that see it, and nothing for the others
+        // what no row sees is 0, whatever it holds, and so is a value that is not finite: nothing
+        // for the rows that do not see it
         const int tok = t0 + lane;
         const bool none = bad || tok >= sp.len || tok < any_first;
         bool wild = false;
 #pragma unroll
         for (int g = 0; g < NG; ++g)
           wild |= (vs[g] & 0x7C00u) == 0x7C00u || (vs[g] & 0x7C000000u) == 0x7C000000u;
-        if (none || wild) {
-          ks[0] = wild ? 0x7E00u : ks[0];
+        if (none || wild)
 #pragma unroll
           for (int g = 0; g < NG; ++g) vs[g] = 0;
-        }
       }
       lds_order();
 #pragma unroll

@@ -578,7 +578,8 @@ int lvq_kv_read(const lvq_kv_cache* cache, const int32_t* seq, const int32_t* po
  * A query that sees nothing (a length of 0, or fewer tokens than queries before it) gets
  * zeros.  Tokens on pages outside the pool are not seen.  What no query of a sequence sees
  * has no effect on it, whatever it holds, nor has a NaN or an infinity that only its other queries
- * see; one that a query sees gives NaN.  Sums and weights are fp32, the weights times the
+ * see; one that a query sees (in the query, or as a scale or low end of a token's keys or values,
+ * in any of its groups) gives NaN in every channel.  Sums and weights are fp32, the weights times the
  * values' scales in two fp16 (22 bits, in a unit that goes by the largest scale so far, of
  * any query's tokens).  The result is the same from run to run; how a sequence is split, and
  * so the order of its sums, depends on its length, the cache's sizes, the window and the

@@ -317,3 +317,56 @@ def test_streams_and_graphs():
             graphs[i].replay()
         for i in range(2):
             assert torch.equal(outs[i], _call(cache, q[i], now, 1)), (step, i)
+
+
+def _spoil(c, seq, head, token, which, part, value, group=0):
+    """Overwrites the scale (part 0) or the low end (1) of a token's keys (which 0) or values (1)."""
+    p, i = c.place(seq, token)
+    m = c.blocks()[p, head, i // 16, 16 * c.dim:].view(np.float16).reshape(2, c.groups, 16, 2)
+    m[which, group, i % 16, part] = value
+
+
+@pytest.mark.parametrize("per,dim,group,length", [
+    (4, 128, 0, 300), (4, 64, 32, 2000), (8, 128, 64, 300), (8, 256, 0, 1500), (16, 64, 0, 2000),
+    (16, 128, 32, 450), (1, 256, 32, 2000)])
+def test_a_seen_token_that_is_not_finite(per, dim, group, length):
+    """A scale or a low end that is an infinity or a NaN makes the rows that see its token NaN in
+    every channel, wherever the token lies: in a block that all rows see whole, in the first, in the
+    last, and one that only later queries see; other heads and sequences keep their bits."""
+    c, cache = _cache(2, dim, 16, group, 2, -(-length // 16))
+    queries, heads, lens = 2, 2 * per, [length, length - 33]
+    q = _q(2 * queries, heads * dim, "f16")[0]
+    want = _call(cache, q, lens, queries)
+    assert want.isfinite().all()
+    keep = c.pool.copy()
+    for token in (3, 140, length // 128 * 64 + 5, length - 5, length - 1):
+        for which in (0, 1):
+            for part, value in ((0, np.inf), (1, np.inf), (1, -np.inf), (1, np.nan)):
+                c.pool[:] = keep
+                _spoil(c, 0, 1, token, which, part, value, c.groups - 1)
+                got = _call(_upload(c), q, lens, queries).view(2, queries, 2, per * dim)
+                sees = torch.tensor([token <= length - queries + i for i in range(queries)])
+                at = (token, which, part, value)
+                assert got[0, sees, 1].isnan().all(), at
+                other = torch.ones(2, 2, dtype=torch.bool)
+                other[0, 1] = False
+                pair = [t.transpose(1, 2)[other] for t in (got, want.view(got.shape))]
+                assert torch.equal(*pair), at
+                # the unit of this head's weights goes by the other tokens' scales alone: within
+                # the bound of test_error_in_the_whole
+                here, then = (t[0, ~sees, 1] for t in (got, want.view(got.shape)))
+                assert (here - then).norm() <= 2.0 ** -19 * then.norm(), at
+
+
+def test_stored_keys_and_values_past_fp16():
+    """Keys and values around -70000 with a small range: their low end is minus infinity."""
+    c, cache = _cache(1, 64, 16, 0, 1, 20)
+    q = _q(1, 4 * 64, "f16")[0]
+    for token in (70, 299):
+        for bad in ("k", "v"):
+            cache = _upload(c)
+            rows = {n: torch.randn(1, 64, device=DEV) for n in ("k", "v")}
+            rows[bad] -= 7e4
+            lvq.kv_append(cache, rows["k"], rows["v"], _ints([token]))
+            assert _call(cache, q, [300], 1).isnan().all(), (token, bad)
+            assert _call(cache, q, [token], 1).isfinite().all()
