@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(kAttMostWaves* kWave, att_waves(DIM, NG))
       for (int i = 0; i < 8; ++i) qs[s / GS] += (float)qa[s][i];
 #pragma unroll
     for (int g = 0; g < NG; ++g) qs[g] = quarter_sum(qs[g]) * (1.f / kCodeUnit);
-    unit_rest = fmaxf(unit_rest, 0x1p-126f);  // above 0: times minus infinity it is no NaN
+    // above 0, so that times minus infinity they are no NaN (logits in them are 0 all the same)
+    unit = fmaxf(unit, 0x1p-126f), unit_rest = fmaxf(unit_rest, 0x1p-126f);
   }
   // tokens that every row sees, and the first that any does
   int all_first = 0, any_first = 0, all_last;

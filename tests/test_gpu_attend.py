@@ -370,3 +370,19 @@ def test_stored_keys_and_values_past_fp16():
             lvq.kv_append(cache, rows["k"], rows["v"], _ints([token]))
             assert _call(cache, q, [300], 1).isnan().all(), (token, bad)
             assert _call(cache, q, [token], 1).isfinite().all()
+
+
+@pytest.mark.parametrize("length", [1, 100, 300, 2000])
+def test_logits_too_small_to_matter(length):
+    """Queries and scales whose product leaves fp32: the plain average of the values, no NaN where
+    the last block holds tokens that no query sees."""
+    c, cache = _cache(1, 64, 16, 32, 1, 125)
+    for kind, size, scale in (("bf16", 2.0 ** -100, 2.0 ** -70), ("bf16", 2.0 ** -120, 1e-38),
+                              ("bf16", 1.0, 2.0 ** -149), ("f16", 2.0 ** -10, 2.0 ** -149)):
+        for queries in (1, 2):
+            qd, qh = _q(queries, 8 * 64, kind, scale=size)
+            got = _call(cache, qd, [length], queries, scale=scale).double().cpu().numpy()
+            want, tol = ok.attend(c, qh.reshape(1, queries, 8, 64), [length], queries, scale, 0,
+                                  kind == "bf16")
+            want, tol = want.reshape(got.shape), tol.reshape(got.shape)
+            assert (np.abs(got - want) <= tol + on.half_step(want, "f32")).all(), (kind, size, scale)
