@@ -11,8 +11,9 @@ Bounds, u = 2^-24 a nearest rounding to fp32, STEP32 = 2^-23 any fp32 operation:
               roundings are off by half of that each (the sum is 1 at least), whatever the size
   gate, up    as oracle.q4.gemv
   activation  silu(g) u: |silu'| < 1.1, so 1.1 |u| dg + |silu(g)| du + dg du, and the activation's
-              own (2 |g| + 7) u relative (oracle.norm); kept as two fp16: 2^-22 of it, and
-              2^-25 where the rest is below the normal numbers
+              own (2 |g| + 7) u relative (oracle.norm); kept as two fp16, the rounded value and
+              2^11 times the rest: 2^-22 of it, and 2^-25 / 2^11 where that is below the normal
+              numbers
   down        as oracle.q4.gemv over the activations, plus their error times |w|; three
               STEP32 more for the weight's product and at most jobs + 8 additions of experts
 """
@@ -57,7 +58,7 @@ def layer(x, ids, w, dw, gate_up, down) -> tuple:
         s = g / (1 + np.exp(-g))
         a = s * u
         da = 1.1 * np.abs(u) * dg + np.abs(s) * du + dg * du
-        da += (2 * np.abs(g) + 7) * U * np.abs(a) + 2.0 ** -22 * np.abs(a) + 2.0 ** -25
+        da += (2 * np.abs(g) + 7) * U * np.abs(a) + 2.0 ** -22 * np.abs(a) + 2.0 ** -36
         d, dd = q4.gemv(dwt, dt, a)
         dd = 2 * dd + da @ np.abs(dwt).T  # two chains, of the rounded values and the rests
         we, dwe = w[t, slot][:, None], dw[t, slot][:, None]

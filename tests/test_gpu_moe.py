@@ -233,3 +233,20 @@ def test_determinism_streams_and_graphs():
             g.replay()
         for m, x, y in zip(layers, xs, ys):
             assert torch.equal(y, m.run(x)[0])
+
+
+@pytest.mark.parametrize("hidden,inner,experts,top,group,tokens", [
+    (512, 256, 8, 2, 64, 4), (300, 331, 5, 2, 32, 1), (1001, 70, 3, 2, 0, 7), (256, 513, 2, 2, 128, 16)])
+@pytest.mark.parametrize("size", [2.0 ** -5, 2.0 ** -10])
+def test_small_activations_value_by_value(hidden, inner, experts, top, group, tokens, size):
+    """As test_small_activations, every value within the oracle's bound: inner sizes cut short, one
+    token, more than two tokens of an expert; with 2^-10 the activations themselves are below the
+    normal numbers."""
+    m = Layer(hidden, inner, experts, top, group, True)
+    m.router = (m.router.float() / size).half()  # the choice stays as clear as it is
+    m.args = (m.router.to(DEV),) + m.args[1:]
+    for seed in range(20):
+        x = (m.x(tokens, seed).float() * size).half()
+        if om.choose(x.double().cpu().numpy(), m.router.double().numpy(), top, True)[3] > 1:
+            break
+    m.check(x)

@@ -146,3 +146,35 @@ def test_ties_by_the_lowest_index():
     x, router = np.ones((1, 4)), np.ones((6, 4))
     ids, w, _, gap = om.choose(x, router, 3, False)
     assert ids.tolist() == [[0, 1, 2]] and np.allclose(w, 1 / 6) and gap == 0
+
+
+@pytest.mark.parametrize("size", [2.0 ** -4, 2.0 ** -8, 2.0 ** -12])
+@pytest.mark.parametrize("inner,tokens", [(256, 1), (331, 3), (70, 7)])
+def test_moe_bound_tells_how_activations_are_kept(inner, tokens, size):
+    """Small activations as two fp16: with the rest times 2^11 they are inside the bound; with the
+    rest as it is they are not once an activation (about size^2) is a step of the subnormal
+    numbers, 2^-24, or less, and its rest is nothing."""
+    r = np.random.default_rng(6)
+    hidden, experts, top, mats = 96, 3, 2, {}
+    x, router = size * r.standard_normal((tokens, hidden)), r.standard_normal((experts, hidden)) / size
+    for name, rows, cols in (("gu", 2 * inner, hidden), ("down", hidden, inner)):
+        for e in range(experts):
+            codes = r.integers(0, 256, (rows, -(-cols // 32) * 16)).astype(np.uint8)
+            scale = (0.25 * cols ** -0.5 * r.uniform(0.5, 1.5, (rows, -(-cols // 32)))).astype(np.float16)
+            mats[name, e] = oq.weights(codes, scale.view(np.uint16), None, rows, cols, 32)
+    ids, w, dw, _ = om.choose(x, router, top, True)
+    y, tol = om.layer(x, ids, w, dw, lambda e: mats["gu", e], lambda e: mats["down", e])
+    worst = {}
+    for unit in (1.0, 2.0 ** 11):
+        got = np.zeros(y.shape)
+        for t in range(tokens):
+            for e, we in zip(ids[t], w[t]):
+                gu = mats["gu", e][0] @ x[t]
+                a = gu[:inner] / (1 + np.exp(-gu[:inner])) * gu[inner:]
+                hi = a.astype(np.float16).astype(float)
+                rest = ((a - hi) * unit).astype(np.float16).astype(float) / unit
+                got[t] += we * (mats["down", e][0] @ (hi + rest))
+        worst[unit] = (np.abs(got - y) / tol).max()
+    assert worst[2.0 ** 11] <= 1
+    if size ** 2 <= 2.0 ** -24:
+        assert worst[1.0] > 1
