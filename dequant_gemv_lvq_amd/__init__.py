@@ -767,8 +767,10 @@ class KvCache:
             _refuse(pool, "pool", _types("uint8"), s.pages, 0, dev)
         if table.get_device() != dev:
             _refuse(table, "table", _types("int32"), s.seqs, s.max_pages, dev)
-        if (pool.numel(), table.numel()) != self._sizes:
+        if (pool.nbytes, table.nbytes) != self._sizes:
             raise ValueError("the cache's pool or table has changed its size")
+        if not (pool.is_contiguous() and table.is_contiguous()):
+            raise ValueError("the cache's pool or table is no longer contiguous")
         s.pool, s.table = pool.data_ptr(), table.data_ptr()
         return self._ref
 
@@ -800,7 +802,7 @@ def kv_cache(pool, table, kv_heads: int, dim: int, page: int, group: int = 0) ->
     _in_32_bits(pool.shape[0], table.shape[0], table.shape[1])
     c = KvCache()
     c._pool, c._table = pool, table
-    c._sizes = pool.numel(), table.numel()
+    c._sizes = pool.nbytes, table.nbytes
     c._struct = _CacheStruct(0, 0, pool.shape[0], table.shape[0], table.shape[1], int(kv_heads),
                              int(dim), int(page), int(group))
     c._ref = ctypes.addressof(c._struct)

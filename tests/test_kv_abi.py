@@ -257,3 +257,28 @@ def test_host_tensors_are_refused():
     for call in (_do_append, _do_read, _do_attend):
         with pytest.raises(ValueError, match="on the GPU"):
             call()
+
+
+def test_binding_refuses_a_cache_that_lies_otherwise(library):
+    """Tensors given other memory: fewer bytes in as many values, values that are one and the same,
+    rows and columns exchanged in place."""
+    def data(name, other):
+        def change(c):
+            getattr(c, name).data = other
+        return change
+
+    size = ok.page_bytes(2, 64, 16, 32)
+    for change, why in (
+            (data("table", torch.zeros(3, 2, dtype=torch.int16)), "size"),
+            (data("table", torch.zeros(1, 1, dtype=torch.int32).expand(3, 2)), "contiguous"),
+            (data("pool", torch.zeros(1, 1, dtype=torch.uint8).expand(6, size)), "contiguous"),
+            (lambda c: c.table.t_(), "contiguous"), (lambda c: c.pool.t_(), "contiguous")):
+        c = _host_cache()
+        change(c)
+        with pytest.raises(ValueError, match=why):
+            _do_append(cache=c)
+        with pytest.raises(ValueError, match=why):
+            lvq.kv_read(c, _ints(5), torch.zeros(5, 128), None, seq=_ints(5))
+        with pytest.raises(ValueError, match=why):
+            lvq.attend(c, torch.zeros(6, 256).half(), _ints(3), torch.zeros(6, 256), None, queries=2)
+    assert not library.calls
