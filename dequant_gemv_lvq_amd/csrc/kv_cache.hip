@@ -505,7 +505,9 @@ extern "C" int lvq_kv_append(const lvq_kv_cache* cache, const void* k, int64_t k
     return LVQ_E_SHAPE;
   if (!seq && tokens > cache->seqs) return LVQ_E_SHAPE;
   if (tokens == 0) return LVQ_OK;
-  if (!k || !v || !pos || (rot && (!cos || !sin)) || (heads && (!q || !q_out))) return LVQ_E_NULL;
+  // an empty table of angles may have no address: every position is past it
+  if (!k || !v || !pos || (rot && positions && (!cos || !sin)) || (heads && (!q || !q_out)))
+    return LVQ_E_NULL;
   const size_t tb = kv_type_bytes(type);
   if ((uintptr_t)k % tb || (uintptr_t)v % tb || (heads && (uintptr_t)q % tb) ||
       (uintptr_t)seq % 4 || (uintptr_t)pos % 4 || !aligned16(cos) || !aligned16(sin) ||

@@ -541,7 +541,7 @@ size_t lvq_kv_page_bytes(int kv_heads, int dim, int page, int group);
  *              and v_stride values from one row's start to the next's (< 2^31)
  *   seq, pos   device, int32 [tokens]
  *   cos, sin   device, fp32 [positions][rot/2]; rot a multiple of 16, at most dim, 0 for
- *              no rotation (then NULL will do)
+ *              no rotation (NULL will do where rot or positions is 0)
  *   q, q_out   heads (0..1024; 0 for none) heads of dim channels per token: rows of `type`,
  *              q_stride apart, and fp16, bf16 or fp32 (q_out_type) [tokens][heads * dim]
  * A token whose sequence, position (negative, past the table of pages, or past `positions`

@@ -330,3 +330,14 @@ def test_other_stream_and_graph():
         assert np.array_equal(st.pool(), st.want.pool)
         want = ok.rotate(hosts[0].reshape(n, 8, 128), c, z, 128, False).astype(np.float16)
         assert np.array_equal(q_out.cpu().numpy().reshape(n, 8, 128), want)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_an_empty_table_of_angles(interleaved):
+    """Every position is past it: all tokens are left out."""
+    st = Setup(2, 64, 16, 32, 1, 3)
+    x, q = torch.randn(20, 128, device=DEV), torch.randn(20, 256, device=DEV)
+    none, q_out = torch.empty(0, 32, device=DEV), torch.full((20, 256), 77.0, device=DEV)
+    lvq.kv_append(st.cache, x, x, _ints(range(20)), seq=_ints([0] * 20), cos=none, sin=none,
+                  interleaved=interleaved, q=q, q_out=q_out)
+    assert np.array_equal(st.pool(), st.want.pool) and (q_out == 77).all()

@@ -282,3 +282,9 @@ def test_binding_refuses_a_cache_that_lies_otherwise(library):
         with pytest.raises(ValueError, match=why):
             lvq.attend(c, torch.zeros(6, 256).half(), _ints(3), torch.zeros(6, 256), None, queries=2)
     assert not library.calls
+
+
+def test_append_with_an_empty_table_of_angles():
+    """No position is inside it, so no address is asked for (the later check answers)."""
+    assert _append(positions=0, cos=None, sin=None, k=K + 1) == E.LVQ_E_ALIGN
+    assert _append(positions=1, cos=None, k=K + 1) == E.LVQ_E_NULL
