@@ -250,3 +250,82 @@ def test_small_activations_value_by_value(hidden, inner, experts, top, group, to
         if om.choose(x.double().cpu().numpy(), m.router.double().numpy(), top, True)[3] > 1:
             break
     m.check(x)
+
+
+@pytest.mark.parametrize("hidden,inner,experts,top,group,zeros,tokens", [
+    (2048, 768, 64, 8, 128, False, 1), (2048, 768, 64, 8, 128, True, 16), (1001, 331, 13, 3, 32, True, 3),
+    (4096, 1024, 9, 2, 64, True, 4), (512, 2500, 4, 2, 0, False, 7), (100, 4100, 5, 2, 256, True, 2)])
+def test_error_in_the_whole(hidden, inner, experts, top, group, zeros, tokens):
+    """The norm of the error over the norm of the result, where a bound on every value is too wide
+    to see a lost unit.  A product of n columns passes through roundings of 2^-24 of its partial sums
+    at each of them at most, independent: n^1/2 2^-24, 2^-18 for 4096; three products, of which two
+    meet in the activation, and their terms some times the result (codes and zeros apart): 2^-16.
+    The loss of 32 columns of inner is (32 / inner)^1/2, a thousand times as much."""
+    m = Layer(hidden, inner, experts, top, group, zeros)
+    x = m.x(tokens)
+    y = m.run(x)[0].double().cpu().numpy()
+    xh = x.double().cpu().numpy()
+    ids, w, dw, gap = om.choose(xh, m.router.double().numpy(), top, True)
+    assert gap > 1
+    want, _ = om.layer(xh, ids, w, dw, m.gu.expert, m.down.expert)
+    for t in range(tokens):
+        assert np.linalg.norm(y[t] - want[t]) <= 2.0 ** -16 * np.linalg.norm(want[t]), t
+
+
+@pytest.mark.parametrize("group", [0, 32])
+def test_experts_past_4_gib(group):
+    """The last of 140 experts of 67 and 34 MB of codes holds what the only one of another layer
+    does, and gives the same bits."""
+    hidden = inner = 8192
+    near = Layer(hidden, inner, 1, 1, group, True)
+    x = near.x(1).expand(2, -1).contiguous()
+    x[1] *= 0.5
+    near.router[:] = x[:1].cpu().sign()
+    near.args = (near.router.to(DEV),) + near.args[1:]
+    want = near.run(x)[0]
+    far = []
+    for of in near.args[1:3]:
+        made = []
+        for t in of[:3]:
+            big = torch.empty((140,) + t.shape[1:], dtype=t.dtype, device=DEV)
+            big[139].copy_(t[0])
+            made.append(big)
+        assert made[0].numel() > 1 << 32
+        far.append(tuple(made) + (group,))
+    router = torch.zeros(140, hidden, dtype=torch.float16, device=DEV)
+    router[139] = near.args[0][0]
+    y = torch.full((2, hidden), float("nan"), device=DEV)
+    ids = torch.full((2, 1), -9, device=DEV, dtype=torch.int32)
+    space = torch.empty(lvq.q4_moe_workspace_bytes(2, hidden, inner, 140, 1), dtype=torch.uint8,
+                        device=DEV)
+    lvq.q4_moe(x, router, *far, inner, 1, y, space, ids=ids)
+    assert ids.tolist() == [[139], [139]]
+    assert torch.equal(y, want) and want.isfinite().all()
+
+
+@pytest.mark.parametrize("most,fits", [(6e4, True), (7e4, False)])
+def test_activations_past_fp16(most, fits):
+    """Up to 65504 an activation is kept as any other; past it its token is NaN, as an infinity in x
+    makes it, and the other tokens of the expert are what they are."""
+    m = Layer(64, 33, 1, 1, 32, True)
+    x = m.x(3)
+    x[[0, 2]] *= 0.125
+
+    def activations():
+        g, u = np.split(x.double().cpu().numpy() @ m.gu.expert(0)[0].T, 2, axis=1)
+        return np.abs(g / (1 + np.exp(-g)) * u).max(1)
+
+    m.gu.scale[0, 33:] = (m.gu.scale[0, 33:].astype(np.float64) * (most / activations()[1])).astype(
+        np.float16)
+    m.args = (m.args[0], m.gu.dev()) + m.args[2:]
+    a = activations()
+    assert (a[[0, 2]] < 6e4).all() and (a[1] < 65504) == fits and np.isfinite(m.gu.scale).all()
+    if fits:
+        m.check(x)
+        return
+    y = m.run(x)[0].double().cpu().numpy()
+    xh = x.double().cpu().numpy()
+    want, tol = om.layer(xh, *om.choose(xh, m.router.double().numpy(), 1, True)[:3], m.gu.expert,
+                         m.down.expert)
+    assert np.isnan(y[1]).all()
+    assert (np.abs(y - want) <= tol)[[0, 2]].all()
