@@ -568,6 +568,8 @@ int lvq_kv_read(const lvq_kv_cache* cache, const int32_t* seq, const int32_t* po
  * `window` of them), k and v those of key/value head h / (heads / kv_heads).
  *   q          fp16 or bf16 (q_type), rows of heads * dim values, q_stride apart, row
  *              s * queries + i for query i of sequence s
+ *              (bf16: a head's values times a power of two are taken as fp16, so those below
+ *              2^-17 of its largest are off by up to 2^-25 of it)
  *   heads      a multiple of kv_heads, at most 1024; queries 1..LVQ_MAX_QUERIES
  *   lens       device, int32 [seqs]: tokens of each sequence, the queries' own included
  *              (a length past the table counts as the table's end, a negative one as 0)
