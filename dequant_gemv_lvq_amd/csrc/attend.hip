@@ -791,7 +791,10 @@ extern "C" int lvq_attend(const lvq_kv_cache* cache, const void* q, int q_type, 
   a.tiles = (uint16_t)att_tiles(a.c, heads, queries);
   const Split split = att_split(a.c, queries, window, a.tiles);
   a.splits = split.parts, a.waves = (uint8_t)split.waves;
-  // in order where a workgroup may have long to run: it costs a trip to memory
+  // in order where a workgroup may have long to run, 32 blocks or more: it costs a trip to memory (as
+  // they come and in order, sequences of up to so many tokens, 8 heads of 128.  64, one part each:
+  // 1024 14.9, 15.8 us; 2048 22.7, 20.9; 8192 69, 56.  Below 32 blocks mixed: 16, four parts, 4096
+  // 17.9, 16.9; 64 of 2 heads, four parts, 2048 13.3, 16.4, 8192 26.1, 24.4)
   const int per_seq = a.c.kv_heads * a.tiles * a.splits;
   const bool ordered = a.c.seqs > 1 && a.c.seqs <= kWave &&
                        att_blocks(a.c, queries, window) >= 32LL * a.splits;

@@ -358,8 +358,11 @@ struct ReadArgs {
 };
 
 // H: heads of a workgroup.  It waits for positions, then pages, then the cache: where tokens are
-// many, four heads' loads are on their way at once (8192 tokens, 8 heads: 15.4 us, 18 with one);
-// where few, one, so that more workgroups share the work.
+// many, four heads' loads are on their way at once; where few, one, so that more workgroups share
+// the work.  us in a graph with one and with four, 8 heads of 128 channels: 1024 tokens 4.7, 7.0;
+// 2048 6.3, 7.7; 4096, where the rule changes, 9.9, 9.5; 8192 17.3, 14.8; 16384 29.6, 23.9.  8 heads
+// of 64: 4096 8.1, 8.0; 8192 13.0, 10.0.  2 heads of 256: 8192 12.2, 12.3; 16384, where it changes
+// there, 22.4, 21.0.
 constexpr int kReadHeads = 4;
 inline int heads_at_once(const KvPages& c, long long tiles) {
   return tiles * c.kv_heads >= 8LL * device_cus() ? kReadHeads : 1;
