@@ -749,7 +749,7 @@ class KvCache:
     """A key/value cache in 4 bits as kv_append(), kv_read() and attend() take it: the
     pool of pages and the table of pages per sequence, both the caller's tensors."""
 
-    __slots__ = ("_pool", "_table", "_struct", "_ref", "_sizes")
+    __slots__ = ("_pool", "_table", "_struct", "_ref", "_pool_bytes", "_table_bytes", "_at")
 
     @property
     def pool(self):
@@ -761,18 +761,26 @@ class KvCache:
 
     def _here(self, dev):
         """Address of the description; its tensors are looked at anew in every call, as they
-        may have been moved or resized in place."""
+        may have been moved, resized or given other memory in place."""
+        pool, table = self._pool, self._table
+        if (pool.get_device() != dev or table.get_device() != dev
+                or pool.nbytes != self._pool_bytes or table.nbytes != self._table_bytes
+                or not pool.is_contiguous() or not table.is_contiguous()):
+            self._changed(dev)
+        at = pool.data_ptr(), table.data_ptr()
+        if at != self._at:
+            self._struct.pool, self._struct.table = self._at = at
+        return self._ref
+
+    def _changed(self, dev):
         s, pool, table = self._struct, self._pool, self._table
         if pool.get_device() != dev:
             _refuse(pool, "pool", _types("uint8"), s.pages, 0, dev)
         if table.get_device() != dev:
             _refuse(table, "table", _types("int32"), s.seqs, s.max_pages, dev)
-        if (pool.nbytes, table.nbytes) != self._sizes:
+        if pool.nbytes != self._pool_bytes or table.nbytes != self._table_bytes:
             raise ValueError("the cache's pool or table has changed its size")
-        if not (pool.is_contiguous() and table.is_contiguous()):
-            raise ValueError("the cache's pool or table is no longer contiguous")
-        s.pool, s.table = pool.data_ptr(), table.data_ptr()
-        return self._ref
+        raise ValueError("the cache's pool or table is no longer contiguous")
 
 
 def kv_page_bytes(kv_heads: int, dim: int, page: int, group: int = 0) -> int:
@@ -802,7 +810,7 @@ def kv_cache(pool, table, kv_heads: int, dim: int, page: int, group: int = 0) ->
     _in_32_bits(pool.shape[0], table.shape[0], table.shape[1])
     c = KvCache()
     c._pool, c._table = pool, table
-    c._sizes = pool.nbytes, table.nbytes
+    c._pool_bytes, c._table_bytes, c._at = pool.nbytes, table.nbytes, (0, 0)
     c._struct = _CacheStruct(0, 0, pool.shape[0], table.shape[0], table.shape[1], int(kv_heads),
                              int(dim), int(page), int(group))
     c._ref = ctypes.addressof(c._struct)
@@ -900,7 +908,7 @@ def attend_workspace_bytes(cache: KvCache, heads: int, queries: int = 1) -> int:
     s = cache._struct
     if heads < 1 or heads % s.kv_heads or not 1 <= queries <= MAX_QUERIES:
         _check(LVQ_E_SHAPE)
-    s.pool, s.table = cache.pool.data_ptr(), cache.table.data_ptr()
+    s.pool, s.table = cache._at = cache.pool.data_ptr(), cache.table.data_ptr()
     return int(_lib.lvq_attend_workspace(cache._ref, heads, queries))
 
 
