@@ -27,9 +27,9 @@
 // What bounds it, and what it measured (GPU, one call): long sequences, the read of the cache
 // with 4 rows or less (64 sequences of 4096 tokens, 8 key/value heads of 128: 57 us, 5.0 TB/s;
 // each further token 5.9 TB/s), with 16 rows the vector instructions that unpack the codes and
-// make the weights (131072 tokens in groups of 32, 168 MB: 45 us with 5 of the join). Short
-// ones, the length of the code that a wave runs through once: 1001 tokens of 128 channels
-// 6.2 us and 3.5 of the join, 490 tokens 7.7 in one launch (6.0 of 64 channels, 11.4 of 256).
+// make the weights (131072 tokens in groups of 32, 168 MB: 44.6 us in a trace and 4.7 of the join,
+// 46 a call). Short ones, the length of the code that a wave runs through once: 1001 tokens of 128
+// channels 6.2 us and 3.6 of the join, 490 tokens 7.7 in one launch (6.0 of 64 channels, 11.4 of 256).
 
 #include "kv_cache.h"
 

@@ -16,12 +16,12 @@
 // value and the rest times 2^11 (22 bits), which the down product multiplies side by side.
 //
 // What bounds it, and what it measured (GPU, one call; 128 experts of 2048 x 768, 8 chosen):
-// one token, the three launches and in each a few trips to memory (router 3.0 us, gate and up
-// 8.2 for 13 MB, of which about 2 for the choice, down 4.1 for 7 MB); sixteen tokens, the
-// read of the weights and, in the down product, the instructions around it (4.6 us; 32.7 for
-// 128 MB, 3.9 TB/s; 26.0 for 78 MB with the activations, 3.0 TB/s); four tokens through 8
-// experts of 4096 x 12288 with zeros, 2 chosen, the read (5.8; 57 for 284 MB, 5.0 TB/s; 43
-// for 145 MB, 3.4).
+// one token, the three launches and in each a few trips to memory (in a trace, router 3.0 us, gate
+// and up 8.5 for 13 MB, of which about 2 for the choice, down 4.5 for 7 MB); sixteen tokens, the
+// read of the weights and, in the down product, the instructions around it (4.6 us; 32.9 for
+// 128 MB, 3.9 TB/s; 26.6 for 78 MB with the activations, 2.9 TB/s); four tokens through 8
+// experts of 4096 x 12288 with zeros, 2 chosen, the read (5.9; 57 for 284 MB, 5.0 TB/s; 44
+// for 145 MB, 3.3).
 
 #include "q4_dev.h"
 
