@@ -4,7 +4,7 @@
 //   y = sum_e w_e D_e (silu(G_e x) * (U_e x))
 //
 // Three launches, each needing all of the one before: the router's logits (a workgroup per
-// expert), the choice and the chosen experts' gate and up products with the activation,
+// expert and four tokens), the choice and the chosen experts' gate and up products with the activation,
 // the down products with the weighted sum.  The choice is a few hundred operations, so
 // every workgroup of the second launch makes it for itself.
 //
@@ -16,11 +16,11 @@
 // value and the rest times 2^11 (22 bits), which the down product multiplies side by side.
 //
 // What bounds it, and what it measured (GPU, one call; 128 experts of 2048 x 768, 8 chosen):
-// one token, the three launches and in each a few trips to memory (in a trace, router 3.0 us, gate
-// and up 8.5 for 13 MB, of which about 2 for the choice, down 4.5 for 7 MB); sixteen tokens, the
-// read of the weights and, in the down product, the instructions around it (4.6 us; 32.9 for
-// 128 MB, 3.9 TB/s; 26.6 for 78 MB with the activations, 2.9 TB/s); four tokens through 8
-// experts of 4096 x 12288 with zeros, 2 chosen, the read (5.9; 57 for 284 MB, 5.0 TB/s; 44
+// one token, the three launches and in each a few trips to memory (in a trace, router 2.9 us, gate
+// and up 8.4 for 13 MB, of which about 2 for the choice, down 4.5 for 7 MB); sixteen tokens, the
+// read of the weights and, in the down product, the instructions around it (4.7 us; 33 for
+// 128 MB, 3.9 TB/s; 27 for 78 MB with the activations, 2.9 TB/s); four tokens through 8
+// experts of 4096 x 12288 with zeros, 2 chosen, the read (4.7; 57 for 284 MB, 5.0 TB/s; 44
 // for 145 MB, 3.3).
 
 #include "q4_dev.h"
@@ -39,69 +39,100 @@ constexpr int kMaxExperts = 512;
 struct RouterArgs {
   const uint16_t* x;
   const void* router;
-  float* logits;
+  float* logits;  // [tokens][experts], then as many rests
   int tokens, hidden, experts;
   int type;
 };
 
-__device__ __forceinline__ float router_value(const void* p, int type, size_t i) {
-  if (type == LVQ_F32) return ((const float*)p)[i];
-  const uint32_t b = ((const uint16_t*)p)[i];
-  return type == LVQ_F16 ? f16_to_f32(b) : __builtin_bit_cast(float, b << 16);
+// Sum over the 64 lanes of a wave, valid in lane 63, as wave_sum_lane63 adds them.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_add64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, CTRL, ROW_MASK, 0xF, false);
+  const uint32_t hi =
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROW_MASK, 0xF, false);
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum64_lane63(double v) {
+  v = dpp_add64<0xB1, 0xF>(v);
+  v = dpp_add64<0x4E, 0xF>(v);
+  v = dpp_add64<0x141, 0xF>(v);
+  v = dpp_add64<0x140, 0xF>(v);
+  v = dpp_add64<0x142, 0xA>(v);
+  return dpp_add64<0x143, 0xC>(v);
 }
 
-// A workgroup: one expert, four tokens.
-__global__ void __launch_bounds__(256) moe_router_kernel(RouterArgs a) {
-  __shared__ float red[4][4];
-  const int e = blockIdx.x, t0 = blockIdx.y * 4;
-  const int n = a.tokens - t0 < 4 ? a.tokens - t0 : 4;
+// A workgroup: one expert, N tokens, a thread for eight columns (up to kRouterWaves of them, then
+// in rounds), so that one trip to memory serves all.  The choice is between logits as close as they
+// come, so they are summed in 64 bits (every product is exact there) and left as two floats, the
+// rounded value and the rest.  In fp32, experts nearer than 2^-20 or so were chosen by the roundings;
+// the sums cost 0.1 us of one token's layer of 15.
+constexpr int kRouterWaves = 16;
+
+template <int N>
+__global__ void __launch_bounds__(kRouterWaves* kWave) moe_router_kernel(RouterArgs a) {
+  __shared__ double red[kRouterWaves][N];
+  const int e = blockIdx.x, t0 = blockIdx.y * N;
+  const int n = a.tokens - t0 < N ? a.tokens - t0 : N;
   const size_t row = (size_t)e * a.hidden;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int c = threadIdx.x * 8; c < a.hidden; c += 256 * 8) {
-    float w[8];
-    const bool whole = c + 8 <= a.hidden;
-    if (whole && a.type == LVQ_F32) {
-      __builtin_memcpy(w, (const float*)a.router + row + c, 32);
-    } else if (whole) {
-      uint32_t r[4];
-      __builtin_memcpy(r, (const uint16_t*)a.router + row + c, 16);
+  double acc[N];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t b = (r[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
-        w[i] = a.type == LVQ_F16 ? f16_to_f32(b) : __builtin_bit_cast(float, b << 16);
-      }
+  for (int k = 0; k < N; ++k) acc[k] = 0;
+  for (int c = threadIdx.x * 8; c < a.hidden; c += blockDim.x * 8) {
+    uint32_t r[8], x[N][4];
+    // tokens past the last: the last again, not stored
+    auto x_row = [&](int k) { return a.x + (size_t)(t0 + (k < n ? k : n - 1)) * a.hidden + c; };
+    if (c + 8 <= a.hidden) {
+      if (a.type == LVQ_F32) __builtin_memcpy(r, (const float*)a.router + row + c, 32);
+      else __builtin_memcpy(r, (const uint16_t*)a.router + row + c, 16);
+#pragma unroll
+      for (int k = 0; k < N; ++k) __builtin_memcpy(x[k], x_row(k), 16);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[i] = c + i < a.hidden ? router_value(a.router, a.type, row + c + i) : 0.f;
-    }
+      for (int i = 0; i < 8; ++i) {
+        r[i] = 0;
+        if (i < 4)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k >= n) break;
-      const uint16_t* xr = a.x + (size_t)(t0 + k) * a.hidden + c;
-      uint32_t r[4] = {0, 0, 0, 0};
-      if (whole) {
-        __builtin_memcpy(r, xr, 16);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c + i < a.hidden) r[i >> 1] |= (uint32_t)xr[i] << (16 * (i & 1));
+          for (int k = 0; k < N; ++k) x[k][i] = 0;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (whole || c + i < a.hidden)
-          acc[k] = __builtin_fmaf(w[i], f16_to_f32((r[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), acc[k]);
+      for (int i = 0; i < 7; ++i) {
+        if (c + i >= a.hidden) break;
+        if (a.type == LVQ_F32) r[i] = ((const uint32_t*)a.router)[row + c + i];
+        else r[i >> 1] |= (uint32_t)((const uint16_t*)a.router)[row + c + i] << (16 * (i & 1));
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[k][i >> 1] |= (uint32_t)x_row(k)[i] << (16 * (i & 1));
+      }
     }
+    double w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t b = (r[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+      const float v = a.type == LVQ_F32   ? __builtin_bit_cast(float, r[i])
+                      : a.type == LVQ_F16 ? f16_to_f32(b)
+                                          : __builtin_bit_cast(float, b << 16);
+      w[i] = (double)v;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        acc[k] = __builtin_fma(w[i], (double)f16_to_f32((x[k][i >> 1] >> (16 * (i & 1))) & 0xFFFFu),
+                               acc[k]);
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float s = wave_sum_lane63(acc[k]);
+  for (int k = 0; k < N; ++k) {
+    const double s = wave_sum64_lane63(acc[k]);
     if ((threadIdx.x & 63) == 63) red[threadIdx.x >> 6][k] = s;
   }
   __syncthreads();
   if ((int)threadIdx.x < n) {
     const int k = threadIdx.x;
-    a.logits[(size_t)(t0 + k) * a.experts + e] = (red[0][k] + red[1][k]) + (red[2][k] + red[3][k]);
+    double l = red[0][k];
+    for (int w = 1; w < (int)blockDim.x / kWave; ++w) l += red[w][k];
+    float* to = a.logits + (size_t)(t0 + k) * a.experts + e;
+    *to = (float)l;
+    to[(size_t)a.tokens * a.experts] = (float)(l - (double)(float)l);
   }
 }
 
@@ -123,13 +154,19 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
   return q[0] > q[1] ? q[0] : q[1];
 }
 
+// Integers of the floats' order, above 1 for all but NaN.
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  return (b >> 31) ? ~b : b | 0x80000000u;
+}
+
 // The top of a token's logits, by a wave: expert j goes to lane j's *id and *weight.
-// Values are compared as integers of the same order; equal ones go by their index.  A NaN
-// is below everything, and makes the token's weights NaN.
+// Values are compared as integers of the same order, equal ones by their rests and then by their
+// index.  A NaN is below everything, and makes the token's weights NaN.
 // S: values per lane.
 template <int S>
-__device__ __forceinline__ void choose(const float* logits, int experts, int top, bool renormalize,
-                                       int lane, int* id, float* weight) {
+__device__ __forceinline__ void choose(const float* logits, const float* rests, int experts, int top,
+                                       bool renormalize, int lane, int* id, float* weight) {
   float v[S];
   uint32_t key[S];
   bool nan = false;
@@ -137,8 +174,7 @@ __device__ __forceinline__ void choose(const float* logits, int experts, int top
   for (int s = 0; s < S; ++s) {
     const int e = s * kWave + lane;
     v[s] = e < experts ? logits[e] + 0.f : -__builtin_inff();  // + 0: no negative zero
-    const uint32_t b = __builtin_bit_cast(uint32_t, v[s]);
-    key[s] = e >= experts ? 0u : v[s] != v[s] ? 1u : (b >> 31) ? ~b : b | 0x80000000u;
+    key[s] = e >= experts ? 0u : v[s] != v[s] ? 1u : order_of(v[s]);
     nan |= v[s] != v[s];
   }
   nan = __any(nan);
@@ -149,11 +185,31 @@ __device__ __forceinline__ void choose(const float* logits, int experts, int top
 #pragma unroll
     for (int s = 1; s < S; ++s) m = m > key[s] ? m : key[s];
     m = wave_umax(m);
-    int e = 0;
+    int e = 0, equal = 0;
 #pragma unroll
     for (int s = S - 1; s >= 0; --s) {
       const uint64_t who = __ballot(key[s] == m);
       if (who) e = s * kWave + __builtin_ctzll(who);
+      equal += __builtin_popcountll(who);
+    }
+    if (equal > 1) {
+      // the rest of an infinity or a NaN is none
+      uint32_t rest[S], most = 0;
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        rest[s] = 0;
+        if (key[s] == m) {
+          const float r = rests[s * kWave + lane] + 0.f;
+          rest[s] = order_of(r == r ? r : 0.f);
+        }
+        most = most > rest[s] ? most : rest[s];
+      }
+      most = wave_umax(most);
+#pragma unroll
+      for (int s = S - 1; s >= 0; --s) {
+        const uint64_t who = __ballot(key[s] == m && rest[s] == most);
+        if (who) e = s * kWave + __builtin_ctzll(who);
+      }
     }
 #pragma unroll
     for (int s = 0; s < S; ++s)
@@ -313,11 +369,12 @@ __global__ void __launch_bounds__(kGateWaves* kWave) moe_gate_kernel(GateArgs a)
   const bool chooses = wv < a.tokens;
   if (chooses) {
     const float* l = a.logits + (size_t)wv * a.experts;
+    const float* rests = l + (size_t)a.tokens * a.experts;
     // two values per lane where they hold all: eight cost 1.2 us more of the layer's (one token of
     // 2048 x 768, 8 chosen of 16, 64, 128: 14.6, 14.8, 15.0 us with two, 15.9, 16.0, 16.3 with
     // eight; of 256 and 512, with eight, 16.4 and 17.3)
-    if (a.experts <= 2 * kWave) choose<2>(l, a.experts, a.top, a.renormalize, lane, &id, &weight);
-    else choose<kMaxExperts / kWave>(l, a.experts, a.top, a.renormalize, lane, &id, &weight);
+    if (a.experts <= 2 * kWave) choose<2>(l, rests, a.experts, a.top, a.renormalize, lane, &id, &weight);
+    else choose<kMaxExperts / kWave>(l, rests, a.experts, a.top, a.renormalize, lane, &id, &weight);
   }
 
   // 2. x into LDS, and minus the sums of its units, as the products start from them
@@ -775,7 +832,7 @@ inline MoeSpace moe_space(int tokens, int inner, int experts, int top) {
   MoeSpace s;
   const size_t pairs = (size_t)tokens * top;
   s.logits = 0;
-  s.jobs = up((size_t)tokens * experts * 4);
+  s.jobs = up((size_t)tokens * experts * 8);
   s.act = s.jobs + up(sizeof(JobList));
   s.all = s.act + up(pairs * act_pitch(inner) * 4);
   return s;
@@ -873,7 +930,10 @@ extern "C" int q4_moe(const uint16_t* x, int tokens, int hidden, const void* rou
   hipStream_t st = (hipStream_t)stream;
   RouterArgs r = {x, router, (float*)(w + sp.logits), tokens, hidden, experts, router_type};
   clear_hip_error();
-  hipLaunchKernelGGL(moe_router_kernel, dim3(experts, (tokens + 3) / 4), dim3(256), 0, st, r);
+  const int columns = (hidden + 8 * kWave - 1) / (8 * kWave);  // in waves
+  const dim3 threads((columns < kRouterWaves ? columns : kRouterWaves) * kWave);
+  if (tokens == 1) hipLaunchKernelGGL(moe_router_kernel<1>, dim3(experts), threads, 0, st, r);
+  else hipLaunchKernelGGL(moe_router_kernel<4>, dim3(experts, (tokens + 3) / 4), threads, 0, st, r);
   int e = launch_status();
   if (e) return e;
   GateArgs g;

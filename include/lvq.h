@@ -428,9 +428,11 @@ int q4_gemv_q8(const uint8_t* codes, const uint16_t* scale, const uint16_t* zero
  *   ids_out, weights_out  int32 and fp32 [tokens][top], largest first; either may be NULL
  *   workspace    device, q4_moe_workspace bytes, its content of no account before and after;
  *                calls that may run at the same time need one each
- * Logits, sums and weights are fp32; an activation is kept as two fp16, the rounded value
- * and the rest (22 bits), so one past 65504 makes its token's y NaN (lvq_silu_mul's fp16 output is
- * infinite there, and q4_gemv's y of it NaN), and one below 2^-14 is off by 2^-36.  A NaN among a token's logits makes its weights NaN.  An
+ * Logits are summed in fp64 and compared as two fp32, the rounded value and the rest; sums
+ * and weights are fp32, the weights from the rounded logits.  An activation is kept as two
+ * fp16, the rounded value and the rest (22 bits), so one past 65504 makes its token's y NaN
+ * (lvq_silu_mul's fp16 output is infinite there, and q4_gemv's y of it NaN), and one below
+ * 2^-14 is off by 2^-36.  A NaN among a token's logits makes its weights NaN.  An
  * infinity in x gives NaN in its token.  Tokens do not affect each other's values, and the
  * result is the same from run to run; the order of its sums depends on the sizes, the
  * device and, for the sum over the experts, on which are chosen by the tokens together.

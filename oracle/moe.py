@@ -2,12 +2,12 @@
 (oracle; test infrastructure).
 
 Bounds, u = 2^-24 a nearest rounding to fp32, STEP32 = 2^-23 any fp32 operation:
-  logits      exact products, a chain of at most hidden / 256 + 8 additions per thread and
-              10 to join: n STEP32 sum |r x|
-  weights     p = exp(l - max) / sum: the difference's error is twice the largest bound of a
-              logit, the exponential and its argument's rounding (|l - max| + 2) STEP32, the sum
-              over at most 512 experts (in 8 + 6 additions) and the division 16 STEP32.  Below
-              2^-126 fp32 numbers are 2^-149 apart: the exponential's and the division's
+  logits      exact products, summed in float64 here and there: each off by at most hidden
+              2^-53 sum |r x|; compared as two fp32, 2^-47 of the logit
+  weights     p = exp(l - max) / sum of logits rounded to fp32, 2^-24 |l| more: the difference's
+              error is twice the largest bound of a logit, the exponential and its argument's
+              rounding (|l - max| + 2) STEP32, the sum over at most 512 experts (in 8 + 6
+              additions) and the division 16 STEP32.  Below 2^-126 fp32 numbers are 2^-149 apart: the exponential's and the division's
               roundings are off by half of that each (the sum is 1 at least), whatever the size
   gate, up    as oracle.q4.gemv
   activation  silu(g) u: |silu'| < 1.1, so 1.1 |u| dg + |silu(g)| du + dg du, and the activation's
@@ -29,13 +29,14 @@ def choose(x, router, top: int, renormalize: bool) -> tuple:
     """(ids, w, dw, gap): chosen experts, their weights and the bound of those, and by how
     much the last chosen logit is above the first that is not, in bounds (inf if none is left)."""
     l = x @ router.T
-    big = (x.shape[1] / 256 + 18) * STEP32 * (np.abs(x) @ np.abs(router).T)
+    big = (2 * x.shape[1] * 2.0 ** -53 + 2.0 ** -47) * (np.abs(x) @ np.abs(router).T)
+    near = big + U * np.abs(l)
     ids = np.argsort(-l, axis=1, kind="stable")[:, :top]
     p = np.exp(l - l.max(1, keepdims=True))
     chosen = np.take_along_axis(p, ids, 1)
     w = chosen / (chosen.sum(1, keepdims=True) if renormalize else p.sum(1, keepdims=True))
     spread = l.max(1, keepdims=True) - np.take_along_axis(l, ids, 1)
-    dw = w * (4 * big.max(1, keepdims=True) + (2 * spread + 2 + 2 + 16) * STEP32) + 2.0 ** -149
+    dw = w * (4 * near.max(1, keepdims=True) + (2 * spread + 2 + 2 + 16) * STEP32) + 2.0 ** -149
     rest = np.sort(l, axis=1)[:, ::-1]
     gap = np.inf
     for j in range(min(top, l.shape[1] - 1)):

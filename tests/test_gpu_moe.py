@@ -329,3 +329,28 @@ def test_activations_past_fp16(most, fits):
                          m.down.expert)
     assert np.isnan(y[1]).all()
     assert (np.abs(y - want) <= tol)[[0, 2]].all()
+
+
+@pytest.mark.parametrize("experts,top,tokens", [(40, 8, 1), (128, 16, 5), (200, 8, 16), (512, 16, 3)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_logits_closer_than_fp32(experts, top, tokens, sign):
+    """Logits 2^-40 apart beside a common part of 1 to 60, some of them equal: the order is that of
+    the exact sums (whole multiples of 2^-40, so float64 has them exactly), not of fp32's."""
+    m = Layer(72, 32, experts, top, 32, False, router="f32")
+    r = np.random.default_rng(12)
+    common = sign * r.integers(1, 16, 72) / 16
+    rows = np.tile(common, (experts, 1))
+    rows[:, 5] = r.integers(-3 * experts, 3 * experts, experts) * 2.0 ** -40
+    rows[r.permutation(experts)[:experts // 4], 5] = 0
+    m.router = torch.from_numpy(rows).float()
+    assert torch.equal(m.router.double(), torch.from_numpy(rows))
+    m.args = (m.router.to(DEV),) + m.args[1:]
+    x = torch.from_numpy(r.integers(1, 9, (tokens, 72)) / 8).half()
+    x[:, 5] = 1
+    exact = x.double().numpy() @ rows.T
+    want = np.argsort(-exact, axis=1, kind="stable")[:, :top]
+    assert (np.argsort(-exact.astype(np.float32), axis=1, kind="stable")[:, :top] != want).any()
+    ids, w = m.run(x.to(DEV))[1:]
+    assert np.array_equal(ids.cpu().numpy(), want)
+    # the weights differ by less than their roundings
+    assert (w.double() - 1 / top).abs().max() <= 8 * 2.0 ** -24 / top
